@@ -12,6 +12,13 @@ argument layouts, ownership and error behaviour:
   iris_mm_ar_local    C = A @ B + bias; out = C + sum(partials)
   iris_concurrent     C = A @ B + bias beside an independent all_reduce of W buffers
 
+and, in block-scaled 8-bit floating point (Fp8: codes, scales):
+
+  iris_fp8_quantize    a matrix to 8 bits, along its rows and / or transposed
+  iris_fp8_mm          C = A @ B^T + bias
+  iris_fp8_swiglu      h = silu(gate) * up, gate and up kept in 8 bits if wanted
+  iris_fp8_swiglu_bwd  its backward pass from the kept gate and up
+
 There is no fallback: if the library is missing or fails to load, importing
 this package raises.
 """
@@ -34,6 +41,7 @@ IRIS_MODE_TWO_STREAM = 2
 IRIS_FLAG_NO_STEAL = 1
 IRIS_FLAG_BIAS_ALONG_M = 2
 IRIS_FLAG_NO_LOCKSTEP = 4
+IRIS_FLAG_ACCUMULATE = 8
 IRIS_OP_AG_MM = 1
 IRIS_OP_MM_RS = 2
 IRIS_OP_MM_AR = 3
@@ -92,6 +100,11 @@ class _OpArgs(ctypes.Structure):
     ]
 
 
+class _Fp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("ld_scales", ctypes.c_int64), ("block", ctypes.c_int32)]
+
+
 class _PredictParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in (
         "gemm_tflops_per_cu", "tile_overhead_us", "comm_gbps_per_cu", "comm_gbps_chip", "unit_overhead_us",
@@ -114,6 +127,7 @@ def _load() -> ctypes.CDLL:
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     vpp = ctypes.POINTER(ctypes.c_void_p)
     cfgp = ctypes.POINTER(_Config)
+    f8 = ctypes.POINTER(_Fp8)
     sig = {
         "iris_ag_mm": [vp, vp, vpp, i32, vp, vp, i64, i64, i64, cfgp, vp, sz, vp],
         "iris_ag_mm_noalloc": [vp, vp, vpp, i32, vp, vp, i64, i64, i64, cfgp, vp],
@@ -121,6 +135,10 @@ def _load() -> ctypes.CDLL:
         "iris_mm_ar_local": [vp, vp, vp, vp, vp, vpp, i32, i64, i64, i64, cfgp, vp, sz, vp],
         "iris_concurrent": [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vpp, i32, i64, cfgp, vp, sz, vp],
         "iris_mm_ag_local": [vp, vp, vp, vp, vpp, i32, i32, i64, i64, i64, cfgp, vp, sz, vp],
+        "iris_fp8_quantize": [f8, f8, vp, i32, i64, f8, i64, i64, vp],
+        "iris_fp8_mm": [vp, i32, i64, f8, f8, vp, i64, i64, i64, i32, vp, sz, vp],
+        "iris_fp8_swiglu": [f8, f8, f8, vp, vp, i32, i64, i64, i64, i64, vp],
+        "iris_fp8_swiglu_bwd": [f8, f8, f8, f8, f8, vp, i32, i64, f8, f8, i64, i64, vp],
         "iris_grid_size": [ctypes.c_int32, cfgp],
         "iris_tune_gemm_wgs": [ctypes.POINTER(_OpArgs), ctypes.POINTER(i32), i32, i32, i32,
                                ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_float), vp],
@@ -142,6 +160,8 @@ def _load() -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     lib.iris_workspace_size.argtypes = [i32, i64, i64, i64, i32, cfgp]
     lib.iris_workspace_size.restype = sz
+    lib.iris_fp8_mm_workspace_size.argtypes = [i64, i64, i64]
+    lib.iris_fp8_mm_workspace_size.restype = sz
     lib.iris_status_str.restype = ctypes.c_char_p
     lib.iris_last_error_message.restype = ctypes.c_char_p
     return lib
@@ -384,6 +404,195 @@ def iris_mm_ag_local(out, A, B, peers, W, rank=0, bias=None, config=None, worksp
     _check(_lib.iris_mm_ag_local(_ptr(out, "out"), _ptr(A, "A"), _ptr(B, "B"), _ptr(bias, "bias", True),
                                  _ptr_array(peers, "peers"), W, rank, M, N, K, _cfg(config), ws, wsb,
                                  _stream(stream)))
+
+
+# ---------------------------------------------------------- 8-bit operators
+
+_FP8_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 3}
+
+
+class Fp8:
+    """A block-scaled 8-bit matrix: `codes` (rows, cols) float8_e4m3fn or uint8,
+    `scales` (ceil(rows / block), ceil(cols / 128)) float8_e8m0fnu or uint8,
+    `block` 1 (a scale for every 1 x 128 entries) or 128 (128 x 128). An entry's
+    value is its code times 2^(scale byte - 127). Rows of codes start at
+    multiples of 16 bytes and, in an operand of iris_fp8_mm, rows of scales at
+    multiples of 4 (iris_fp8_empty lays memory out that way).
+
+    The object is a handle: it reads the tensors' addresses once and holds the
+    tensors, so their memory must not be exchanged (set_, resize_) under it.
+    """
+    __slots__ = ("codes", "scales", "block", "shape", "_c", "_p", "_on_gpu")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, block: int = 1):
+        rows, cols = _shape2(codes, "codes")
+        if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError("codes must be a float8_e4m3fn (or uint8) torch tensor")
+        if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+            raise TypeError("scales must be a float8_e8m0fnu (or uint8) torch tensor")
+        if block not in (1, 128):
+            raise ValueError(f"block must be 1 or 128 (got {block})")
+        _want_shape(scales, (-(-rows // block), -(-cols // 128)), "scales")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on different devices")
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
+                raise ValueError(f"{name} must be contiguous along its rows")
+        ld, lds = _pitch(codes, 16), _pitch(scales, 4)
+        if codes.numel() > 0:
+            if ld % 16 != 0:
+                raise ValueError(f"rows of codes must start at multiples of 16 bytes (pitch {ld}); see iris_fp8_empty")
+            end = codes.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
+            if end > codes.untyped_storage().nbytes():
+                raise ValueError("the last row of codes must be followed by memory up to the next multiple of 16 bytes")
+        self.codes, self.scales, self.block, self.shape = codes, scales, block, (rows, cols)
+        self._on_gpu = codes.is_cuda
+        self._c = _Fp8(codes.data_ptr(), scales.data_ptr(), ld, lds, block)
+        self._p = ctypes.pointer(self._c)
+
+
+def _pitch(t: torch.Tensor, unit: int) -> int:
+    """Row pitch in elements; a single row has any pitch, so it gets a whole one."""
+    return t.stride(0) if t.shape[0] > 1 else -(-max(1, t.shape[1]) // unit) * unit
+
+
+def iris_fp8_empty(rows: int, cols: int, block: int = 1, device=None) -> Fp8:
+    """Memory of a (rows, cols) block-scaled matrix, laid out as every 8-bit
+    operator takes it: codes with a row pitch that is a multiple of 16, scales
+    with one that is a multiple of 4 (uninitialised)."""
+    device = torch.device("cuda") if device is None else device
+    nb = -(-cols // 128)
+    codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+    scales = torch.empty((-(-rows // block), -(-nb // 4) * 4), dtype=torch.uint8, device=device)
+    return Fp8(codes[:, :cols], scales.view(torch.float8_e8m0fnu)[:, :nb], block)
+
+
+def _want_fp8(q, shape, name: str, allow_none=False):
+    """Pointer to q's C struct after its shape (and, last, its device) check."""
+    if q is None:
+        if allow_none:
+            return None
+        raise ValueError(f"{name} is required")
+    if not isinstance(q, Fp8):
+        raise TypeError(f"{name} must be an Fp8 matrix")
+    if q.shape != shape:
+        raise ValueError(f"{name} has shape {q.shape}, expected {shape}")
+    return q
+
+
+def _fp8_ptr(q, name: str):
+    if q is None:
+        return None
+    if not q._on_gpu:
+        raise ValueError(f"{name} must be on a GPU")
+    return q._p
+
+
+def _plain(t, name: str, dtypes):
+    """(pointer, type, row pitch) of a row-major matrix with any row pitch."""
+    kind = dtypes.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be one of {', '.join(str(d)[6:] for d in dtypes)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    return t.data_ptr(), kind, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+_FP8_HALVES = {torch.float16: 1, torch.bfloat16: 2}
+
+
+def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, stream=None) -> None:
+    """x (rows, cols) to 8 bits: q (rows, cols) with blocks along its rows and /
+    or q_t (cols, rows), x transposed, both in one pass. x is a float16, bfloat16
+    or float32 tensor, or an Fp8 matrix (then only q_t, blocks of 1 x 128)."""
+    if isinstance(x, Fp8):
+        rows, cols = x.shape
+    else:
+        rows, cols = _shape2(x, "x")
+    _want_fp8(q, (rows, cols), "q", True)
+    _want_fp8(q_t, (cols, rows), "q_t", True)
+    if isinstance(x, Fp8):
+        ptr, kind, ld, x8 = None, 0, 0, _fp8_ptr(x, "x")
+    else:
+        (ptr, kind, ld), x8 = _plain(x, "x", _FP8_TYPES), None
+    st = _lib.iris_fp8_quantize(_fp8_ptr(q, "q"), _fp8_ptr(q_t, "q_t"), ptr, kind, ld, x8, rows, cols, _stream(stream))
+    if st:
+        _check(st)
+
+
+def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, workspace=None, stream=None) -> None:
+    """C = A @ B^T + bias (+ C with accumulate): A (M, K) Fp8 with blocks of
+    1 x 128, B (N, K) Fp8, C (M, N) float16, bfloat16 or float32, bias of C's type."""
+    if not isinstance(A, Fp8) or not isinstance(B, Fp8):
+        raise TypeError("A and B must be Fp8 matrices")
+    M, K = A.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError(f"B has shape {B.shape}, expected ({N}, {K})")
+    _want_shape(C, (M, N), "C")
+    flags = IRIS_FLAG_ACCUMULATE if accumulate else 0
+    bias_ptr = None
+    if bias is not None:
+        _want_bias(bias, M, N, config)
+        if bias.dtype != C.dtype:
+            raise TypeError(f"bias must be {C.dtype} as C is")
+        if not bias.is_contiguous():
+            raise ValueError("bias must be contiguous")
+        if _bias_along_m(config):
+            flags |= IRIS_FLAG_BIAS_ALONG_M
+        bias_ptr = bias.data_ptr()
+    ptr, kind, ld = _plain(C, "C", _FP8_TYPES)
+    if bias is not None and not bias.is_cuda:
+        raise ValueError("bias must be on a GPU")
+    ws, wsb = _ws(workspace)
+    st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8_ptr(A, "A"), _fp8_ptr(B, "B"), bias_ptr, M, N, K, flags, ws, wsb,
+                          _stream(stream))
+    if st:
+        _check(st)
+
+
+def iris_fp8_swiglu(h: Fp8, gate, up, gate_kept: Optional[Fp8] = None, up_kept: Optional[Fp8] = None,
+                    stream=None) -> None:
+    """h = silu(gate) * up in 8 bits; gate, up (rows, cols) float16 or bfloat16
+    (views of one matrix will do); gate_kept and up_kept receive them in 8 bits."""
+    rows, cols = _shape2(gate, "gate")
+    _want_shape(up, (rows, cols), "up")
+    if up.dtype != gate.dtype:
+        raise TypeError("gate and up must have one dtype")
+    _want_fp8(h, (rows, cols), "h")
+    _want_fp8(gate_kept, (rows, cols), "gate_kept", up_kept is None)
+    _want_fp8(up_kept, (rows, cols), "up_kept", gate_kept is None)
+    gp, kind, gld = _plain(gate, "gate", _FP8_HALVES)
+    up_, _, uld = _plain(up, "up", _FP8_HALVES)
+    st = _lib.iris_fp8_swiglu(_fp8_ptr(h, "h"), _fp8_ptr(gate_kept, "gate_kept"), _fp8_ptr(up_kept, "up_kept"), gp,
+                              up_, kind, gld, uld, rows, cols, _stream(stream))
+    if st:
+        _check(st)
+
+
+def iris_fp8_swiglu_bwd(dgate: Fp8, dup: Fp8, dh, gate_kept: Fp8, up_kept: Fp8, dgate_t: Optional[Fp8] = None,
+                        dup_t: Optional[Fp8] = None, h_t: Optional[Fp8] = None, stream=None) -> None:
+    """Backward pass of iris_fp8_swiglu at the kept gate and up: dgate, dup
+    (rows, cols) and, if given, dgate_t, dup_t and the recomputed h_t (cols,
+    rows), all in 8 bits; dh (rows, cols) float16 or bfloat16."""
+    rows, cols = _shape2(dh, "dh")
+    for q, name in ((dgate, "dgate"), (dup, "dup"), (gate_kept, "gate_kept"), (up_kept, "up_kept")):
+        _want_fp8(q, (rows, cols), name)
+    for q, name in ((dgate_t, "dgate_t"), (dup_t, "dup_t"), (h_t, "h_t")):
+        _want_fp8(q, (cols, rows), name, True)
+    ptr, kind, ld = _plain(dh, "dh", _FP8_HALVES)
+    st = _lib.iris_fp8_swiglu_bwd(_fp8_ptr(dgate, "dgate"), _fp8_ptr(dup, "dup"), _fp8_ptr(dgate_t, "dgate_t"),
+                                  _fp8_ptr(dup_t, "dup_t"), _fp8_ptr(h_t, "h_t"), ptr, kind, ld,
+                                  _fp8_ptr(gate_kept, "gate_kept"), _fp8_ptr(up_kept, "up_kept"), rows, cols,
+                                  _stream(stream))
+    if st:
+        _check(st)
+
+
+def iris_fp8_mm_workspace_size(M, N, K) -> int:
+    return int(_lib.iris_fp8_mm_workspace_size(M, N, K))
 
 
 # ------------------------------------------------------------------- helpers

@@ -23,7 +23,8 @@ COMMON = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
     "-Wall", "-Wno-unused-command-line-argument",
 ]
-SOURCES = ["kernels.hip", "iris_local.cpp", "predict.cpp", "mfma_ceiling.hip"]
+SOURCES = ["kernels.hip", "iris_local.cpp", "predict.cpp", "mfma_ceiling.hip",
+           "fp8_gemm.hip", "fp8_quant.hip", "fp8_ops.cpp"]
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -1,0 +1,258 @@
+// Entry points of the 8-bit operators: argument checks (all of them before
+// any HIP call) and launches.
+#include "../../include/iris_local.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+
+#include "fp8.hpp"
+
+namespace iris {
+// beside the other entry points
+int set_error(int status, const char* msg);
+int use_device(int* dev, int* cus);
+}  // namespace iris
+
+namespace {
+
+using iris::Fp8Mat;
+
+int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int fail(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return iris::set_error(status, buf);
+}
+
+int launched(hipError_t e, const char* what) {
+  if (e == hipSuccess) return IRIS_OK;
+  return fail(IRIS_ERR_HIP, "%s launch: %s (%d)", what, hipGetErrorString(e), (int)e);
+}
+
+constexpr int64_t kBlk = iris::kFp8Block;
+int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
+
+// rows and columns of a memory-bound operator: its grid numbers 128-wide
+// blocks of rows (or tiles) in 31 bits
+int check_dims(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0)
+    return fail(IRIS_ERR_INVALID_ARG, "rows and cols must not be negative (got %lld, %lld)", (long long)rows,
+                (long long)cols);
+  if (rows > (1 << 30) || cols > (1 << 30) || (rows > 0 && blocks(cols) > (((int64_t)1 << 31) - 1) / rows))
+    return fail(IRIS_ERR_UNSUPPORTED, "matrix too large (limits: rows and cols <= 2^30, rows * ceil(cols / 128) < 2^31)");
+  return IRIS_OK;
+}
+
+int check_fp8(const iris_fp8_t* q, int64_t rows, int64_t cols, const char* name) {
+  if (!q) return fail(IRIS_ERR_INVALID_ARG, "%s is NULL", name);
+  if (q->block != 1 && q->block != kBlk)
+    return fail(IRIS_ERR_INVALID_ARG, "%s: block must be 1 or 128 (got %d)", name, q->block);
+  if (rows == 0 || cols == 0) return IRIS_OK;
+  if (!q->codes || !q->scales) return fail(IRIS_ERR_INVALID_ARG, "%s: codes and scales must not be NULL", name);
+  if ((uintptr_t)q->codes % 16 != 0 || q->ld % 16 != 0)
+    return fail(IRIS_ERR_ALIGNMENT, "%s: codes must be 16-byte aligned and ld a multiple of 16 (ld %lld)", name,
+                (long long)q->ld);
+  if (q->ld < cols)
+    return fail(IRIS_ERR_INVALID_ARG, "%s: ld %lld is shorter than the %lld columns", name, (long long)q->ld, (long long)cols);
+  if (q->ld_scales < blocks(cols))
+    return fail(IRIS_ERR_INVALID_ARG, "%s: ld_scales %lld is shorter than the %lld blocks of a row", name,
+                (long long)q->ld_scales, (long long)blocks(cols));
+  return IRIS_OK;
+}
+
+int check_blocks1(const iris_fp8_t* q, int64_t rows, int64_t cols, const char* name) {
+  const int st = check_fp8(q, rows, cols, name);
+  if (st) return st;
+  if (q->block != 1) return fail(IRIS_ERR_UNSUPPORTED, "%s: block must be 1 here (got %d)", name, q->block);
+  return IRIS_OK;
+}
+
+int type_bytes(int32_t type) { return type == IRIS_TYPE_FP32 ? 4 : 2; }
+
+int check_plain(const void* x, int32_t type, bool fp32_too, int64_t ld, int64_t rows, int64_t cols, const char* name) {
+  if (type != IRIS_TYPE_FP16 && type != IRIS_TYPE_BF16 && !(fp32_too && type == IRIS_TYPE_FP32))
+    return fail(IRIS_ERR_INVALID_ARG, "%s: type %d is not served here", name, type);
+  if (rows == 0 || cols == 0) return IRIS_OK;
+  if (!x) return fail(IRIS_ERR_INVALID_ARG, "%s is NULL", name);
+  if ((uintptr_t)x % type_bytes(type) != 0) return fail(IRIS_ERR_ALIGNMENT, "%s is not aligned to its type", name);
+  if (ld < cols)
+    return fail(IRIS_ERR_INVALID_ARG, "%s: row pitch %lld is shorter than the %lld columns", name, (long long)ld, (long long)cols);
+  return IRIS_OK;
+}
+
+// every row of a plain matrix starts at a multiple of 16 bytes
+bool rows16(const void* x, int64_t ld, int32_t type) {
+  return (uintptr_t)x % 16 == 0 && ld * type_bytes(type) % 16 == 0;
+}
+
+Fp8Mat mat(const iris_fp8_t* q) {
+  if (!q) return Fp8Mat{};
+  return Fp8Mat{(uint8_t*)q->codes, (uint8_t*)q->scales, q->ld, q->ld_scales};
+}
+
+int ready() {
+  int dev = 0, cus = 0;
+  return iris::use_device(&dev, &cus);
+}
+
+}  // namespace
+
+extern "C" {
+
+int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x, int32_t x_type, int64_t ldx,
+                      const iris_fp8_t* x8, int64_t rows, int64_t cols, void* stream) {
+  iris::set_error(IRIS_OK, "");
+  int st;
+  if ((st = check_dims(rows, cols)) || (st = check_dims(cols, rows))) return st;
+  if (!q && !q_t) return fail(IRIS_ERR_INVALID_ARG, "q and q_t are both NULL");
+  if (q && (st = check_fp8(q, rows, cols, "q"))) return st;
+  if (q_t && (st = check_fp8(q_t, cols, rows, "q_t"))) return st;
+  if (q && q_t && q->block != q_t->block)
+    return fail(IRIS_ERR_INVALID_ARG, "q and q_t have different blocks (%d, %d)", q->block, q_t->block);
+  iris::Fp8QuantArgs a{};
+  a.block = q ? q->block : q_t->block;
+  if (x8) {
+    if (x) return fail(IRIS_ERR_INVALID_ARG, "x and x8 are both given");
+    if (q || a.block != 1)
+      return fail(IRIS_ERR_UNSUPPORTED, "an 8-bit matrix is only turned around: q must be NULL and q_t's block 1");
+    if ((st = check_blocks1(x8, rows, cols, "x8"))) return st;
+    a.x8 = mat(x8);
+    a.x_type = iris::T_FP8;
+  } else {
+    if ((st = check_plain(x, x_type, true, ldx, rows, cols, "x"))) return st;
+    a.x = x;
+    a.ldx = ldx;
+    a.x_type = x_type;
+    a.vec = rows16(x, ldx, x_type);
+  }
+  if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = ready())) return st;
+  a.q = mat(q);
+  a.qt = mat(q_t);
+  a.rows = (int)rows;
+  a.cols = (int)cols;
+  return launched(iris::launch_fp8_quantize(a, (hipStream_t)stream), "iris_fp8_quantize");
+}
+
+size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K) {
+  (void)M;
+  (void)N;
+  (void)K;
+  return 0;
+}
+
+int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B, const void* bias,
+                int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  iris::set_error(IRIS_OK, "");
+  (void)workspace;
+  (void)workspace_bytes;
+  int st;
+  if (M < 0 || N < 0 || K < 0)
+    return fail(IRIS_ERR_INVALID_ARG, "M, N, K must not be negative (got %lld, %lld, %lld)", (long long)M, (long long)N,
+                (long long)K);
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 30) || blocks(M) * blocks(N) >= ((int64_t)1 << 31))
+    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N, K <= 2^30 and fewer than 2^31 output blocks)");
+  if (flags & ~(IRIS_FLAG_BIAS_ALONG_M | IRIS_FLAG_ACCUMULATE))
+    return fail(IRIS_ERR_CONFIG, "unknown flag bits 0x%x", flags);
+  if ((st = check_plain(C, c_type, true, ldc, M, N, "C")) || (st = check_blocks1(A, M, K, "A")) ||
+      (st = check_fp8(B, N, K, "B")))
+    return st;
+  if (M > 0 && K > 0 && ((uintptr_t)A->scales % 4 != 0 || A->ld_scales % 4 != 0))
+    return fail(IRIS_ERR_ALIGNMENT, "A: scales must be 4-byte aligned and ld_scales a multiple of 4");
+  if (N > 0 && K > 0 && ((uintptr_t)B->scales % 4 != 0 || B->ld_scales % 4 != 0))
+    return fail(IRIS_ERR_ALIGNMENT, "B: scales must be 4-byte aligned and ld_scales a multiple of 4");
+  if (bias && (uintptr_t)bias % type_bytes(c_type) != 0) return fail(IRIS_ERR_ALIGNMENT, "bias is not aligned to its type");
+  if (M == 0 || N == 0) return IRIS_OK;
+  if ((st = ready())) return st;
+  iris::Fp8MmArgs a{};
+  a.A = mat(A);
+  a.B = mat(B);
+  a.b_block = B->block;
+  a.bias = bias;
+  a.bias_along_m = (flags & IRIS_FLAG_BIAS_ALONG_M) ? 1 : 0;
+  a.accumulate = (flags & IRIS_FLAG_ACCUMULATE) ? 1 : 0;
+  a.C = C;
+  a.c_type = c_type;
+  a.ldc = ldc;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  return launched(iris::launch_fp8_mm(a, (hipStream_t)stream), "iris_fp8_mm");
+}
+
+int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept, const void* gate,
+                    const void* up, int32_t type, int64_t ld_gate, int64_t ld_up, int64_t rows, int64_t cols,
+                    void* stream) {
+  iris::set_error(IRIS_OK, "");
+  int st;
+  if ((st = check_dims(rows, cols)) || (st = check_blocks1(h, rows, cols, "h"))) return st;
+  if (!gate_kept != !up_kept) return fail(IRIS_ERR_INVALID_ARG, "gate_kept and up_kept go together");
+  if (gate_kept && ((st = check_blocks1(gate_kept, rows, cols, "gate_kept")) ||
+                    (st = check_blocks1(up_kept, rows, cols, "up_kept"))))
+    return st;
+  if ((st = check_plain(gate, type, false, ld_gate, rows, cols, "gate")) ||
+      (st = check_plain(up, type, false, ld_up, rows, cols, "up")))
+    return st;
+  if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = ready())) return st;
+  iris::Fp8SwigluArgs a{};
+  a.gate = gate;
+  a.up = up;
+  a.ld_gate = ld_gate;
+  a.ld_up = ld_up;
+  a.type = type;
+  a.vec = rows16(gate, ld_gate, type) && rows16(up, ld_up, type);
+  a.h = mat(h);
+  a.gate8 = mat(gate_kept);
+  a.up8 = mat(up_kept);
+  a.rows = (int)rows;
+  a.cols = (int)cols;
+  return launched(iris::launch_fp8_swiglu(a, (hipStream_t)stream), "iris_fp8_swiglu");
+}
+
+int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const iris_fp8_t* dgate_t,
+                        const iris_fp8_t* dup_t, const iris_fp8_t* h_t, const void* dh, int32_t type, int64_t ld_dh,
+                        const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept, int64_t rows, int64_t cols,
+                        void* stream) {
+  iris::set_error(IRIS_OK, "");
+  int st;
+  if ((st = check_dims(rows, cols)) || (st = check_dims(cols, rows))) return st;
+  const struct {
+    const iris_fp8_t* q;
+    const char* name;
+    bool turned, required;
+  } mats[] = {{dgate, "dgate", false, true},          {dup, "dup", false, true},
+              {gate_kept, "gate_kept", false, true},  {up_kept, "up_kept", false, true},
+              {dgate_t, "dgate_t", true, false},      {dup_t, "dup_t", true, false},
+              {h_t, "h_t", true, false}};
+  for (const auto& m : mats)
+    if ((m.required || m.q) &&
+        (st = check_blocks1(m.q, m.turned ? cols : rows, m.turned ? rows : cols, m.name)))
+      return st;
+  if ((st = check_plain(dh, type, false, ld_dh, rows, cols, "dh"))) return st;
+  if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = ready())) return st;
+  iris::Fp8SwigluBwdArgs a{};
+  a.dh = dh;
+  a.ld_dh = ld_dh;
+  a.type = type;
+  a.vec = rows16(dh, ld_dh, type);
+  a.gate8 = mat(gate_kept);
+  a.up8 = mat(up_kept);
+  a.dgate = mat(dgate);
+  a.dup = mat(dup);
+  a.dgate_t = mat(dgate_t);
+  a.dup_t = mat(dup_t);
+  a.h_t = mat(h_t);
+  a.rows = (int)rows;
+  a.cols = (int)cols;
+  return launched(iris::launch_fp8_swiglu_bwd(a, (hipStream_t)stream), "iris_fp8_swiglu_bwd");
+}
+
+}  // extern "C"

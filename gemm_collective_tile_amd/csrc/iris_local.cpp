@@ -733,6 +733,14 @@ int set_error(int status, const char* msg) {
   g_msg = msg;
   return status;
 }
+
+// The current device, which has to be one that this library runs on.
+int use_device(int* dev, int* cus) {
+  DevInfo di;
+  const int st = current_device(dev, &di);
+  *cus = di.cus;
+  return st;
+}
 }  // namespace iris
 
 namespace {

@@ -272,6 +272,103 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
                     int32_t W, int64_t comm_elems, const iris_config_t* cfg,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * 8-bit operators: the feed-forward layer around the products above, in
+ * block-scaled 8-bit floating point, for training and for serving. They have
+ * no counterpart on the pages.
+ *
+ * A block-scaled matrix holds e4m3 codes (OCP FP8: no infinity, 0x7f and 0xff
+ * are NaN, largest value 448) and power-of-two scales: scale byte s stands
+ * for 2^(s-127), and an entry's value is code * scale. Blocks run along the
+ * row, which is always the direction a product contracts: `block` 1 gives
+ * every 1 x 128 entries a scale (activations, gradients), 128 every 128 x 128
+ * (weights). The last block of a row or column may be shorter; any number of
+ * rows and columns >= 0 is served.
+ *   codes      device, 16-byte aligned; row r starts at codes + r * ld, ld a
+ *              multiple of 16 and >= the number of columns. The bytes of a
+ *              row up to the next multiple of 16 are allocated; nothing is
+ *              written past the last column and what is there is ignored.
+ *   scales     device; block (i, j) is at scales + i * ld_scales + j. Operands
+ *              of iris_fp8_mm: 4-byte aligned, ld_scales a multiple of 4 (the
+ *              bytes up to it allocated; ignored).
+ * The structs are read before the call returns; the buffers belong to the
+ * caller. Unlike above, plain matrices (x, C, gate, up, dh) may have any row
+ * pitch >= their columns and need only the alignment of their type; rows that
+ * start at multiples of 16 bytes are faster.
+ */
+typedef struct iris_fp8 {
+  void* codes;
+  void* scales;
+  int64_t ld;
+  int64_t ld_scales;
+  int32_t block;
+} iris_fp8_t;
+
+#define IRIS_TYPE_FP16 1
+#define IRIS_TYPE_BF16 2
+#define IRIS_TYPE_FP32 3
+
+#define IRIS_FLAG_ACCUMULATE 8 /* iris_fp8_mm: add to what C holds */
+
+/*
+ * x -> 8 bits. Scale of a block: the smallest power of two, at least 2^-126,
+ * that brings the largest finite magnitude to 448 or less; 1 if there is
+ * none but 0. Code: value / scale (exact) rounded to nearest even; infinities
+ * and NaN become NaN.
+ *   q     (rows, cols), blocks along x's rows, or NULL
+ *   q_t   (cols, rows): x transposed, blocks along x's columns, or NULL
+ *         Both come from one pass over x. If both are given they have the same
+ *         `block`.
+ *   x     (rows, cols) of x_type, row pitch ldx elements; or NULL, and then
+ *   x8    is an 8-bit matrix with block 1 (a kept activation) and q is NULL:
+ *         its values get new scales along the other direction.
+ */
+int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x, int32_t x_type,
+                      int64_t ldx, const iris_fp8_t* x8, int64_t rows, int64_t cols, void* stream);
+
+/*
+ * C = A @ B^T + bias,  A (M, K) with block 1, B (N, K) with block 1 or 128.
+ * C: (M, N) of c_type, row pitch ldc elements. bias: NULL, or N values of
+ * c_type (M with IRIS_FLAG_BIAS_ALONG_M). Sums run in 32 bits; each output is
+ * rounded once, after the bias and, with IRIS_FLAG_ACCUMULATE, C's old value.
+ * K = 0 gives the bias (and old value) alone. C must not overlap an input.
+ * The product of a layer is A = activations, B = weights (out, in); the
+ * input's gradient A = output gradients, B = transposed weights; the weight's
+ * gradient A = transposed output gradients, B = transposed activations.
+ * workspace: as for the ops above (NULL: the library's own), at least
+ * iris_fp8_mm_workspace_size() bytes, 256-byte aligned and zero-filled before
+ * its first use. One workspace may not serve two ops at the same time.
+ */
+int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B,
+                const void* bias, int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace,
+                size_t workspace_bytes, void* stream);
+size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * The gated activation between a layer's two products:
+ *   h = silu(gate) * up,  silu(g) = g / (1 + exp(-g)),  to 8 bits, block 1.
+ * gate, up: (rows, cols) of `type` (fp16 or bf16), row pitches ld_gate, ld_up
+ * (two halves of one matrix will do). gate_kept, up_kept: both NULL, or both
+ * receive gate and up in 8 bits, block 1, for the backward pass.
+ */
+int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept,
+                    const void* gate, const void* up, int32_t type, int64_t ld_gate, int64_t ld_up,
+                    int64_t rows, int64_t cols, void* stream);
+
+/*
+ * Its backward pass at the kept gate and up. With s = 1 / (1 + exp(-gate)):
+ *   dgate = dh * up * s * (1 + gate * (1 - s))
+ *   dup   = dh * gate * s
+ *   h     = gate * s * up      (computed again)
+ * dgate, dup: (rows, cols), block 1. dgate_t, dup_t, h_t: (cols, rows), block
+ * 1, the operands of the weight gradients; each may be NULL. dh: (rows, cols)
+ * of `type` (fp16 or bf16), row pitch ld_dh.
+ */
+int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const iris_fp8_t* dgate_t,
+                        const iris_fp8_t* dup_t, const iris_fp8_t* h_t, const void* dh, int32_t type,
+                        int64_t ld_dh, const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept,
+                        int64_t rows, int64_t cols, void* stream);
+
 /* Bytes of device workspace an op needs (0 on invalid arguments). The
  * workspace holds per-workgroup timestamps, then the queue counters (one
  * GEMM queue per XCD and the comm queue), the finished-workgroup and
