@@ -24,7 +24,7 @@ COMMON = [
     "-Wall", "-Wno-unused-command-line-argument",
 ]
 SOURCES = ["kernels.hip", "iris_local.cpp", "predict.cpp", "mfma_ceiling.hip",
-           "fp8_gemm.hip", "fp8_quant.hip", "fp8_ops.cpp"]
+           "fp8_gemm.hip", "fp8_gemm_few.hip", "fp8_quant.hip", "fp8_ops.cpp"]
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -22,6 +22,9 @@ struct Fp8MmArgs {
   int32_t M, N, K;
 };
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, hipStream_t s);
+// at most kFp8FewRows rows of A
+constexpr int kFp8FewRows = 64;
+hipError_t launch_fp8_mm_few(const Fp8MmArgs& a, hipStream_t s);
 
 struct Fp8QuantArgs {
   const void* x;          // fp16, bf16 or fp32 values with a row pitch of ldx elements

@@ -25,39 +25,13 @@
 // step of 128 bytes goes through registers into LDS, rows of 128 bytes whose
 // 16-byte pieces are permuted by the row.
 #include "fp8.hpp"
+#include "fp8_mma.hpp"
 
 namespace iris {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// 8 codes times a scale, exactly (the scale's bits: byte << 23)
-__device__ __forceinline__ bf16x8 to_bf16x8(uint32_t lo, uint32_t hi, float scale) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 constexpr int kBK = 128;
 constexpr int kTM = 128, kTN = 128;
-
-// bytes of a 16-byte piece from `valid` on become 0
-__device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int valid) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = valid - 4 * i;
-    v[i] = n >= 4 ? v[i] : (n <= 0 ? 0u : v[i] & ((1u << (8 * n)) - 1u));
-  }
-  return v;
-}
-
-__device__ __forceinline__ i32x8 pair(u32x4 lo, u32x4 hi) {
-  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
 
 __device__ __forceinline__ uint32_t swz(uint32_t row) { return (row >> 1) & 7u; }
 
@@ -148,10 +122,7 @@ __global__ __launch_bounds__(256) void fp8_mm_kernel(Fp8MmArgs g) {
       for (int e = 0; e < 16; ++e) {
         const int n = n0 + wn + 32 * j + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
         if (n >= g.N) continue;
-        float v = acc[i][j][e];
-        if (bias) v += widen(bias[g.bias_along_m ? m : n]);
-        if (g.accumulate) v += widen(crow[n]);
-        narrow(v, crow[n]);
+        put_output(crow + n, acc[i][j][e], bias, g.bias_along_m ? m : n, g.accumulate);
       }
   }
 }
@@ -159,6 +130,7 @@ __global__ __launch_bounds__(256) void fp8_mm_kernel(Fp8MmArgs g) {
 }  // namespace
 
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, hipStream_t s) {
+  if (a.M <= kFp8FewRows) return launch_fp8_mm_few(a, s);
   const uint32_t grid = (uint32_t)(((int64_t)a.M + kTM - 1) / kTM * (((int64_t)a.N + kTN - 1) / kTN));
   switch (a.c_type) {
     case T_FP16: hipLaunchKernelGGL((fp8_mm_kernel<f16>), dim3(grid), dim3(256), 0, s, a); break;

@@ -1,0 +1,44 @@
+// Pieces that the 8-bit products share: operands of the matrix instructions
+// and the last steps of an output.
+#pragma once
+
+#include "fp8_common.hpp"
+
+namespace iris {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// 8 codes times a scale, exactly (the scale's bits: byte << 23)
+__device__ __forceinline__ bf16x8 to_bf16x8(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// bytes of a 16-byte piece from `valid` on become 0
+__device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int valid) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = valid - 4 * i;
+    v[i] = n >= 4 ? v[i] : (n <= 0 ? 0u : v[i] & ((1u << (8 * n)) - 1u));
+  }
+  return v;
+}
+
+__device__ __forceinline__ i32x8 pair(u32x4 lo, u32x4 hi) {
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// bias and old value, then the one rounding
+template <class OUT>
+__device__ __forceinline__ void put_output(OUT* c, float v, const OUT* bias, int64_t bias_at, int accumulate) {
+  if (bias) v += widen(bias[bias_at]);
+  if (accumulate) v += widen(*c);
+  narrow(v, *c);
+}
+
+}  // namespace iris
