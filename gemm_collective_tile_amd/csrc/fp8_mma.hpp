@@ -33,6 +33,21 @@ __device__ __forceinline__ i32x8 pair(u32x4 lo, u32x4 hi) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// 16 bytes per lane from global memory into LDS: lane l's go to base + 16 l
+// (base is the same in all lanes; lanes that are off load nothing). Complete
+// after wait_loads.
+__device__ __forceinline__ void load_to_lds(const uint8_t* src, char* base) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)base, 16, 0, 0);
+}
+// until at most N of this wave's vector loads are under way
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// until this wave's LDS reads are in registers
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // bias and old value, then the one rounding
 template <class OUT>
 __device__ __forceinline__ void put_output(OUT* c, float v, const OUT* bias, int64_t bias_at, int accumulate) {
