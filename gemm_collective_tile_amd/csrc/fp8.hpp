@@ -19,6 +19,7 @@ struct Fp8MmArgs {
   void* C;
   int32_t c_type;
   int64_t ldc;            // elements
+  int32_t vec;            // rows of C start at multiples of 16 bytes
   int32_t M, N, K;
 };
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, hipStream_t s);

@@ -15,129 +15,391 @@
 // fp32 C (weight gradients to be summed up) asks for more: the codes become
 // bf16 values with their scales applied (v_cvt_scalef32_pk_bf16_fp8, exact)
 // and v_mfma_f32_32x32x16_bf16, at half the rate, multiplies them exactly and
-// sums in 32 bits (4e-8 of the result, measured).
+// sums in 32 bits (4e-8 of the result, measured). The conversions run in the
+// shadow of the matrix instructions.
 //
 // Any order of k inside an instruction's slice gives the same sum as long as
 // both operands use it, and a block's scale is the same for all its slices, so
 // a lane takes the 16-byte pieces that are cheapest to read.
 //
-// One workgroup of 4 waves takes a 128 x 128 tile, a wave 64 x 64 of it. A K
-// step of 128 bytes goes through registers into LDS, rows of 128 bytes whose
-// 16-byte pieces are permuted by the row.
+// Design (4 waves, 2 x 2, each a (BM/2) x (BN/2) part of the tile in 32-bit
+// accumulators):
+//   * K is walked in steps of 128 bytes per row. Rows go from memory straight
+//     into one of two LDS stages (no registers in between: the accumulators
+//     and one step's operands fill the file), 8 lanes to a row's 128 bytes,
+//     the 16-byte pieces permuted by the row so that the operand reads of 16
+//     rows' same pieces meet 16 different bank groups.
+//   * A step has two slices of 64. While slice 0 multiplies, slice 1's
+//     operands are read. Then every wave has this stage in registers, one
+//     barrier says so, and while slice 1 multiplies, the loads of the step
+//     after the next go into this stage and slice 0 of the next step is read
+//     from the other one. A load has more than a step's time (0.9 us at 256 x
+//     256) to arrive, and no operand read is waited for.
+//   * The loads into LDS are written as assembly, because the compiler would
+//     wait for all of them at the next LDS read.
 #include "fp8.hpp"
 #include "fp8_mma.hpp"
+#include "schedule.hpp"
 
 namespace iris {
 namespace {
 
 constexpr int kBK = 128;
-constexpr int kTM = 128, kTN = 128;
+constexpr int kGroupM = 8;     // tile rows of a patch that one XCD works on
+constexpr int kPatch = 32;     // tiles of a patch: the workgroups of an XCD
 
-__device__ __forceinline__ uint32_t swz(uint32_t row) { return (row >> 1) & 7u; }
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-template <class OUT>
-__global__ __launch_bounds__(256) void fp8_mm_kernel(Fp8MmArgs g) {
-  __shared__ char lds[(kTM + kTN) * kBK];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n_pn = (g.N + kTN - 1) / kTN;
-  const int m0 = (int)(blockIdx.x / n_pn) * kTM, n0 = (int)(blockIdx.x % n_pn) * kTN;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  const int ch = tid & 7;
+// 16 bytes per lane from a buffer into LDS at base + 16 * lane. m0 holds the
+// base for this one instruction; nothing else here keeps a value in it.
+__device__ __forceinline__ void buffer_to_lds(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(base), "v"(voff),
+               "s"(rsrc), "s"(soff)
+               : "memory");
+}
 
-  f32x16 acc[2][2] = {};
-  const int nk = (g.K + kBK - 1) / kBK;
-  for (int t = 0; t < nk; ++t) {
-    u32x4 r[8];
-    const int valid = min(16, g.K - (t * kBK + 16 * ch));
+__device__ __forceinline__ i32x4 buffer_words(const void* p) {
+  const uint64_t a = (uint64_t)p;
+  return i32x4{(int)__builtin_amdgcn_readfirstlane((uint32_t)a),
+               (int)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu), (int)0xfffffff0u, kRsrcWord3};
+}
+
+template <int BM, int BN>
+struct Tile {
+  static constexpr int WM = BM / 2, WN = BN / 2;       // a wave's part
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int A_STAGE = BM * kBK, B_STAGE = BN * kBK;
+  static constexpr int B_AT = 2 * A_STAGE;             // LDS: [A stages | B stages]
+  static constexpr int LDS = B_AT + 2 * B_STAGE;
+  static constexpr int LA = BM / 32, LB = BN / 32;     // loads of 1 KB per wave and step
+  static constexpr int NM = FM * FN;                   // 32 x 32 blocks per wave
+  static constexpr int NR = 2 * (FM + FN);             // operand reads per slice
+};
+
+// one slice's operands: two pieces per 32-row block
+template <class T>
+struct Slice {
+  u32x4 a[T::FM][2], b[T::FN][2];
+};
+
+template <class OUT, int BM, int BN>
+struct Work {
+  using T = Tile<BM, BN>;
+  static constexpr bool EXACT = sizeof(OUT) == 4;
+
+  const char* lds;
+  i32x4 ra, rb;                       // codes of this tile's first rows
+  uint32_t va[T::LA], vb[T::LB];      // this lane's loads, from there
+  uint32_t piece;                     // their offset in a row
+  uint32_t lds_wave;                  // LDS address of this wave's first load of a stage
+  uint32_t at[4];                     // this lane's pieces h, 2 + h, 4 + h, 6 + h in a wave's part
+  uint32_t at_a, at_b;                // that part of stage 0
+  uint32_t sa[T::FM], sb[T::FN];      // scale bytes of the coming steps, the present one lowest
+
+  // Load `item` of a step. In a ragged last step the pieces past the row's
+  // last one read that one again (`back` bytes before their place).
+  __device__ __forceinline__ void load(int item, uint32_t k, uint32_t back, int stage) const {
+    if (item < T::LA)
+      buffer_to_lds(ra, va[item < T::LA ? item : 0] - back, k, lds_wave + stage * T::A_STAGE + item * 32 * kBK);
+    else
+      buffer_to_lds(rb, vb[item < T::LA ? 0 : item - T::LA] - back, k,
+                    lds_wave + T::B_AT + stage * T::B_STAGE + (item - T::LA) * 32 * kBK);
+  }
+  __device__ __forceinline__ uint32_t back(uint32_t k, int K) const {
+    return (uint32_t)max(0, (int)(k + piece + 16) - ((K + 15) & ~15));
+  }
+  // Zeros for the bytes past K of a ragged last step that has landed in `stage`
+  __device__ __forceinline__ void cut(char* l, int tail, int stage, int tid) const {
+    const int r = tid >> 3, p = tid & 7, valid = tail - 16 * p;
+    if (valid < 16) {
+      char* const at0 = l + r * kBK + ((p ^ ((r >> 1) & 7)) << 4);
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int row = tid / 8 + 32 * (n & 3);
-      // rows past the end repeat the last one: their outputs are not stored
-      const uint8_t* p = n < 4 ? g.A.codes + (int64_t)min(m0 + row, g.M - 1) * g.A.ld
-                               : g.B.codes + (int64_t)min(n0 + row, g.N - 1) * g.B.ld;
-      r[n] = u32x4{};
-      if (valid > 0) r[n] = keep_bytes(ld16(p + t * kBK + 16 * ch), valid);
-    }
-    int sa[2], sb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sa[i] = g.A.scales[(int64_t)min(m0 + wm + 32 * i + (lane & 31), g.M - 1) * g.A.lds + t];
-      sb[i] = g.B.scales[(int64_t)(min(n0 + wn + 32 * i + (lane & 31), g.N - 1) / g.b_block) * g.B.lds + t];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int row = tid / 8 + 32 * n;
-      *(u32x4*)(lds + row * kBK + ((ch ^ swz(row)) << 4)) = r[n];
-    }
-    __syncthreads();
-    // lane (r, h) of a 32-row block takes pieces h, 2 + h, 4 + h, 6 + h of row r
-    u32x4 a[2][4], b[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t c = 2 * p + (lane >> 5);
-        const uint32_t ra = wm + 32 * i + (lane & 31), rb = kTM + wn + 32 * i + (lane & 31);
-        a[i][p] = *(const u32x4*)(lds + ra * kBK + ((c ^ swz(ra)) << 4));
-        b[i][p] = *(const u32x4*)(lds + rb * kBK + ((c ^ swz(rb)) << 4));
+      for (int i = 0; i < T::LA; ++i) {
+        u32x4* const q = (u32x4*)(at0 + stage * T::A_STAGE + i * 32 * kBK);
+        *q = keep_bytes(*q, valid);
       }
-    if constexpr (sizeof(OUT) == 4) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        bf16x8 x[2], y[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          x[i] = to_bf16x8(a[i][s / 2][2 * (s & 1)], a[i][s / 2][2 * (s & 1) + 1], __builtin_bit_cast(float, sa[i] << 23));
-          y[i] = to_bf16x8(b[i][s / 2][2 * (s & 1)], b[i][s / 2][2 * (s & 1) + 1], __builtin_bit_cast(float, sb[i] << 23));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[j], x[i], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < T::LB; ++i) {
+        u32x4* const q = (u32x4*)(at0 + T::B_AT + stage * T::B_STAGE + i * 32 * kBK);
+        *q = keep_bytes(*q, valid);
       }
-    } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                pair(b[j][2 * s], b[j][2 * s + 1]), pair(a[i][2 * s], a[i][2 * s + 1]), acc[i][j], 0, 0, 0, sb[j], 0, sa[i]);
     }
   }
 
+  // operand read X of slice s: a0, b0 .. b(FN-1), a1 .., the two pieces of each in turn
+  __device__ __forceinline__ void read(int x, int s, int stage, Slice<T>& f) const {
+    const int item = x / 2, h = x & 1;
+    if (item == 0 || item > T::FN) {
+      const int i = item == 0 ? 0 : item - T::FN;
+      f.a[i][h] = *(const u32x4*)(lds + (at_a + stage * T::A_STAGE + at[2 * s + h]) + i * 32 * kBK);
+    } else {
+      f.b[item - 1][h] = *(const u32x4*)(lds + (at_b + stage * T::B_STAGE + at[2 * s + h]) + (item - 1) * 32 * kBK);
+    }
+  }
+};
+
+// multiplies one slice; `other` is what is done beside it, in n shares
+template <class OUT, int BM, int BN, class F>
+__device__ __forceinline__ void multiply(const Work<OUT, BM, BN>& w, const Slice<Tile<BM, BN>>& f,
+                                         f32x16 (&acc)[Tile<BM, BN>::FM][Tile<BM, BN>::FN], F other) {
+  using T = Tile<BM, BN>;
+  if constexpr (!Work<OUT, BM, BN>::EXACT) {
+#pragma unroll
+    for (int k = 0; k < T::NM; ++k) {
+      const int i = k / T::FN, j = k % T::FN;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          pair(f.b[j][0], f.b[j][1]), pair(f.a[i][0], f.a[i][1]), acc[i][j], 0, 0, 0, (int)w.sb[j], 0, (int)w.sa[i]);
+      other(k, T::NM);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bf16x8 x[T::FM], y[T::FN];
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+        x[i] = to_bf16x8(f.a[i][q / 2][2 * (q & 1)], f.a[i][q / 2][2 * (q & 1) + 1],
+                         __builtin_bit_cast(float, (w.sa[i] & 0xffu) << 23));
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+        y[j] = to_bf16x8(f.b[j][q / 2][2 * (q & 1)], f.b[j][q / 2][2 * (q & 1) + 1],
+                         __builtin_bit_cast(float, (w.sb[j] & 0xffu) << 23));
+#pragma unroll
+      for (int k = 0; k < T::NM; ++k) {
+        const int i = k / T::FN, j = k % T::FN;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[j], x[i], acc[i][j], 0, 0, 0);
+        other(q * T::NM + k, 4 * T::NM);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// everything that this wave read and loaded is there, in all waves
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The 16 columns n .. n + 15 of a row that lanes l and l ^ 32 hold between them:
+// v[d] are columns n + 8 d + 4 h .. + 3. All lanes call it.
+template <class OUT>
+__device__ __forceinline__ void put_16(const Fp8MmArgs& g, OUT* crow, bool on, int n, int h, float (&v)[2][4]) {
+  const bool whole = on && g.vec && n + 16 <= g.N;
+  if (g.accumulate) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = n + 8 * d + 4 * h + e;
+        if (on && c < g.N) v[d][e] += widen(crow[c]);
+      }
+  }
+  if constexpr (sizeof(OUT) == 4) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      if (whole) *(f32x4*)(crow + n + 8 * d + 4 * h) = f32x4{v[d][0], v[d][1], v[d][2], v[d][3]};
+  } else {
+    // two columns per word; one swap per word gives each lane 8 neighbouring
+    // columns (the lower lanes the first 8), written at once
+    uint32_t w[2][2];
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      OUT o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) narrow(v[d][e], o[e]);
+      __builtin_memcpy(w[d], o, 8);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const auto sw = __builtin_amdgcn_permlane32_swap(w[0][x], w[1][x], false, false);
+      w[0][x] = sw[0];
+      w[1][x] = sw[1];
+    }
+    if (whole) *(u32x4*)(crow + n + 8 * h) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+  }
+  if (on && !whole) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = n + 8 * d + 4 * h + e;
+        if (c < g.N) narrow(v[d][e], crow[c]);
+      }
+  }
+}
+
+// shares [k n / N, (k + 1) n / N) of n things over N places
+#define IRIS_SHARE(x, n, k, N) for (int x = (k) * (n) / (N); x < ((k) + 1) * (n) / (N); ++x)
+
+template <class OUT, int BM, int BN>
+__global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
+  using T = Tile<BM, BN>;
+  __shared__ __align__(16) char lds[T::LDS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n_pm = (g.M + BM - 1) / BM, n_pn = (g.N + BN - 1) / BN;
+  int pm, pn;
+  {
+    // workgroups go to the XCDs in turn: each takes whole patches of 8 x 4 tiles
+    const int t = xcd_tile(kPatch, blockIdx.x % kXcds, blockIdx.x / kXcds);
+    if (t >= n_pm * n_pn) return;
+    grouped(t, n_pm, n_pn, kGroupM, pm, pn);
+  }
+  const int m0 = pm * BM, n0 = pn * BN;
+  const int wm = (wave >> 1) * T::WM, wn = (wave & 1) * T::WN;
+  const int r32 = lane & 31;
+
+  Work<OUT, BM, BN> w;
+  w.lds = lds;
+  w.ra = buffer_words(g.A.codes + (int64_t)m0 * g.A.ld);
+  w.rb = buffer_words(g.B.codes + (int64_t)n0 * g.B.ld);
+  {
+    const int r = wave * 8 + (lane >> 3);
+    w.piece = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    // rows past the end repeat the last one: their outputs are not stored
+#pragma unroll
+    for (int i = 0; i < T::LA; ++i) w.va[i] = (uint32_t)(min(32 * i + r, g.M - 1 - m0) * (int)g.A.ld) + w.piece;
+#pragma unroll
+    for (int i = 0; i < T::LB; ++i) w.vb[i] = (uint32_t)(min(32 * i + r, g.N - 1 - n0) * (int)g.B.ld) + w.piece;
+  }
+  w.lds_wave = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 1024);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) w.at[p] = r32 * kBK + (((2 * p + (lane >> 5)) ^ ((r32 >> 1) & 7)) << 4);
+  w.at_a = wm * kBK;
+  w.at_b = T::B_AT + wn * kBK;
+
+  // scales: 4 steps' bytes per word
+  const int nk = (g.K + kBK - 1) / kBK;
+  const uint8_t *psa[T::FM], *psb[T::FN];
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) psa[i] = g.A.scales + (int64_t)min(m0 + wm + 32 * i + r32, g.M - 1) * g.A.lds;
+#pragma unroll
+  for (int j = 0; j < T::FN; ++j)
+    psb[j] = g.B.scales + (int64_t)(min(n0 + wn + 32 * j + r32, g.N - 1) / g.b_block) * g.B.lds;
+
+  f32x16 acc[T::FM][T::FN] = {};
+  Slice<T> f0, f1;
+  if (nk > 0) {
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) w.sa[i] = *(const uint32_t*)psa[i];
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) w.sb[j] = *(const uint32_t*)psb[j];
+  }
+  // the tile's bias: a value per thread, parked until the end
+  float bias_v = 0.0f;
+  if (g.bias) {
+    const int e = tid + (g.bias_along_m ? m0 : n0);
+    if (tid < (g.bias_along_m ? BM : BN) && e < (g.bias_along_m ? g.M : g.N)) bias_v = widen(((const OUT*)g.bias)[e]);
+  }
+
+  constexpr int NL = T::LA + T::LB;
+  const int tail = g.K % kBK;
+  if (nk > 0) {
+    const uint32_t b0 = w.back(0, g.K);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) w.load(i, 0, b0, 0);
+    const uint32_t k1 = min(1, nk - 1) * kBK, b1 = w.back(k1, g.K);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) w.load(i, k1, b1, 1);
+    step_barrier();
+    if (tail && nk == 1) {
+      w.cut(lds, tail, 0, tid);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int x = 0; x < T::NR; ++x) w.read(x, 0, 0, f0);
+  }
+  uint32_t na[T::FM] = {}, nb[T::FN] = {};
+  for (int t = 0; t < nk; ++t) {
+    const int st = t & 1;
+    __builtin_amdgcn_sched_barrier(0);
+    if ((t & 3) == 0 && t + 4 < nk) {
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i) na[i] = *(const uint32_t*)(psa[i] + t + 4);
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) nb[j] = *(const uint32_t*)(psb[j] + t + 4);
+    }
+    multiply<OUT, BM, BN>(w, f0, acc, [&](int k, int N) {
+      IRIS_SHARE(x, T::NR, k, N) w.read(x, 1, st, f1);
+    });
+    // the matrix instructions above stay above (the compiler would move them
+    // behind the branch, and leave the unit idle here)
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    step_barrier();
+    if (tail && t + 2 == nk) {
+      w.cut(lds, tail, st ^ 1, tid);
+      __syncthreads();
+    }
+    // the scales that were loaded above are there: say so here, where it costs nothing
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) asm volatile("" : "+v"(na[i]));
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) asm volatile("" : "+v"(nb[j]));
+    __builtin_amdgcn_sched_barrier(0);
+    // the last two steps load the last step again: one loop body, 2 / nk more loads
+    const uint32_t k2 = min(t + 2, nk - 1) * kBK, b2 = w.back(k2, g.K);
+    multiply<OUT, BM, BN>(w, f1, acc, [&](int k, int N) {
+      IRIS_SHARE(i, NL, k, N) w.load(i, k2, b2, st);
+      IRIS_SHARE(x, T::NR, k, N) w.read(x, 0, st ^ 1, f0);
+    });
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) w.sa[i] = (t & 3) == 3 ? na[i] : w.sa[i] >> 8;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) w.sb[j] = (t & 3) == 3 ? nb[j] : w.sb[j] >> 8;
+  }
+
+  // Epilogue. The last loads have to land before the LDS is used again.
+  step_barrier();
+  float* const bl = (float*)lds;
+  bl[tid] = bias_v;
+  __syncthreads();
   // B is the first operand, so a lane holds row lane % 32 of each block and,
   // for q = 0..3, its columns 8 q + 4 (lane / 32) .. + 3
-  const OUT* bias = (const OUT*)g.bias;
+  const int h = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = m0 + wm + 32 * i + (lane & 31);
-    if (m >= g.M) continue;
-    OUT* crow = (OUT*)g.C + (int64_t)m * g.ldc;
+  for (int i = 0; i < T::FM; ++i) {
+    const int m = m0 + wm + 32 * i + r32;
+    OUT* const crow = (OUT*)g.C + (int64_t)m * g.ldc;
+    const float bm = g.bias_along_m ? bl[wm + 32 * i + r32] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < T::FN; ++j) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int n = n0 + wn + 32 * j + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if (n >= g.N) continue;
-        put_output(crow + n, acc[i][j][e], bias, g.bias_along_m ? m : n, g.accumulate);
+      for (int q = 0; q < 4; q += 2) {
+        const int c = wn + 32 * j + 8 * q;   // 16 columns: 4 in this lane, 4 in lane ^ 32, twice
+        float v[2][4];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          f32x4 bn = {bm, bm, bm, bm};
+          if (!g.bias_along_m) bn = *(const f32x4*)(bl + c + 8 * d + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[d][e] = acc[i][j][4 * (q + d) + e] + bn[e];
+        }
+        put_16(g, crow, m < g.M, n0 + c, h, v);
       }
+    }
   }
+}
+
+template <class OUT, int BM, int BN>
+hipError_t launch(const Fp8MmArgs& a, hipStream_t s) {
+  const int64_t tiles = ((int64_t)a.M + BM - 1) / BM * (((int64_t)a.N + BN - 1) / BN);
+  const int64_t round = kPatch * kXcds;
+  const uint32_t grid = (uint32_t)((tiles + round - 1) / round * round);
+  hipLaunchKernelGGL((fp8_mm_kernel<OUT, BM, BN>), dim3(grid), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, hipStream_t s) {
   if (a.M <= kFp8FewRows) return launch_fp8_mm_few(a, s);
-  const uint32_t grid = (uint32_t)(((int64_t)a.M + kTM - 1) / kTM * (((int64_t)a.N + kTN - 1) / kTN));
   switch (a.c_type) {
-    case T_FP16: hipLaunchKernelGGL((fp8_mm_kernel<f16>), dim3(grid), dim3(256), 0, s, a); break;
-    case T_BF16: hipLaunchKernelGGL((fp8_mm_kernel<bf16>), dim3(grid), dim3(256), 0, s, a); break;
-    default: hipLaunchKernelGGL((fp8_mm_kernel<float>), dim3(grid), dim3(256), 0, s, a); break;
+    case T_FP16: return launch<f16, 256, 256>(a, s);
+    case T_BF16: return launch<bf16, 256, 256>(a, s);
+    default: return launch<float, 256, 256>(a, s);
   }
-  return hipGetLastError();
 }
 
 }  // namespace iris

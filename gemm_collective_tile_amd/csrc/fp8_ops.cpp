@@ -156,13 +156,16 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   if (M < 0 || N < 0 || K < 0)
     return fail(IRIS_ERR_INVALID_ARG, "M, N, K must not be negative (got %lld, %lld, %lld)", (long long)M, (long long)N,
                 (long long)K);
-  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 30) || blocks(M) * blocks(N) >= ((int64_t)1 << 31))
-    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N, K <= 2^30 and fewer than 2^31 output blocks)");
+  // the kernels address a tile's rows of codes with 32-bit offsets
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 21) || blocks(M) * blocks(N) > (1 << 30))
+    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N <= 2^30, K <= 2^21, 2^30 output blocks)");
   if (flags & ~(IRIS_FLAG_BIAS_ALONG_M | IRIS_FLAG_ACCUMULATE))
     return fail(IRIS_ERR_CONFIG, "unknown flag bits 0x%x", flags);
   if ((st = check_plain(C, c_type, true, ldc, M, N, "C")) || (st = check_blocks1(A, M, K, "A")) ||
       (st = check_fp8(B, N, K, "B")))
     return st;
+  if ((M > 0 && K > 0 && A->ld > (1 << 22)) || (N > 0 && K > 0 && B->ld > (1 << 22)))
+    return fail(IRIS_ERR_UNSUPPORTED, "row pitch of codes too large (limit 2^22)");
   if (M > 0 && K > 0 && ((uintptr_t)A->scales % 4 != 0 || A->ld_scales % 4 != 0))
     return fail(IRIS_ERR_ALIGNMENT, "A: scales must be 4-byte aligned and ld_scales a multiple of 4");
   if (N > 0 && K > 0 && ((uintptr_t)B->scales % 4 != 0 || B->ld_scales % 4 != 0))
@@ -180,6 +183,7 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   a.C = C;
   a.c_type = c_type;
   a.ldc = ldc;
+  a.vec = rows16(C, ldc, c_type);
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
