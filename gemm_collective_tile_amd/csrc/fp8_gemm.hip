@@ -25,16 +25,26 @@
 // Design (4 waves, 2 x 2, each a (BM/2) x (BN/2) part of the tile in 32-bit
 // accumulators):
 //   * K is walked in steps of 128 bytes per row. Rows go from memory straight
-//     into one of two LDS stages (no registers in between: the accumulators
-//     and one step's operands fill the file), 8 lanes to a row's 128 bytes,
-//     the 16-byte pieces permuted by the row so that the operand reads of 16
-//     rows' same pieces meet 16 different bank groups.
+//     into LDS (no registers in between: the accumulators and one step's
+//     operands fill the file), 8 lanes to a row's 128 bytes, the 16-byte pieces
+//     permuted by the row so that the operand reads of 16 rows' same pieces
+//     meet 16 different bank groups.
 //   * A step has two slices of 64. While slice 0 multiplies, slice 1's
-//     operands are read. Then every wave has this stage in registers, one
-//     barrier says so, and while slice 1 multiplies, the loads of the step
-//     after the next go into this stage and slice 0 of the next step is read
-//     from the other one. A load has more than a step's time (0.9 us at 256 x
-//     256) to arrive, and no operand read is waited for.
+//     operands are read. Then every wave has this step in registers, one
+//     barrier says so, and while slice 1 multiplies, slice 0 of the next step
+//     is read. No operand read is waited for.
+//   * A has three LDS stages and B two (all of the 160 KB at 256 x 256), so that
+//     half of a step's loads, A's for the step after the next, go out beside
+//     slice 0 and the other half, B's, beside slice 1: all of them beside one
+//     slice is what a CU's load path can take at most, and the waves then
+//     wait to issue them. A load has half a step or more to arrive.
+//   * The 32 tiles of an XCD's patch share their rows through its L2, but in
+//     step they would all wait for the same lines' first fetch, and a CU's load
+//     path, which returns in order, would be full of waiting loads. So within
+//     every four steps of k the tiles of a row (and of a column) of the patch
+//     start at different ones: each fetches a quarter first and finds the
+//     others' quarters in L2. 8192^3: 505 -> 438 us on MI355X; with eight steps
+//     449, with sixteen 506 (the patch's rows no longer stay in L2).
 //   * The loads into LDS are written as assembly, because the compiler would
 //     wait for all of them at the next LDS read.
 #include "fp8.hpp"
@@ -69,7 +79,7 @@ struct Tile {
   static constexpr int WM = BM / 2, WN = BN / 2;       // a wave's part
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int A_STAGE = BM * kBK, B_STAGE = BN * kBK;
-  static constexpr int B_AT = 2 * A_STAGE;             // LDS: [A stages | B stages]
+  static constexpr int B_AT = 3 * A_STAGE;             // LDS: [A stages | B stages]
   static constexpr int LDS = B_AT + 2 * B_STAGE;
   static constexpr int LA = BM / 32, LB = BN / 32;     // loads of 1 KB per wave and step
   static constexpr int NM = FM * FN;                   // 32 x 32 blocks per wave
@@ -96,51 +106,51 @@ struct Work {
   uint32_t at_a, at_b;                // that part of stage 0
   uint32_t sa[T::FM], sb[T::FN];      // scale bytes of the coming steps, the present one lowest
 
-  // Load `item` of a step. In a ragged last step the pieces past the row's
-  // last one read that one again (`back` bytes before their place).
-  __device__ __forceinline__ void load(int item, uint32_t k, uint32_t back, int stage) const {
-    if (item < T::LA)
-      buffer_to_lds(ra, va[item < T::LA ? item : 0] - back, k, lds_wave + stage * T::A_STAGE + item * 32 * kBK);
-    else
-      buffer_to_lds(rb, vb[item < T::LA ? 0 : item - T::LA] - back, k,
-                    lds_wave + T::B_AT + stage * T::B_STAGE + (item - T::LA) * 32 * kBK);
+  // Load `item` of a step's A or B rows into the stage at `to`. In a ragged last
+  // step the pieces past the row's last one read that one again (`back` bytes
+  // before their place).
+  __device__ __forceinline__ void load_a(int item, uint32_t k, uint32_t back, uint32_t to) const {
+    buffer_to_lds(ra, va[item] - back, k, lds_wave + to + item * 32 * kBK);
+  }
+  __device__ __forceinline__ void load_b(int item, uint32_t k, uint32_t back, uint32_t to) const {
+    buffer_to_lds(rb, vb[item] - back, k, lds_wave + T::B_AT + to + item * 32 * kBK);
   }
   __device__ __forceinline__ uint32_t back(uint32_t k, int K) const {
     return (uint32_t)max(0, (int)(k + piece + 16) - ((K + 15) & ~15));
   }
-  // Zeros for the bytes past K of a ragged last step that has landed in `stage`
-  __device__ __forceinline__ void cut(char* l, int tail, int stage, int tid) const {
+  // Zeros for the bytes past K of a ragged last step that has landed in these stages
+  __device__ __forceinline__ void cut(char* l, int tail, uint32_t a_at, uint32_t b_at, int tid) const {
     const int r = tid >> 3, p = tid & 7, valid = tail - 16 * p;
     if (valid < 16) {
       char* const at0 = l + r * kBK + ((p ^ ((r >> 1) & 7)) << 4);
 #pragma unroll
       for (int i = 0; i < T::LA; ++i) {
-        u32x4* const q = (u32x4*)(at0 + stage * T::A_STAGE + i * 32 * kBK);
+        u32x4* const q = (u32x4*)(at0 + a_at + i * 32 * kBK);
         *q = keep_bytes(*q, valid);
       }
 #pragma unroll
       for (int i = 0; i < T::LB; ++i) {
-        u32x4* const q = (u32x4*)(at0 + T::B_AT + stage * T::B_STAGE + i * 32 * kBK);
+        u32x4* const q = (u32x4*)(at0 + T::B_AT + b_at + i * 32 * kBK);
         *q = keep_bytes(*q, valid);
       }
     }
   }
 
   // operand read X of slice s: a0, b0 .. b(FN-1), a1 .., the two pieces of each in turn
-  __device__ __forceinline__ void read(int x, int s, int stage, Slice<T>& f) const {
+  __device__ __forceinline__ void read(int x, int s, uint32_t a_at, uint32_t b_at, Slice<T>& f) const {
     const int item = x / 2, h = x & 1;
     if (item == 0 || item > T::FN) {
       const int i = item == 0 ? 0 : item - T::FN;
-      f.a[i][h] = *(const u32x4*)(lds + (at_a + stage * T::A_STAGE + at[2 * s + h]) + i * 32 * kBK);
+      f.a[i][h] = *(const u32x4*)(lds + (at_a + a_at + at[2 * s + h]) + i * 32 * kBK);
     } else {
-      f.b[item - 1][h] = *(const u32x4*)(lds + (at_b + stage * T::B_STAGE + at[2 * s + h]) + (item - 1) * 32 * kBK);
+      f.b[item - 1][h] = *(const u32x4*)(lds + (at_b + b_at + at[2 * s + h]) + (item - 1) * 32 * kBK);
     }
   }
 };
 
 // multiplies one slice; `other` is what is done beside it, in n shares
 template <class OUT, int BM, int BN, class F>
-__device__ __forceinline__ void multiply(const Work<OUT, BM, BN>& w, const Slice<Tile<BM, BN>>& f,
+__device__ __forceinline__ void multiply(Work<OUT, BM, BN>& w, const Slice<Tile<BM, BN>>& f,
                                          f32x16 (&acc)[Tile<BM, BN>::FM][Tile<BM, BN>::FN], F other) {
   using T = Tile<BM, BN>;
   if constexpr (!Work<OUT, BM, BN>::EXACT) {
@@ -175,9 +185,10 @@ __device__ __forceinline__ void multiply(const Work<OUT, BM, BN>& w, const Slice
   }
 }
 
-// everything that this wave read and loaded is there, in all waves
+// in all waves: everything read is in registers, and at most the last N loads are under way
+template <int N>
 __device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // The 16 columns n .. n + 15 of a row that lanes l and l ^ 32 hold between them:
@@ -227,6 +238,13 @@ __device__ __forceinline__ void put_16(const Fp8MmArgs& g, OUT* crow, bool on, i
       }
   }
 }
+
+__device__ __forceinline__ uint32_t rotate(uint32_t word, uint32_t bits) {
+  return __builtin_amdgcn_alignbit(word, word, bits);
+}
+
+// a where the mask has ones: no branch between the matrix instructions
+__device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
 
 // shares [k n / N, (k + 1) n / N) of n things over N places
 #define IRIS_SHARE(x, n, k, N) for (int x = (k) * (n) / (N); x < ((k) + 1) * (n) / (N); ++x)
@@ -278,12 +296,6 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
 
   f32x16 acc[T::FM][T::FN] = {};
   Slice<T> f0, f1;
-  if (nk > 0) {
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i) w.sa[i] = *(const uint32_t*)psa[i];
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j) w.sb[j] = *(const uint32_t*)psb[j];
-  }
   // the tile's bias: a value per thread, parked until the end
   float bias_v = 0.0f;
   if (g.bias) {
@@ -291,26 +303,45 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
     if (tid < (g.bias_along_m ? BM : BN) && e < (g.bias_along_m ? g.M : g.N)) bias_v = widen(((const OUT*)g.bias)[e]);
   }
 
-  constexpr int NL = T::LA + T::LB;
   const int tail = g.K % kBK;
+  // Where step t stands in the row: within each four whole steps, tiles that
+  // share rows start at different ones. Steps past the last load the last one
+  // again, so that the count of loads under way is the same in every step.
+  const int turn = (pm + pn) & 3, nkf = g.K / kBK;
+  const auto at_k = [&](int t) {
+    t = min(t, nk - 1);
+    return (uint32_t)((t | 3) < nkf ? (t & ~3) | ((t + turn) & 3) : t) * kBK;
+  };
+  // the scale bytes of the four steps from t on, in that order
+  const auto turn_bits = [&](int t) { return (t | 3) < nkf ? 8 * turn : 0; };
   if (nk > 0) {
-    const uint32_t b0 = w.back(0, g.K);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) w.load(i, 0, b0, 0);
-    const uint32_t k1 = min(1, nk - 1) * kBK, b1 = w.back(k1, g.K);
+    for (int i = 0; i < T::FM; ++i) w.sa[i] = rotate(*(const uint32_t*)psa[i], turn_bits(0));
 #pragma unroll
-    for (int i = 0; i < NL; ++i) w.load(i, k1, b1, 1);
-    step_barrier();
+    for (int j = 0; j < T::FN; ++j) w.sb[j] = rotate(*(const uint32_t*)psb[j], turn_bits(0));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t k = at_k(t), back = w.back(k, g.K);
+#pragma unroll
+      for (int i = 0; i < T::LA; ++i) w.load_a(i, k, back, t * T::A_STAGE);
+#pragma unroll
+      for (int i = 0; i < T::LB; ++i) w.load_b(i, k, back, t * T::B_STAGE);
+    }
+    step_barrier<T::LA + T::LB>();
     if (tail && nk == 1) {
-      w.cut(lds, tail, 0, tid);
+      w.cut(lds, tail, 0, 0, tid);
       __syncthreads();
     }
 #pragma unroll
-    for (int x = 0; x < T::NR; ++x) w.read(x, 0, 0, f0);
+    for (int x = 0; x < T::NR; ++x) w.read(x, 0, 0, 0, f0);
   }
   uint32_t na[T::FM] = {}, nb[T::FN] = {};
+  uint32_t a_this = 0, a_next = T::A_STAGE, a_free = 2 * T::A_STAGE;
   for (int t = 0; t < nk; ++t) {
-    const int st = t & 1;
+    const uint32_t b_this = t & 1 ? T::B_STAGE : 0, b_next = T::B_STAGE - b_this;
+    const uint32_t k2 = at_k(t + 2), back = w.back(k2, g.K);
+    const uint32_t new_word = (t & 3) == 3 ? ~0u : 0u;
+    const uint32_t bits = turn_bits(t + 1);
     __builtin_amdgcn_sched_barrier(0);
     if ((t & 3) == 0 && t + 4 < nk) {
 #pragma unroll
@@ -319,7 +350,8 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
       for (int j = 0; j < T::FN; ++j) nb[j] = *(const uint32_t*)(psb[j] + t + 4);
     }
     multiply<OUT, BM, BN>(w, f0, acc, [&](int k, int N) {
-      IRIS_SHARE(x, T::NR, k, N) w.read(x, 1, st, f1);
+      IRIS_SHARE(i, T::LA, k, N) w.load_a(i, k2, back, a_free);
+      IRIS_SHARE(x, T::NR, k, N) w.read(x, 1, a_this, b_this, f1);
     });
     // the matrix instructions above stay above (the compiler would move them
     // behind the branch, and leave the unit idle here)
@@ -327,9 +359,9 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
     for (int i = 0; i < T::FM; ++i)
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) asm volatile("" : "+a"(acc[i][j]));
-    step_barrier();
+    step_barrier<T::LA>();
     if (tail && t + 2 == nk) {
-      w.cut(lds, tail, st ^ 1, tid);
+      w.cut(lds, tail, a_next, b_next, tid);
       __syncthreads();
     }
     // the scales that were loaded above are there: say so here, where it costs nothing
@@ -338,20 +370,26 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) asm volatile("" : "+v"(nb[j]));
     __builtin_amdgcn_sched_barrier(0);
-    // the last two steps load the last step again: one loop body, 2 / nk more loads
-    const uint32_t k2 = min(t + 2, nk - 1) * kBK, b2 = w.back(k2, g.K);
     multiply<OUT, BM, BN>(w, f1, acc, [&](int k, int N) {
-      IRIS_SHARE(i, NL, k, N) w.load(i, k2, b2, st);
-      IRIS_SHARE(x, T::NR, k, N) w.read(x, 0, st ^ 1, f0);
+      IRIS_SHARE(i, T::LB, k, N) w.load_b(i, k2, back, b_this);
+      IRIS_SHARE(x, T::NR, k, N) w.read(x, 0, a_next, b_next, f0);
+      // the next step's scale bytes, each behind its last use
+      const int last = k - (N - T::NM);
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+        if (last == (i + 1) * T::FN - 1) w.sa[i] = choose(new_word, rotate(na[i], bits), w.sa[i] >> 8);
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+        if (last == T::NM - 1) w.sb[j] = choose(new_word, rotate(nb[j], bits), w.sb[j] >> 8);
     });
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i) w.sa[i] = (t & 3) == 3 ? na[i] : w.sa[i] >> 8;
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j) w.sb[j] = (t & 3) == 3 ? nb[j] : w.sb[j] >> 8;
+    const uint32_t a_was = a_this;
+    a_this = a_next;
+    a_next = a_free;
+    a_free = a_was;
   }
 
   // Epilogue. The last loads have to land before the LDS is used again.
-  step_barrier();
+  step_barrier<0>();
   float* const bl = (float*)lds;
   bl[tid] = bias_v;
   __syncthreads();
