@@ -50,19 +50,20 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   return amax_bits == 0 ? 127u : (uint32_t)(e < 1 ? 1 : e);
 }
-// 2^(127 - s): s is in [1, 247], so this is a normal number
-__device__ __forceinline__ float scale_inverse(uint32_t s) { return __builtin_bit_cast(float, (254u - s) << 23); }
 // 2^(s - 127) for any byte a caller may pass (0: 2^-127, subnormal; 255: NaN)
 __device__ __forceinline__ float scale_value(uint32_t s) {
   return __builtin_bit_cast(float, s == 0 ? 0x00400000u : (s == 255 ? 0x7fc00000u : s << 23));
 }
 
-// Four values, already divided by their scale, to four e4m3 codes, each
-// rounded to nearest even (v_cvt_pk_fp8_f32; values beyond the format, which
-// are only infinities and NaN here, give NaN codes).
-__device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+// Four values over their scale (a power of two), to four e4m3 codes, each
+// rounded to nearest even (v_cvt_scalef32_pk_fp8_f32 divides and rounds at
+// once; |value / scale| <= 448 but for infinities and NaN, which give NaN codes).
+__device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d, float scale) {
+  typedef short i16x2 __attribute__((ext_vector_type(2)));
+  i16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, w);
 }
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -87,46 +88,69 @@ __device__ __forceinline__ void narrow(float v, bf16& o) {
   o.bits = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// C consecutive values of a row starting at p, widened; those from `valid` on
-// read as 0. `vec`: p is 16-byte aligned whenever the piece is whole.
-template <int C, class T>
-__device__ __forceinline__ void load_piece(const T* p, int valid, bool vec, float (&v)[C]) {
-  if (vec && valid >= C) {
-    constexpr int W = C * (int)sizeof(T) / 16;
-    static_assert(W >= 1, "piece shorter than a 16-byte load");
-    u32x4 w[W];
+// C consecutive values of a row, as they came. WHOLE: the row's pieces are whole
+// and 16-byte aligned; otherwise they are read value by value. A piece at
+// `col` has its values from cols - col on as zeros; nothing past the row's
+// last value is read. `row` is the offset of the row's first value from `x`.
+template <class T, int C>
+struct Piece {
+  T t[C];
+  __device__ __forceinline__ float value(int i) const { return widen(t[i]); }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const T* x, uint32_t row, int col, int cols, bool on) {
+    if constexpr (WHOLE) {
+      // a piece that is off reads another one of the row and drops it: no
+      // branch between the loads
+      constexpr int W = C * (int)sizeof(T) / 16;
+      static_assert(W >= 1, "piece shorter than a 16-byte load");
+      on = on && col < cols;
+      const uint32_t at = (row + (col < cols ? col : 0)) * (uint32_t)sizeof(T);
+      u32x4 w[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = ld16((const char*)p + 16 * i);
-    T t[C];
-    __builtin_memcpy(t, w, sizeof t);
+      for (int i = 0; i < W; ++i) w[i] = ld16((const char*)x + at + 16 * i);
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = widen(t[i]);
-  } else {
+      for (int i = 0; i < W; ++i)
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = i < valid ? widen(p[i]) : 0.0f;
-  }
-}
-
-// C consecutive codes (C = 8 or 16) times their scale. Rows of codes start at
-// multiples of 16 bytes and pieces at multiples of C, so a whole piece is one
-// load; past `valid` no byte is read.
-template <int C>
-__device__ __forceinline__ void load_codes(const uint8_t* p, int valid, float scale, float (&v)[C]) {
-  uint32_t w[C / 4];
-  if (valid >= C) {
-    if constexpr (C == 16)
-      *(u32x4*)w = *(const u32x4*)p;
-    else
-      *(u32x2*)w = *(const u32x2*)p;
-  } else {
+        for (int e = 0; e < 4; ++e) w[i][e] = on ? w[i][e] : 0u;
+      __builtin_memcpy(t, w, sizeof t);
+    } else {
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
-      w[i] = 0;
+      for (int i = 0; i < C; ++i) t[i] = x[row + min(col + i, cols - 1)];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (4 * i + b < valid) w[i] |= (uint32_t)p[4 * i + b] << (8 * b);
+      for (int i = 0; i < C; ++i) t[i] = on && col + i < cols ? t[i] : T{};
     }
   }
+};
+template <bool WHOLE, int C, class T>
+__device__ __forceinline__ void load_piece(const T* x, uint32_t row, int col, int cols, bool on, float (&v)[C]) {
+  Piece<T, C> p;
+  p.template load<WHOLE>(x, row, col, cols, on);
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] = p.value(i);
+}
+
+// C consecutive codes (C = 8 or 16). Rows of codes start at multiples of 16
+// bytes, which are allocated up to the next one, so a piece is one load. Codes
+// past the row's last one become zeros.
+template <bool WHOLE, int C>
+__device__ __forceinline__ void load_codes(const uint8_t* x, uint32_t row, int col, int cols, uint32_t (&w)[C / 4]) {
+  const uint8_t* p = x + (row + (col < cols ? col : 0));
+  if constexpr (C == 16)
+    *(u32x4*)w = *(const u32x4*)p;
+  else
+    *(u32x2*)w = *(const u32x2*)p;
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) {
+      const int n = cols - col - 4 * i;   // codes of this word inside the row
+      w[i] = n >= 4 ? w[i] : (n <= 0 ? 0u : w[i] & ((1u << (8 * n)) - 1u));
+    }
+  }
+}
+// their values. A scale of 0 drops the piece (but for NaN codes, which no
+// block's scale counts).
+template <int C>
+__device__ __forceinline__ void decode(const uint32_t (&w)[C / 4], float scale, float (&v)[C]) {
 #pragma unroll
   for (int i = 0; i < C / 4; ++i) {
     from_fp8x4(w[i], v + 4 * i);
@@ -135,42 +159,81 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int valid, float sc
   }
 }
 
-// C codes to row memory, no byte past `valid`
-template <int C>
-__device__ __forceinline__ void store_codes(uint8_t* p, int valid, const uint32_t (&w)[C / 4]) {
-  if (valid >= C) {
+// C codes to a row, none past its last column
+template <bool WHOLE, int C>
+__device__ __forceinline__ void store_codes(uint8_t* x, uint32_t row, int col, int cols, const uint32_t (&w)[C / 4]) {
+  if (WHOLE ? col < cols : col + C <= cols) {
     if constexpr (C == 16)
-      *(u32x4*)p = *(const u32x4*)w;
+      *(u32x4*)(x + (row + col)) = *(const u32x4*)w;
     else
-      *(u32x2*)p = *(const u32x2*)w;
-  } else {
+      *(u32x2*)(x + (row + col)) = *(const u32x2*)w;
+  } else if constexpr (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < C; ++i)
-      if (i < valid) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+      if (col + i < cols) x[row + col + i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
   }
 }
 
 template <int C>
-__device__ __forceinline__ void encode_piece(const float (&v)[C], float inv, uint32_t (&w)[C / 4]) {
+__device__ __forceinline__ void encode_piece(const float (&v)[C], float scale, uint32_t (&w)[C / 4]) {
 #pragma unroll
-  for (int i = 0; i < C / 4; ++i)
-    w[i] = to_fp8x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+  for (int i = 0; i < C / 4; ++i) w[i] = to_fp8x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], scale);
 }
+
+// Largest magnitudes, as bits. v_max3_f32 takes two values at once and their
+// magnitudes for free; an infinity (or a signalling NaN) leaves something that
+// is not finite, and only then are the values looked at one by one.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(m) : "v"(a), "v"(b));
+  return m;
+}
+constexpr uint32_t kInfBits = 0x7f800000u;
 
 template <int C>
 __device__ __forceinline__ uint32_t piece_amax(const float (&v)[C]) {
-  uint32_t m = 0;
+  float f = 0.0f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) m = max(m, finite_bits(v[i]));
+  for (int i = 0; i < C; i += 2) f = max_abs(f, v[i], v[i + 1]);
+  uint32_t m = __builtin_bit_cast(uint32_t, f);
+  if (__builtin_expect(m >= kInfBits, 0)) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) m = max(m, finite_bits(v[i]));
+  }
   return m;
 }
 
+// the larger of this lane's and another lane's
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t m) {
+  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t max_xor8(uint32_t m) { return max_dpp<0x128>(m); }  // row_ror:8
+__device__ __forceinline__ uint32_t max_xor16(uint32_t m) {
+  const auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  return max((uint32_t)r[0], (uint32_t)r[1]);
+}
+__device__ __forceinline__ uint32_t max_xor32(uint32_t m) {
+  const auto r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return max((uint32_t)r[0], (uint32_t)r[1]);
+}
 // the largest over each aligned group of N lanes, in all of them
 template <int N>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
-#pragma unroll
-  for (int d = 1; d < N; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  static_assert(N == 8 || N == 16 || N == 64, "");
+  m = max_dpp<0xb1>(m);    // lane ^ 1
+  m = max_dpp<0x4e>(m);    // lane ^ 2
+  m = max_dpp<0x141>(m);   // 7 - lane: the other four of eight
+  if constexpr (N >= 16) m = max_dpp<0x140>(m);  // 15 - lane
+  if constexpr (N == 64) m = max_xor32(max_xor16(m));
   return m;
+}
+// the largest over the lanes l, l + L, l + 2 L, ... of the wave
+template <int L>
+__device__ __forceinline__ uint32_t stride_max(uint32_t m) {
+  static_assert(L == 8 || L == 16, "");
+  if constexpr (L == 8) m = max_xor8(m);
+  return max_xor32(max_xor16(m));
 }
 
 // silu and its derivative from sigma(g) = 1 / (1 + 2^(-g log2 e)). v_exp_f32

@@ -35,6 +35,8 @@ int launched(hipError_t e, const char* what) {
 }
 
 constexpr int64_t kBlk = iris::kFp8Block;
+// the kernels address a tile's rows with 32-bit offsets
+constexpr int64_t kMaxPitch = 1 << 22;
 int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
 
 // rows and columns of a memory-bound operator: its grid numbers 128-wide
@@ -57,6 +59,8 @@ int check_fp8(const iris_fp8_t* q, int64_t rows, int64_t cols, const char* name)
   if ((uintptr_t)q->codes % 16 != 0 || q->ld % 16 != 0)
     return fail(IRIS_ERR_ALIGNMENT, "%s: codes must be 16-byte aligned and ld a multiple of 16 (ld %lld)", name,
                 (long long)q->ld);
+  if (q->ld > kMaxPitch || q->ld_scales > kMaxPitch)
+    return fail(IRIS_ERR_UNSUPPORTED, "%s: row pitch too large (limit 2^22)", name);
   if (q->ld < cols)
     return fail(IRIS_ERR_INVALID_ARG, "%s: ld %lld is shorter than the %lld columns", name, (long long)q->ld, (long long)cols);
   if (q->ld_scales < blocks(cols))
@@ -80,6 +84,7 @@ int check_plain(const void* x, int32_t type, bool fp32_too, int64_t ld, int64_t 
   if (rows == 0 || cols == 0) return IRIS_OK;
   if (!x) return fail(IRIS_ERR_INVALID_ARG, "%s is NULL", name);
   if ((uintptr_t)x % type_bytes(type) != 0) return fail(IRIS_ERR_ALIGNMENT, "%s is not aligned to its type", name);
+  if (ld > kMaxPitch) return fail(IRIS_ERR_UNSUPPORTED, "%s: row pitch too large (limit 2^22)", name);
   if (ld < cols)
     return fail(IRIS_ERR_INVALID_ARG, "%s: row pitch %lld is shorter than the %lld columns", name, (long long)ld, (long long)cols);
   return IRIS_OK;
@@ -156,7 +161,6 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   if (M < 0 || N < 0 || K < 0)
     return fail(IRIS_ERR_INVALID_ARG, "M, N, K must not be negative (got %lld, %lld, %lld)", (long long)M, (long long)N,
                 (long long)K);
-  // the kernels address a tile's rows of codes with 32-bit offsets
   if (M > (1 << 30) || N > (1 << 30) || K > (1 << 21) || blocks(M) * blocks(N) > (1 << 30))
     return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N <= 2^30, K <= 2^21, 2^30 output blocks)");
   if (flags & ~(IRIS_FLAG_BIAS_ALONG_M | IRIS_FLAG_ACCUMULATE))
@@ -164,8 +168,6 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   if ((st = check_plain(C, c_type, true, ldc, M, N, "C")) || (st = check_blocks1(A, M, K, "A")) ||
       (st = check_fp8(B, N, K, "B")))
     return st;
-  if ((M > 0 && K > 0 && A->ld > (1 << 22)) || (N > 0 && K > 0 && B->ld > (1 << 22)))
-    return fail(IRIS_ERR_UNSUPPORTED, "row pitch of codes too large (limit 2^22)");
   if (M > 0 && K > 0 && ((uintptr_t)A->scales % 4 != 0 || A->ld_scales % 4 != 0))
     return fail(IRIS_ERR_ALIGNMENT, "A: scales must be 4-byte aligned and ld_scales a multiple of 4");
   if (N > 0 && K > 0 && ((uintptr_t)B->scales % 4 != 0 || B->ld_scales % 4 != 0))

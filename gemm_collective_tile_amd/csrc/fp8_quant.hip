@@ -23,49 +23,48 @@ constexpr int kTile = 128;
 
 // blocks (row, kb) are numbered along the rows; 8 lanes work on each
 struct RowPlace {
-  int row, kb, col, valid;
+  int row, kb, col;
   bool on;
+  __device__ __forceinline__ RowPlace(int rows, FastDiv nkb) {
+    const uint32_t b = blockIdx.x * (kThreads / 8) + threadIdx.x / 8;
+    const int r = (int)nkb.div(b);
+    kb = (int)(b - (uint32_t)r * nkb.d);
+    col = kb * kFp8Block + 16 * (threadIdx.x & 7);
+    on = r < rows;
+    row = min(r, rows - 1);
+  }
 };
-__device__ __forceinline__ RowPlace row_place(int rows, int cols, FastDiv nkb) {
-  const uint32_t b = blockIdx.x * (kThreads / 8) + threadIdx.x / 8;
-  RowPlace p;
-  p.row = (int)nkb.div(b);
-  p.kb = (int)(b - (uint32_t)p.row * nkb.d);
-  p.col = p.kb * kFp8Block + 16 * (threadIdx.x & 7);
-  p.on = p.row < rows;
-  p.valid = p.on ? max(0, min(16, cols - p.col)) : 0;
-  return p;
-}
 
-__device__ __forceinline__ void put_row_block(const Fp8Mat& q, const RowPlace& p, const float (&v)[16]) {
+template <bool WHOLE>
+__device__ __forceinline__ void put_row_block(const Fp8Mat& q, const RowPlace& p, int cols, const float (&v)[16]) {
   const uint32_t s = scale_byte(group_max<8>(piece_amax(v)));
   uint32_t w[4];
-  encode_piece(v, scale_inverse(s), w);
+  encode_piece(v, scale_value(s), w);
   if (!p.on) return;
-  store_codes<16>(q.codes + (int64_t)p.row * q.ld + p.col, p.valid, w);
+  store_codes<WHOLE, 16>(q.codes + (int64_t)p.row * q.ld, 0, p.col, cols, w);
   if ((threadIdx.x & 7) == 0) q.scales[(int64_t)p.row * q.lds + p.kb] = (uint8_t)s;
 }
 
-template <class T>
+template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8QuantArgs a, FastDiv nkb) {
-  const RowPlace p = row_place(a.rows, a.cols, nkb);
+  const RowPlace p(a.rows, nkb);
   float v[16];
-  load_piece<16>((const T*)a.x + (int64_t)p.row * a.ldx + p.col, p.valid, a.vec, v);
-  put_row_block(a.q, p, v);
+  load_piece<WHOLE>((const T*)a.x + (int64_t)p.row * a.ldx, 0, p.col, a.cols, p.on, v);
+  put_row_block<WHOLE>(a.q, p, a.cols, v);
 }
 
-template <class T>
+template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void fp8_swiglu_kernel(Fp8SwigluArgs a, FastDiv nkb) {
-  const RowPlace p = row_place(a.rows, a.cols, nkb);
+  const RowPlace p(a.rows, nkb);
   float g[16], u[16], h[16];
-  load_piece<16>((const T*)a.gate + (int64_t)p.row * a.ld_gate + p.col, p.valid, a.vec, g);
-  load_piece<16>((const T*)a.up + (int64_t)p.row * a.ld_up + p.col, p.valid, a.vec, u);
+  load_piece<WHOLE>((const T*)a.gate + (int64_t)p.row * a.ld_gate, 0, p.col, a.cols, p.on, g);
+  load_piece<WHOLE>((const T*)a.up + (int64_t)p.row * a.ld_up, 0, p.col, a.cols, p.on, u);
 #pragma unroll
   for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
-  put_row_block(a.h, p, h);
+  put_row_block<WHOLE>(a.h, p, a.cols, h);
   if (a.gate8.codes) {
-    put_row_block(a.gate8, p, g);
-    put_row_block(a.up8, p, u);
+    put_row_block<WHOLE>(a.gate8, p, a.cols, g);
+    put_row_block<WHOLE>(a.up8, p, a.cols, u);
   }
 }
 
@@ -78,31 +77,34 @@ struct TilePlace {
   static constexpr int L = kTile / C;
   static constexpr int T = L * (kTile / 4);
   int r0, c0, ch, j;     // tile origin, piece and row group in it
-  int rows, cols;        // rows and columns of the tile inside the matrix
-  __device__ __forceinline__ TilePlace(int nrows, int ncols, FastDiv ncb) {
+  int nrows, ncols;      // of the matrix
+  __device__ __forceinline__ TilePlace(int nrows, int ncols, FastDiv ncb) : nrows(nrows), ncols(ncols) {
     const uint32_t rb = ncb.div(blockIdx.x);
     r0 = (int)rb * kTile;
     c0 = (int)(blockIdx.x - rb * ncb.d) * kTile;
     ch = threadIdx.x % L;
     j = threadIdx.x / L;
-    rows = min(kTile, nrows - r0);
-    cols = min(kTile, ncols - c0);
   }
-  __device__ __forceinline__ int row(int i) const { return r0 + 4 * j + i; }
-  __device__ __forceinline__ int col() const { return c0 + C * ch; }
-  // valid columns of this thread's piece in its row i
-  __device__ __forceinline__ int valid(int i) const {
-    return 4 * j + i < rows ? max(0, min(C, cols - C * ch)) : 0;
-  }
+  // row i of this thread (rows past the end read the last one), whether it is there
+  __device__ __forceinline__ uint32_t row(int i) const { return (uint32_t)min(4 * j + i, nrows - 1 - r0); }
+  __device__ __forceinline__ bool on(int i) const { return r0 + 4 * j + i < nrows; }
+  __device__ __forceinline__ int col() const { return C * ch; }
+  __device__ __forceinline__ int cols() const { return ncols - c0; }
+  // Addresses: the tile's corner, the same in all threads, and a 32-bit offset
+  // from it (pitches are under 2^22, so a tile's rows lie within 2^31 bytes)
+  template <class U>
+  __device__ __forceinline__ U* corner(U* x, int64_t ld) const { return x + (int64_t)r0 * ld + c0; }
+  __device__ __forceinline__ uint8_t* scales(const Fp8Mat& q) const { return q.scales + (int64_t)r0 * q.lds + c0 / kTile; }
 };
+__device__ __forceinline__ uint32_t offset(uint32_t row, int64_t ld) { return __umul24(row, (uint32_t)ld); }
 
 // LDS of a tile's turn: the transposed codes and the columns' scales
 template <int C>
 struct TileLds {
   static constexpr int WAVES = TilePlace<C>::T / 64;
   alignas(16) uint32_t turn[kTile][kTile / 4];  // [column][word of 4 rows], swizzled
-  uint32_t part[WAVES][kTile];      // a wave's largest magnitude of each column
-  float inv[kTile];
+  uint32_t part[WAVES][kTile];                  // a wave's largest magnitude of each column
+  alignas(16) float scale[kTile];
 };
 
 // The 16-byte pieces of a column's 128 transposed codes are permuted by the
@@ -113,31 +115,32 @@ __device__ __forceinline__ int turn_word(int col, int word) {
   return (((word >> 2) ^ (col / C)) & 7) * 4 + (word & 3);
 }
 
-// Writes the tile's transposed codes and scales. All threads of the workgroup
-// call it; starts and ends with the LDS free for the next use only after a
-// barrier of the caller's (it begins with one).
-// given >= 0: the scale byte of every block (128 x 128 blocks).
+// Writes the transposed codes and scales of a tile of values. All threads of
+// the workgroup call it; the LDS may be the one of an earlier call. given >= 0:
+// the scale byte of every block (128 x 128 blocks), already written.
 template <int C>
-__device__ void put_turned(const Fp8Mat& qt, const TilePlace<C>& p, const float (&v)[4][C], int given,
-                           TileLds<C>& lds) {
+__device__ __forceinline__ void put_turned(const Fp8Mat& qt, const TilePlace<C>& p, const float (&v)[4][C], int given,
+                                           TileLds<C>& lds) {
   constexpr int T = TilePlace<C>::T, L = TilePlace<C>::L;
   const int t = threadIdx.x;
-  __syncthreads();
-  float inv[C];
+  float s[C];
   if (given < 0) {
-    uint32_t m[C];
+    uint32_t m[C], top = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      m[c] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m[c] = max(m[c], finite_bits(v[i][c]));
+      m[c] = __builtin_bit_cast(uint32_t, max_abs(max_abs(0.0f, v[0][c], v[1][c]), v[2][c], v[3][c]));
+      top = max(top, m[c]);
     }
-    // over the wave's 64 / L row groups: lanes t, t + L, t + 2 L, ...
+    if (__builtin_expect(top >= kInfBits, 0)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < C; ++c) {
+        m[c] = 0;
 #pragma unroll
-      for (int d = L; d < 64; d *= 2) m[c] = max(m[c], (uint32_t)__shfl_xor((int)m[c], d));
+        for (int i = 0; i < 4; ++i) m[c] = max(m[c], finite_bits(v[i][c]));
+      }
     }
+#pragma unroll
+    for (int c = 0; c < C; ++c) m[c] = stride_max<L>(m[c]);
     if ((t & 63) < L) {
 #pragma unroll
       for (int c = 0; c < C; ++c) lds.part[t / 64][C * p.ch + c] = m[c];
@@ -147,69 +150,79 @@ __device__ void put_turned(const Fp8Mat& qt, const TilePlace<C>& p, const float 
       uint32_t a = 0;
 #pragma unroll
       for (int w = 0; w < TileLds<C>::WAVES; ++w) a = max(a, lds.part[w][t]);
-      const uint32_t s = scale_byte(a);
-      lds.inv[t] = scale_inverse(s);
-      if (t < p.cols) qt.scales[(int64_t)(p.c0 + t) * qt.lds + p.r0 / kTile] = (uint8_t)s;
+      const uint32_t b = scale_byte(a);
+      lds.scale[t] = scale_value(b);
+      if (t < p.cols()) qt.scales[(int64_t)p.c0 * qt.lds + p.r0 / kTile + offset(t, qt.lds)] = (uint8_t)b;
     }
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < C; ++c) inv[c] = lds.inv[C * p.ch + c];
+    for (int c = 0; c < C; ++c) s[c] = lds.scale[C * p.ch + c];
   } else {
 #pragma unroll
-    for (int c = 0; c < C; ++c) inv[c] = scale_inverse((uint32_t)given);
+    for (int c = 0; c < C; ++c) s[c] = scale_value((uint32_t)given);
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = C * p.ch + c;
-    lds.turn[col][turn_word<C>(col, p.j)] =
-        to_fp8x4(v[0][c] * inv[c], v[1][c] * inv[c], v[2][c] * inv[c], v[3][c] * inv[c]);
+    lds.turn[col][turn_word<C>(col, p.j)] = to_fp8x4(v[0][c], v[1][c], v[2][c], v[3][c], s[c]);
   }
   __syncthreads();
   // 8 lanes write the 128 codes of a column
+  const int piece = t % 8, valid = p.nrows - p.r0 - 16 * piece;
+  uint8_t* const corner = qt.codes + (int64_t)p.c0 * qt.ld + p.r0;
 #pragma unroll
-  for (int n = 0; n < kTile * 8 / T; ++n) {
-    const int col = n * (T / 8) + t / 8, piece = t % 8;
-    uint32_t w[4];
-    *(u32x4*)w = *(const u32x4*)&lds.turn[col][turn_word<C>(col, 4 * piece)];
-    if (col < p.cols)
-      store_codes<16>(qt.codes + (int64_t)(p.c0 + col) * qt.ld + p.r0 + 16 * piece, max(0, min(16, p.rows - 16 * piece)), w);
+  for (int k = 0; k < kTile * 8 / T; ++k) {
+    const int col = k * (T / 8) + t / 8;
+    const uint32_t* const w = &lds.turn[col][turn_word<C>(col, 4 * piece)];
+    if (col >= p.cols()) continue;
+    uint8_t* const to = corner + (offset(col, qt.ld) + 16 * piece);
+    if (valid >= 16) {
+      *(u32x4*)to = *(const u32x4*)w;
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < valid; ++i) to[i] = ((const uint8_t*)w)[i];
+    }
   }
 }
 
 // a thread's four row pieces, blocks along the rows
-template <int C>
+template <bool WHOLE, int C>
 __device__ __forceinline__ void put_rows(const Fp8Mat& q, const TilePlace<C>& p, const float (&v)[4][C], int given) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t s =
         given < 0 ? scale_byte(group_max<TilePlace<C>::L>(piece_amax(v[i]))) : (uint32_t)given;
     uint32_t w[C / 4];
-    encode_piece(v[i], scale_inverse(s), w);
-    const int valid = p.valid(i);
-    if (4 * p.j + i < p.rows) {
-      store_codes<C>(q.codes + (int64_t)p.row(i) * q.ld + p.col(), valid, w);
-      if (given < 0 && p.ch == 0) q.scales[(int64_t)p.row(i) * q.lds + p.c0 / kTile] = (uint8_t)s;
+    encode_piece(v[i], scale_value(s), w);
+    if (p.on(i)) {
+      store_codes<WHOLE, C>(p.corner(q.codes, q.ld), offset(p.row(i), q.ld), p.col(), p.cols(), w);
+      if (given < 0 && p.ch == 0) p.scales(q)[offset(p.row(i), q.lds)] = (uint8_t)s;
     }
   }
 }
 
 // x -> rows and / or columns, or 128 x 128 blocks
-template <class T>
+template <class T, bool WHOLE>
 __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv ncb) {
   constexpr int C = 16;
   __shared__ TileLds<C> lds;
   const TilePlace<C> p(a.rows, a.cols, ncb);
   float v[4][C];
+  if constexpr (sizeof(T) == 1) {
+    uint32_t w[4][C / 4];
+    float s[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int valid = p.valid(i);
-    if constexpr (sizeof(T) == 1) {
-      float s = 0.0f;
-      if (valid > 0) s = scale_value(a.x8.scales[(int64_t)p.row(i) * a.x8.lds + p.c0 / kTile]);
-      load_codes<C>(a.x8.codes + (int64_t)p.row(i) * a.x8.ld + p.col(), valid, s, v[i]);
-    } else {
-      load_piece<C>((const T*)a.x + (int64_t)p.row(i) * a.ldx + p.col(), valid, a.vec, v[i]);
+    for (int i = 0; i < 4; ++i) {
+      load_codes<WHOLE, C>(p.corner(a.x8.codes, a.x8.ld), offset(p.row(i), a.x8.ld), p.col(), p.cols(), w[i]);
+      const uint8_t b = p.scales(a.x8)[offset(p.row(i), a.x8.lds)];
+      s[i] = p.on(i) && p.col() < p.cols() ? scale_value(b) : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) decode<C>(w[i], s[i], v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_piece<WHOLE>(p.corner((const T*)a.x, a.ldx), offset(p.row(i), a.ldx), p.col(), p.cols(), p.on(i), v[i]);
   }
   int given = -1;
   if (a.block == kTile) {
@@ -227,95 +240,149 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv n
       if (a.qt.codes) a.qt.scales[(int64_t)(p.c0 / kTile) * a.qt.lds + p.r0 / kTile] = (uint8_t)given;
     }
   }
-  if (a.q.codes) put_rows<C>(a.q, p, v, given);
+  if (a.q.codes) put_rows<WHOLE>(a.q, p, v, given);
   if (a.qt.codes) put_turned<C>(a.qt, p, v, given, lds);
 }
 
 // With s = sigma(g):  h = g s u,  dgate = dh u s (1 + g (1 - s)),  dup = dh g s,
-// at the kept 8-bit g and u. Three values per entry stay in registers until
-// both directions of blocks have their codes.
-template <class T>
-__global__ __launch_bounds__(512) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
+// at the kept 8-bit g and u. The inputs stay in registers as they came (64
+// bytes a thread) beside s; the three results are formed one after the other,
+// so that 4 waves fit a SIMD (all three at once: 182 registers, 2 waves).
+template <class T, bool WHOLE>
+__global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
   constexpr int C = 8;
   __shared__ TileLds<C> lds;
   const TilePlace<C> p(a.rows, a.cols, ncb);
-  float dg[4][C], du[4][C], h[4][C];
+  Piece<T, C> d[4];
+  uint32_t gw[4][C / 4], uw[4][C / 4];
+  float sg[4], su[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int valid = p.valid(i);
-    const int64_t row = p.row(i);
-    float sg = 0.0f, su = 0.0f;
-    if (valid > 0) {
-      sg = scale_value(a.gate8.scales[row * a.gate8.lds + p.c0 / kTile]);
-      su = scale_value(a.up8.scales[row * a.up8.lds + p.c0 / kTile]);
-    }
-    float d[C], g[C], u[C];
-    load_piece<C>((const T*)a.dh + row * a.ld_dh + p.col(), valid, a.vec, d);
-    load_codes<C>(a.gate8.codes + row * a.gate8.ld + p.col(), valid, sg, g);
-    load_codes<C>(a.up8.codes + row * a.up8.ld + p.col(), valid, su, u);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float s = sigmoid(g[c]), silu = g[c] * s;
-      dg[i][c] = d[c] * u[c] * (s * (1.0f + g[c] * (1.0f - s)));
-      du[i][c] = d[c] * silu;
-      h[i][c] = silu * u[c];
-    }
+    const uint32_t row = p.row(i);
+    const bool on = p.on(i) && p.col() < p.cols();
+    d[i].template load<WHOLE>(p.corner((const T*)a.dh, a.ld_dh), offset(row, a.ld_dh), p.col(), p.cols(), on);
+    load_codes<WHOLE, C>(p.corner(a.gate8.codes, a.gate8.ld), offset(row, a.gate8.ld), p.col(), p.cols(), gw[i]);
+    load_codes<WHOLE, C>(p.corner(a.up8.codes, a.up8.ld), offset(row, a.up8.ld), p.col(), p.cols(), uw[i]);
+    const uint8_t bg = p.scales(a.gate8)[offset(row, a.gate8.lds)];
+    const uint8_t bu = p.scales(a.up8)[offset(row, a.up8.lds)];
+    sg[i] = on ? scale_value(bg) : 0.0f;
+    su[i] = on ? scale_value(bu) : 0.0f;
   }
-  put_rows<C>(a.dgate, p, dg, -1);
-  put_rows<C>(a.dup, p, du, -1);
-  if (a.dgate_t.codes) put_turned<C>(a.dgate_t, p, dg, -1, lds);
-  if (a.dup_t.codes) put_turned<C>(a.dup_t, p, du, -1, lds);
-  if (a.h_t.codes) put_turned<C>(a.h_t, p, h, -1, lds);
+  float s[4][C];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float g[C];
+    decode<C>(gw[i], sg[i], g);
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[i][c] = sigmoid(g[c]);
+  }
+  // decode again where it is needed, instead of keeping all of it
+  const auto forget = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < C / 4; ++k) asm volatile("" : "+v"(gw[i][k]), "+v"(uw[i][k]));
+  };
+  forget();
+  {
+    float v[4][C];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float g[C], u[C];
+      decode<C>(gw[i], sg[i], g);
+      decode<C>(uw[i], su[i], u);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        v[i][c] = d[i].value(c) * u[c] * (s[i][c] * (1.0f + g[c] * (1.0f - s[i][c])));
+    }
+    put_rows<WHOLE>(a.dgate, p, v, -1);
+    if (a.dgate_t.codes) put_turned<C>(a.dgate_t, p, v, -1, lds);
+  }
+  forget();
+  {
+    float v[4][C];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float g[C];
+      decode<C>(gw[i], sg[i], g);
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[i][c] = d[i].value(c) * (g[c] * s[i][c]);
+    }
+    put_rows<WHOLE>(a.dup, p, v, -1);
+    if (a.dup_t.codes) put_turned<C>(a.dup_t, p, v, -1, lds);
+  }
+  forget();
+  if (a.h_t.codes) {
+    float v[4][C];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float g[C], u[C];
+      decode<C>(gw[i], sg[i], g);
+      decode<C>(uw[i], su[i], u);
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[i][c] = g[c] * s[i][c] * u[c];
+    }
+    put_turned<C>(a.h_t, p, v, -1, lds);
+  }
 }
 
 uint32_t blocks_of(int n) { return (uint32_t)((n + kFp8Block - 1) / kFp8Block); }
+
+// Values, types and whether all pieces of 16 are whole and aligned choose the kernel.
+template <bool WHOLE>
+hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
+  const uint32_t nkb = blocks_of(a.cols);
+  const FastDiv d = FastDiv::make(nkb);
+  if (a.block == 1 && !a.qt.codes) {
+    const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads)), block(kThreads);
+    switch (a.x_type) {
+      case T_FP16: hipLaunchKernelGGL((fp8_rows_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
+      case T_BF16: hipLaunchKernelGGL((fp8_rows_kernel<bf16, WHOLE>), grid, block, 0, s, a, d); break;
+      default: hipLaunchKernelGGL((fp8_rows_kernel<float, WHOLE>), grid, block, 0, s, a, d); break;
+    }
+    return hipGetLastError();
+  }
+  const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<16>::T);
+  switch (a.x_type) {
+    case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
+    case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16, WHOLE>), grid, block, 0, s, a, d); break;
+    case T_FP32: hipLaunchKernelGGL((fp8_tile_kernel<float, WHOLE>), grid, block, 0, s, a, d); break;
+    default: hipLaunchKernelGGL((fp8_tile_kernel<uint8_t, WHOLE>), grid, block, 0, s, a, d); break;
+  }
+  return hipGetLastError();
+}
+
+template <class T, bool WHOLE>
+hipError_t swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
+  const uint32_t nkb = blocks_of(a.cols);
+  const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads));
+  hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE>), grid, dim3(kThreads), 0, s, a, FastDiv::make(nkb));
+  return hipGetLastError();
+}
+
+template <class T, bool WHOLE>
+hipError_t swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
+  const uint32_t nkb = blocks_of(a.cols);
+  hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(blocks_of(a.rows) * nkb), dim3(TilePlace<8>::T), 0, s, a,
+                     FastDiv::make(nkb));
+  return hipGetLastError();
+}
 
 }  // namespace
 
 // The host has checked that rows * blocks and the tiles fit 31 bits.
 hipError_t launch_fp8_quantize(const Fp8QuantArgs& a, hipStream_t s) {
-  const uint32_t nkb = blocks_of(a.cols);
-  if (a.block == 1 && !a.qt.codes) {
-    const FastDiv d = FastDiv::make(nkb);
-    const uint32_t grid = (uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads);
-    switch (a.x_type) {
-      case T_FP16: hipLaunchKernelGGL((fp8_rows_kernel<f16>), dim3(grid), dim3(kThreads), 0, s, a, d); break;
-      case T_BF16: hipLaunchKernelGGL((fp8_rows_kernel<bf16>), dim3(grid), dim3(kThreads), 0, s, a, d); break;
-      default: hipLaunchKernelGGL((fp8_rows_kernel<float>), dim3(grid), dim3(kThreads), 0, s, a, d); break;
-    }
-    return hipGetLastError();
-  }
-  const FastDiv d = FastDiv::make(nkb);
-  const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<16>::T);
-  switch (a.x_type) {
-    case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16>), grid, block, 0, s, a, d); break;
-    case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16>), grid, block, 0, s, a, d); break;
-    case T_FP32: hipLaunchKernelGGL((fp8_tile_kernel<float>), grid, block, 0, s, a, d); break;
-    default: hipLaunchKernelGGL((fp8_tile_kernel<uint8_t>), grid, block, 0, s, a, d); break;
-  }
-  return hipGetLastError();
+  return (a.x_type == T_FP8 || a.vec) && a.cols % 16 == 0 ? quantize<true>(a, s) : quantize<false>(a, s);
 }
 
 hipError_t launch_fp8_swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
-  const uint32_t nkb = blocks_of(a.cols);
-  const FastDiv d = FastDiv::make(nkb);
-  const uint32_t grid = (uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads);
-  if (a.type == T_FP16)
-    hipLaunchKernelGGL((fp8_swiglu_kernel<f16>), dim3(grid), dim3(kThreads), 0, s, a, d);
-  else
-    hipLaunchKernelGGL((fp8_swiglu_kernel<bf16>), dim3(grid), dim3(kThreads), 0, s, a, d);
-  return hipGetLastError();
+  if (a.vec && a.cols % 16 == 0) return a.type == T_FP16 ? swiglu<f16, true>(a, s) : swiglu<bf16, true>(a, s);
+  return a.type == T_FP16 ? swiglu<f16, false>(a, s) : swiglu<bf16, false>(a, s);
 }
 
 hipError_t launch_fp8_swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
-  const uint32_t nkb = blocks_of(a.cols);
-  const FastDiv d = FastDiv::make(nkb);
-  const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<8>::T);
-  if (a.type == T_FP16)
-    hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<f16>), grid, block, 0, s, a, d);
-  else
-    hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<bf16>), grid, block, 0, s, a, d);
-  return hipGetLastError();
+  if (a.vec && a.cols % 16 == 0) return a.type == T_FP16 ? swiglu_bwd<f16, true>(a, s) : swiglu_bwd<bf16, true>(a, s);
+  return a.type == T_FP16 ? swiglu_bwd<f16, false>(a, s) : swiglu_bwd<bf16, false>(a, s);
 }
 
 }  // namespace iris
