@@ -203,19 +203,10 @@ __device__ __forceinline__ uint32_t piece_amax(const float (&v)[C]) {
   return m;
 }
 
-// the larger of this lane's and another lane's
+// the larger of this lane's and another lane's (0, what a lane outside gives, loses)
 template <int CTRL>
 __device__ __forceinline__ uint32_t max_dpp(uint32_t m) {
-  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, CTRL, 0xf, 0xf, false));
-}
-__device__ __forceinline__ uint32_t max_xor8(uint32_t m) { return max_dpp<0x128>(m); }  // row_ror:8
-__device__ __forceinline__ uint32_t max_xor16(uint32_t m) {
-  const auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-  return max((uint32_t)r[0], (uint32_t)r[1]);
-}
-__device__ __forceinline__ uint32_t max_xor32(uint32_t m) {
-  const auto r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-  return max((uint32_t)r[0], (uint32_t)r[1]);
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xf, 0xf, true));
 }
 // the largest over each aligned group of N lanes, in all of them
 template <int N>
@@ -225,15 +216,33 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
   m = max_dpp<0x4e>(m);    // lane ^ 2
   m = max_dpp<0x141>(m);   // 7 - lane: the other four of eight
   if constexpr (N >= 16) m = max_dpp<0x140>(m);  // 15 - lane
-  if constexpr (N == 64) m = max_xor32(max_xor16(m));
+  if constexpr (N == 64) {
+    const auto x = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max((uint32_t)x[0], (uint32_t)x[1]);
+    const auto y = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = max((uint32_t)y[0], (uint32_t)y[1]);
+  }
   return m;
 }
-// the largest over the lanes l, l + L, l + 2 L, ... of the wave
-template <int L>
-__device__ __forceinline__ uint32_t stride_max(uint32_t m) {
-  static_assert(L == 8 || L == 16, "");
-  if constexpr (L == 8) m = max_xor8(m);
-  return max_xor32(max_xor16(m));
+
+// For C numbers, the largest over the lanes l, l + L, l + 2 L, ... of the wave
+// (L = 128 / C). One swap of two registers' halves and one maximum reduce both
+// registers; what is left in m[0 .. C / 4 - 1] is that of the numbers
+// C / 2 * (lane / 32) + C / 4 * (lane / 16 % 2) + 0 .. C / 4 - 1.
+template <int C>
+__device__ __forceinline__ void stride_max(uint32_t (&m)[C]) {
+  static_assert(C == 8 || C == 16, "");
+#pragma unroll
+  for (int c = 0; c < C / 2; ++c) {
+    const auto r = __builtin_amdgcn_permlane32_swap(m[c], m[c + C / 2], false, false);
+    m[c] = max((uint32_t)r[0], (uint32_t)r[1]);
+  }
+#pragma unroll
+  for (int c = 0; c < C / 4; ++c) {
+    const auto r = __builtin_amdgcn_permlane16_swap(m[c], m[c + C / 4], false, false);
+    m[c] = max((uint32_t)r[0], (uint32_t)r[1]);
+    if constexpr (C == 16) m[c] = max_dpp<0x128>(m[c]);  // lane ^ 8
+  }
 }
 
 // silu and its derivative from sigma(g) = 1 / (1 + 2^(-g log2 e)). v_exp_f32

@@ -103,7 +103,7 @@ template <int C>
 struct TileLds {
   static constexpr int WAVES = TilePlace<C>::T / 64;
   alignas(16) uint32_t turn[kTile][kTile / 4];  // [column][word of 4 rows], swizzled
-  uint32_t part[WAVES][kTile];                  // a wave's largest magnitude of each column
+  alignas(16) uint32_t part[WAVES][kTile];      // a wave's largest magnitude of each column
   alignas(16) float scale[kTile];
 };
 
@@ -139,11 +139,13 @@ __device__ __forceinline__ void put_turned(const Fp8Mat& qt, const TilePlace<C>&
         for (int i = 0; i < 4; ++i) m[c] = max(m[c], finite_bits(v[i][c]));
       }
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) m[c] = stride_max<L>(m[c]);
-    if ((t & 63) < L) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) lds.part[t / 64][C * p.ch + c] = m[c];
+    stride_max<C>(m);
+    if (L == 16 || (t & 8) == 0) {
+      uint32_t* const to = &lds.part[t / 64][C * p.ch + C / 2 * (t >> 5 & 1) + C / 4 * (t >> 4 & 1)];
+      if constexpr (C == 16)
+        *(u32x4*)to = u32x4{m[0], m[1], m[2], m[3]};
+      else
+        *(u32x2*)to = u32x2{m[0], m[1]};
     }
     __syncthreads();
     if (t < kTile) {
