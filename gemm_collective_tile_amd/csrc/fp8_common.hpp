@@ -68,9 +68,10 @@ __device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d,
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ void from_fp8x4(uint32_t w, float* v) {
-  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-  const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+// four codes times a scale (a power of two), exactly
+__device__ __forceinline__ void from_fp8x4(uint32_t w, float scale, float* v) {
+  const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false);
+  const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
   v[0] = lo[0];
   v[1] = lo[1];
   v[2] = hi[0];
@@ -94,30 +95,37 @@ __device__ __forceinline__ void narrow(float v, bf16& o) {
 // last value is read. `row` is the offset of the row's first value from `x`.
 template <class T, int C>
 struct Piece {
-  T t[C];
-  __device__ __forceinline__ float value(int i) const { return widen(t[i]); }
+  static constexpr int N = C * (int)sizeof(T) / 4;
+  uint32_t w[N];
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __builtin_bit_cast(float, w[i]);
+    } else {
+      const uint16_t h = (uint16_t)(w[i / (4 / sizeof(T))] >> (16 * (i & 1)));
+      return widen(__builtin_bit_cast(T, h));
+    }
+  }
   template <bool WHOLE>
   __device__ __forceinline__ void load(const T* x, uint32_t row, int col, int cols, bool on) {
     if constexpr (WHOLE) {
       // a piece that is off reads another one of the row and drops it: no
       // branch between the loads
-      constexpr int W = C * (int)sizeof(T) / 16;
-      static_assert(W >= 1, "piece shorter than a 16-byte load");
+      static_assert(N % 4 == 0, "piece shorter than a 16-byte load");
       on = on && col < cols;
       const uint32_t at = (row + (col < cols ? col : 0)) * (uint32_t)sizeof(T);
-      u32x4 w[W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[i] = ld16((const char*)x + at + 16 * i);
+      for (int i = 0; i < N / 4; ++i) {
+        const u32x4 v = ld16((const char*)x + at + 16 * i);
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[i][e] = on ? w[i][e] : 0u;
-      __builtin_memcpy(t, w, sizeof t);
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = on ? v[e] : 0u;
+      }
     } else {
+      T t[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) t[i] = x[row + min(col + i, cols - 1)];
 #pragma unroll
       for (int i = 0; i < C; ++i) t[i] = on && col + i < cols ? t[i] : T{};
+      __builtin_memcpy(w, t, sizeof t);
     }
   }
 };
@@ -147,16 +155,11 @@ __device__ __forceinline__ void load_codes(const uint8_t* x, uint32_t row, int c
     }
   }
 }
-// their values. A scale of 0 drops the piece (but for NaN codes, which no
-// block's scale counts).
+// their values; all zeros where `on` is false
 template <int C>
-__device__ __forceinline__ void decode(const uint32_t (&w)[C / 4], float scale, float (&v)[C]) {
+__device__ __forceinline__ void decode(const uint32_t (&w)[C / 4], float scale, bool on, float (&v)[C]) {
 #pragma unroll
-  for (int i = 0; i < C / 4; ++i) {
-    from_fp8x4(w[i], v + 4 * i);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) v[4 * i + b] *= scale;
-  }
+  for (int i = 0; i < C / 4; ++i) from_fp8x4(on ? w[i] : 0u, scale, v + 4 * i);
 }
 
 // C codes to a row, none past its last column

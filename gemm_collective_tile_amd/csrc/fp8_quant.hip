@@ -12,7 +12,10 @@
 //          columns where three values per entry are alive); codes of 4 rows of
 //          one column are one 32-bit word of the transposed tile, which turns
 //          around in LDS and leaves in rows of 128 bytes.
+#include <algorithm>
+
 #include "fp8.hpp"
+#include "schedule.hpp"
 
 namespace iris {
 namespace {
@@ -76,14 +79,23 @@ template <int C>
 struct TilePlace {
   static constexpr int L = kTile / C;
   static constexpr int T = L * (kTile / 4);
+  uint32_t t;            // thread
   int r0, c0, ch, j;     // tile origin, piece and row group in it
   int nrows, ncols;      // of the matrix
-  __device__ __forceinline__ TilePlace(int nrows, int ncols, FastDiv ncb) : nrows(nrows), ncols(ncols) {
-    const uint32_t rb = ncb.div(blockIdx.x);
-    r0 = (int)rb * kTile;
-    c0 = (int)(blockIdx.x - rb * ncb.d) * kTile;
-    ch = threadIdx.x % L;
-    j = threadIdx.x / L;
+  // Tiles that run at a time cover a patch of 16 x 16: with whole rows of tiles
+  // the transposed rows written at a time would all start at the same few places
+  // modulo a power-of-two pitch, on a few of the memory's channels.
+  __device__ __forceinline__ TilePlace(uint32_t tile, int nrows, int ncols) : nrows(nrows), ncols(ncols) {
+    int rb, cb;
+    grouped((int)tile, (nrows + kTile - 1) / kTile, (ncols + kTile - 1) / kTile, 16, rb, cb);
+    r0 = rb * kTile;
+    c0 = cb * kTile;
+    // opaque, so that what hangs on it is computed again for every tile and not
+    // kept in registers across them
+    t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    ch = t % L;
+    j = t / L;
   }
   // row i of this thread (rows past the end read the last one), whether it is there
   __device__ __forceinline__ uint32_t row(int i) const { return (uint32_t)min(4 * j + i, nrows - 1 - r0); }
@@ -98,13 +110,13 @@ struct TilePlace {
 };
 __device__ __forceinline__ uint32_t offset(uint32_t row, int64_t ld) { return __umul24(row, (uint32_t)ld); }
 
-// LDS of a tile's turn: the transposed codes and the columns' scales
-template <int C>
+// LDS of N tiles' turn: the transposed codes and the columns' scales
+template <int C, int N>
 struct TileLds {
   static constexpr int WAVES = TilePlace<C>::T / 64;
-  alignas(16) uint32_t turn[kTile][kTile / 4];  // [column][word of 4 rows], swizzled
-  alignas(16) uint32_t part[WAVES][kTile];      // a wave's largest magnitude of each column
-  alignas(16) float scale[kTile];
+  alignas(16) uint32_t turn[N][kTile][kTile / 4];  // [column][word of 4 rows], swizzled
+  alignas(16) uint32_t part[N][WAVES][kTile];      // a wave's largest magnitude of each column
+  alignas(16) float scale[N][kTile];
 };
 
 // The 16-byte pieces of a column's 128 transposed codes are permuted by the
@@ -115,101 +127,107 @@ __device__ __forceinline__ int turn_word(int col, int word) {
   return (((word >> 2) ^ (col / C)) & 7) * 4 + (word & 3);
 }
 
-// Writes the transposed codes and scales of a tile of values. All threads of
-// the workgroup call it; the LDS may be the one of an earlier call. given >= 0:
-// the scale byte of every block (128 x 128 blocks), already written.
-template <int C>
-__device__ __forceinline__ void put_turned(const Fp8Mat& qt, const TilePlace<C>& p, const float (&v)[4][C], int given,
-                                           TileLds<C>& lds) {
+// Writes the transposed codes and scales of N tiles of values (of those whose
+// codes are not NULL). All threads of the workgroup call it; the LDS may be the
+// one of an earlier call. given >= 0: the scale byte of every block (128 x 128
+// blocks), already written.
+template <int C, int N>
+__device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlace<C>& p, const float (&v)[N][4][C],
+                                           int given, TileLds<C, N>& lds) {
   constexpr int T = TilePlace<C>::T, L = TilePlace<C>::L;
-  const int t = threadIdx.x;
-  float s[C];
+  const int t = p.t;
   if (given < 0) {
-    uint32_t m[C], top = 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      m[c] = __builtin_bit_cast(uint32_t, max_abs(max_abs(0.0f, v[0][c], v[1][c]), v[2][c], v[3][c]));
-      top = max(top, m[c]);
-    }
-    if (__builtin_expect(top >= kInfBits, 0)) {
+    for (int n = 0; n < N; ++n) {
+      uint32_t m[C], top = 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        m[c] = 0;
+        m[c] = __builtin_bit_cast(uint32_t, max_abs(max_abs(0.0f, v[n][0][c], v[n][1][c]), v[n][2][c], v[n][3][c]));
+        top = max(top, m[c]);
+      }
+      if (__builtin_expect(top >= kInfBits, 0)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m[c] = max(m[c], finite_bits(v[i][c]));
+        for (int c = 0; c < C; ++c) {
+          m[c] = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m[c] = max(m[c], finite_bits(v[n][i][c]));
+        }
+      }
+      stride_max<C>(m);
+      if (L == 16 || (t & 8) == 0) {
+        uint32_t* const to = &lds.part[n][t / 64][C * p.ch + C / 2 * (t >> 5 & 1) + C / 4 * (t >> 4 & 1)];
+        if constexpr (C == 16)
+          *(u32x4*)to = u32x4{m[0], m[1], m[2], m[3]};
+        else
+          *(u32x2*)to = u32x2{m[0], m[1]};
       }
     }
-    stride_max<C>(m);
-    if (L == 16 || (t & 8) == 0) {
-      uint32_t* const to = &lds.part[t / 64][C * p.ch + C / 2 * (t >> 5 & 1) + C / 4 * (t >> 4 & 1)];
-      if constexpr (C == 16)
-        *(u32x4*)to = u32x4{m[0], m[1], m[2], m[3]};
-      else
-        *(u32x2*)to = u32x2{m[0], m[1]};
-    }
     __syncthreads();
-    if (t < kTile) {
+    if (t < N * kTile) {
+      const int n = t / kTile, c = t % kTile;
       uint32_t a = 0;
 #pragma unroll
-      for (int w = 0; w < TileLds<C>::WAVES; ++w) a = max(a, lds.part[w][t]);
+      for (int w = 0; w < TileLds<C, N>::WAVES; ++w) a = max(a, lds.part[n][w][c]);
       const uint32_t b = scale_byte(a);
-      lds.scale[t] = scale_value(b);
-      if (t < p.cols()) qt.scales[(int64_t)p.c0 * qt.lds + p.r0 / kTile + offset(t, qt.lds)] = (uint8_t)b;
+      lds.scale[n][c] = scale_value(b);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k == n && qt[k].codes && c < p.cols())
+          qt[k].scales[(int64_t)p.c0 * qt[k].lds + p.r0 / kTile + offset(c, qt[k].lds)] = (uint8_t)b;
     }
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) s[c] = lds.scale[C * p.ch + c];
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; ++c) s[c] = scale_value((uint32_t)given);
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = C * p.ch + c;
-    lds.turn[col][turn_word<C>(col, p.j)] = to_fp8x4(v[0][c], v[1][c], v[2][c], v[3][c], s[c]);
-  }
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = C * p.ch + c;
+      const float s = given < 0 ? lds.scale[n][col] : scale_value((uint32_t)given);
+      lds.turn[n][col][turn_word<C>(col, p.j)] = to_fp8x4(v[n][0][c], v[n][1][c], v[n][2][c], v[n][3][c], s);
+    }
   __syncthreads();
   // 8 lanes write the 128 codes of a column
   const int piece = t % 8, valid = p.nrows - p.r0 - 16 * piece;
-  uint8_t* const corner = qt.codes + (int64_t)p.c0 * qt.ld + p.r0;
 #pragma unroll
-  for (int k = 0; k < kTile * 8 / T; ++k) {
-    const int col = k * (T / 8) + t / 8;
-    const uint32_t* const w = &lds.turn[col][turn_word<C>(col, 4 * piece)];
-    if (col >= p.cols()) continue;
-    uint8_t* const to = corner + (offset(col, qt.ld) + 16 * piece);
-    if (valid >= 16) {
-      *(u32x4*)to = *(const u32x4*)w;
-    } else {
+  for (int n = 0; n < N; ++n) {
+    if (!qt[n].codes) continue;
+    uint8_t* const corner = qt[n].codes + (int64_t)p.c0 * qt[n].ld + p.r0;
+#pragma unroll
+    for (int k = 0; k < kTile * 8 / T; ++k) {
+      const int col = k * (T / 8) + t / 8;
+      const uint32_t* const w = &lds.turn[n][col][turn_word<C>(col, 4 * piece)];
+      if (col >= p.cols()) continue;
+      uint8_t* const to = corner + (offset(col, qt[n].ld) + 16 * piece);
+      if (valid >= 16) {
+        *(u32x4*)to = *(const u32x4*)w;
+      } else {
 #pragma unroll 1
-      for (int i = 0; i < valid; ++i) to[i] = ((const uint8_t*)w)[i];
+        for (int i = 0; i < valid; ++i) to[i] = ((const uint8_t*)w)[i];
+      }
     }
   }
 }
 
-// a thread's four row pieces, blocks along the rows
+// a thread's piece of its row i, blocks along the rows
 template <bool WHOLE, int C>
-__device__ __forceinline__ void put_rows(const Fp8Mat& q, const TilePlace<C>& p, const float (&v)[4][C], int given) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t s =
-        given < 0 ? scale_byte(group_max<TilePlace<C>::L>(piece_amax(v[i]))) : (uint32_t)given;
-    uint32_t w[C / 4];
-    encode_piece(v[i], scale_value(s), w);
-    if (p.on(i)) {
-      store_codes<WHOLE, C>(p.corner(q.codes, q.ld), offset(p.row(i), q.ld), p.col(), p.cols(), w);
-      if (given < 0 && p.ch == 0) p.scales(q)[offset(p.row(i), q.lds)] = (uint8_t)s;
-    }
+__device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace<C>& p, int i, const float (&v)[C], int given) {
+  const uint32_t s = given < 0 ? scale_byte(group_max<TilePlace<C>::L>(piece_amax(v))) : (uint32_t)given;
+  uint32_t w[C / 4];
+  encode_piece(v, scale_value(s), w);
+  if (p.on(i)) {
+    store_codes<WHOLE, C>(p.corner(q.codes, q.ld), offset(p.row(i), q.ld), p.col(), p.cols(), w);
+    if (given < 0 && p.ch == 0) p.scales(q)[offset(p.row(i), q.lds)] = (uint8_t)s;
   }
 }
 
 // x -> rows and / or columns, or 128 x 128 blocks
 template <class T, bool WHOLE>
-__global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv ncb) {
+__global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a) {
   constexpr int C = 16;
-  __shared__ TileLds<C> lds;
-  const TilePlace<C> p(a.rows, a.cols, ncb);
-  float v[4][C];
+  __shared__ TileLds<C, 1> lds;
+  const TilePlace<C> p(blockIdx.x, a.rows, a.cols);
+  float all[1][4][C];
+  float(&v)[4][C] = all[0];
   if constexpr (sizeof(T) == 1) {
     uint32_t w[4][C / 4];
     float s[4];
@@ -217,10 +235,10 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv n
     for (int i = 0; i < 4; ++i) {
       load_codes<WHOLE, C>(p.corner(a.x8.codes, a.x8.ld), offset(p.row(i), a.x8.ld), p.col(), p.cols(), w[i]);
       const uint8_t b = p.scales(a.x8)[offset(p.row(i), a.x8.lds)];
-      s[i] = p.on(i) && p.col() < p.cols() ? scale_value(b) : 0.0f;
+      s[i] = scale_value(b);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) decode<C>(w[i], s[i], v[i]);
+    for (int i = 0; i < 4; ++i) decode<C>(w[i], s[i], p.on(i) && p.col() < p.cols(), v[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -232,99 +250,97 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv n
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = max(m, piece_amax(v[i]));
     m = group_max<64>(m);
-    if ((threadIdx.x & 63) == 0) lds.part[0][threadIdx.x / 64] = m;
+    if ((threadIdx.x & 63) == 0) lds.part[0][0][threadIdx.x / 64] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < TileLds<C>::WAVES; ++w) m = max(m, lds.part[0][w]);
+    for (int w = 0; w < TileLds<C, 1>::WAVES; ++w) m = max(m, lds.part[0][0][w]);
     given = (int)scale_byte(m);
     if (threadIdx.x == 0) {
       if (a.q.codes) a.q.scales[(int64_t)(p.r0 / kTile) * a.q.lds + p.c0 / kTile] = (uint8_t)given;
       if (a.qt.codes) a.qt.scales[(int64_t)(p.c0 / kTile) * a.qt.lds + p.r0 / kTile] = (uint8_t)given;
     }
   }
-  if (a.q.codes) put_rows<WHOLE>(a.q, p, v, given);
-  if (a.qt.codes) put_turned<C>(a.qt, p, v, given, lds);
+  if (a.q.codes) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put_row<WHOLE>(a.q, p, i, v[i], given);
+  }
+  if (a.qt.codes) {
+    const Fp8Mat qt[1] = {a.qt};
+    put_turned<C, 1>(qt, p, all, given, lds);
+  }
 }
 
-// With s = sigma(g):  h = g s u,  dgate = dh u s (1 + g (1 - s)),  dup = dh g s,
-// at the kept 8-bit g and u. The inputs stay in registers as they came (64
-// bytes a thread) beside s; the three results are formed one after the other,
-// so that 4 waves fit a SIMD (all three at once: 182 registers, 2 waves).
-template <class T, bool WHOLE>
-__global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
-  constexpr int C = 8;
-  __shared__ TileLds<C> lds;
-  const TilePlace<C> p(a.rows, a.cols, ncb);
+// One tile's inputs as they came, and their loads.
+template <class T, int C>
+struct BwdInputs {
   Piece<T, C> d[4];
-  uint32_t gw[4][C / 4], uw[4][C / 4];
-  float sg[4], su[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t row = p.row(i);
-    const bool on = p.on(i) && p.col() < p.cols();
-    d[i].template load<WHOLE>(p.corner((const T*)a.dh, a.ld_dh), offset(row, a.ld_dh), p.col(), p.cols(), on);
-    load_codes<WHOLE, C>(p.corner(a.gate8.codes, a.gate8.ld), offset(row, a.gate8.ld), p.col(), p.cols(), gw[i]);
-    load_codes<WHOLE, C>(p.corner(a.up8.codes, a.up8.ld), offset(row, a.up8.ld), p.col(), p.cols(), uw[i]);
-    const uint8_t bg = p.scales(a.gate8)[offset(row, a.gate8.lds)];
-    const uint8_t bu = p.scales(a.up8)[offset(row, a.up8.lds)];
-    sg[i] = on ? scale_value(bg) : 0.0f;
-    su[i] = on ? scale_value(bu) : 0.0f;
-  }
-  float s[4][C];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float g[C];
-    decode<C>(gw[i], sg[i], g);
-#pragma unroll
-    for (int c = 0; c < C; ++c) s[i][c] = sigmoid(g[c]);
-  }
-  // decode again where it is needed, instead of keeping all of it
-  const auto forget = [&] {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int k = 0; k < C / 4; ++k) asm volatile("" : "+v"(gw[i][k]), "+v"(uw[i][k]));
-  };
-  forget();
-  {
-    float v[4][C];
+  uint32_t g[4][C / 4], u[4][C / 4];
+  uint8_t sg[4], su[4];
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const Fp8SwigluBwdArgs& a, const TilePlace<C>& p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uint32_t row = p.row(i);
+      d[i].template load<WHOLE>(p.corner((const T*)a.dh, a.ld_dh), offset(row, a.ld_dh), p.col(), p.cols(), p.on(i));
+      load_codes<WHOLE, C>(p.corner(a.gate8.codes, a.gate8.ld), offset(row, a.gate8.ld), p.col(), p.cols(), g[i]);
+      load_codes<WHOLE, C>(p.corner(a.up8.codes, a.up8.ld), offset(row, a.up8.ld), p.col(), p.cols(), u[i]);
+      sg[i] = p.scales(a.gate8)[offset(row, a.gate8.lds)];
+      su[i] = p.scales(a.up8)[offset(row, a.up8.lds)];
+    }
+  }
+};
+
+// With s = sigma(g):  h = g s u,  dgate = dh u s (1 + g (1 - s)),  dup = dh g s,
+// at the kept 8-bit g and u. The three values per entry stay in registers until
+// both directions of blocks have their codes (96 a thread), which leaves room
+// for one workgroup per CU; so it walks tiles, and the next tile's loads are
+// under way while it works on one.
+template <class T, bool WHOLE>
+__global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a) {
+  constexpr int C = 8;
+  __shared__ TileLds<C, 2> lds;
+  const TilePlace<C> p(blockIdx.x, a.rows, a.cols);
+  BwdInputs<T, C> in;
+  in.template load<WHOLE>(a, p);
+  {
+    float v[2][4][C];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool on = p.on(i) && p.col() < p.cols();
       float g[C], u[C];
-      decode<C>(gw[i], sg[i], g);
-      decode<C>(uw[i], su[i], u);
+      decode<C>(in.g[i], scale_value(in.sg[i]), on, g);
+      decode<C>(in.u[i], scale_value(in.su[i]), on, u);
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        v[i][c] = d[i].value(c) * u[c] * (s[i][c] * (1.0f + g[c] * (1.0f - s[i][c])));
+      for (int c = 0; c < C; ++c) {
+        const float d = in.d[i].value(c), s = sigmoid(g[c]);
+        v[0][i][c] = d * u[c] * (s * (1.0f + g[c] * (1.0f - s)));
+        v[1][i][c] = d * (g[c] * s);
+      }
+      put_row<WHOLE>(a.dgate, p, i, v[0][i], -1);
+      put_row<WHOLE>(a.dup, p, i, v[1][i], -1);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    put_rows<WHOLE>(a.dgate, p, v, -1);
-    if (a.dgate_t.codes) put_turned<C>(a.dgate_t, p, v, -1, lds);
-  }
-  forget();
-  {
-    float v[4][C];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float g[C];
-      decode<C>(gw[i], sg[i], g);
-#pragma unroll
-      for (int c = 0; c < C; ++c) v[i][c] = d[i].value(c) * (g[c] * s[i][c]);
+    if (a.dgate_t.codes || a.dup_t.codes) {
+      const Fp8Mat qt[2] = {a.dgate_t, a.dup_t};
+      put_turned<C, 2>(qt, p, v, -1, lds);
     }
-    put_rows<WHOLE>(a.dup, p, v, -1);
-    if (a.dup_t.codes) put_turned<C>(a.dup_t, p, v, -1, lds);
   }
-  forget();
   if (a.h_t.codes) {
-    float v[4][C];
+    float v[1][4][C];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float g[C], u[C];
-      decode<C>(gw[i], sg[i], g);
-      decode<C>(uw[i], su[i], u);
+      const bool on = p.on(i) && p.col() < p.cols();
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[i][c] = g[c] * s[i][c] * u[c];
+      for (int k = 0; k < C / 4; ++k) asm volatile("" : "+v"(in.g[i][k]), "+v"(in.u[i][k]));
+      float g[C], u[C];
+      decode<C>(in.g[i], scale_value(in.sg[i]), on, g);
+      decode<C>(in.u[i], scale_value(in.su[i]), on, u);
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[0][i][c] = g[c] * sigmoid(g[c]) * u[c];
+      __builtin_amdgcn_sched_barrier(0);
     }
-    put_turned<C>(a.h_t, p, v, -1, lds);
+    const Fp8Mat qt[1] = {a.h_t};
+    put_turned<C, 1>(qt, p, v, -1, *(TileLds<C, 1>*)&lds);
   }
 }
 
@@ -334,8 +350,8 @@ uint32_t blocks_of(int n) { return (uint32_t)((n + kFp8Block - 1) / kFp8Block); 
 template <bool WHOLE>
 hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
-  const FastDiv d = FastDiv::make(nkb);
   if (a.block == 1 && !a.qt.codes) {
+    const FastDiv d = FastDiv::make(nkb);
     const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads)), block(kThreads);
     switch (a.x_type) {
       case T_FP16: hipLaunchKernelGGL((fp8_rows_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
@@ -346,10 +362,10 @@ hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
   }
   const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<16>::T);
   switch (a.x_type) {
-    case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
-    case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16, WHOLE>), grid, block, 0, s, a, d); break;
-    case T_FP32: hipLaunchKernelGGL((fp8_tile_kernel<float, WHOLE>), grid, block, 0, s, a, d); break;
-    default: hipLaunchKernelGGL((fp8_tile_kernel<uint8_t, WHOLE>), grid, block, 0, s, a, d); break;
+    case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16, WHOLE>), grid, block, 0, s, a); break;
+    case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16, WHOLE>), grid, block, 0, s, a); break;
+    case T_FP32: hipLaunchKernelGGL((fp8_tile_kernel<float, WHOLE>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((fp8_tile_kernel<uint8_t, WHOLE>), grid, block, 0, s, a); break;
   }
   return hipGetLastError();
 }
@@ -365,8 +381,7 @@ hipError_t swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
 template <class T, bool WHOLE>
 hipError_t swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
-  hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(blocks_of(a.rows) * nkb), dim3(TilePlace<8>::T), 0, s, a,
-                     FastDiv::make(nkb));
+  hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(blocks_of(a.rows) * nkb), dim3(TilePlace<8>::T), 0, s, a);
   return hipGetLastError();
 }
 
