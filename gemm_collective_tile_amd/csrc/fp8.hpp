@@ -54,7 +54,6 @@ struct Fp8SwigluBwdArgs {
   int32_t type, vec;
   Fp8Mat gate8, up8, dgate, dup, dgate_t, dup_t, h_t;  // the transposed ones: codes NULL: not wanted
   int32_t rows, cols;
-  int32_t cus;            // of the device
 };
 hipError_t launch_fp8_swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s);
 

@@ -100,11 +100,9 @@ Fp8Mat mat(const iris_fp8_t* q) {
   return Fp8Mat{(uint8_t*)q->codes, (uint8_t*)q->scales, q->ld, q->ld_scales};
 }
 
-int ready(int32_t* cus = nullptr) {
-  int dev = 0, n = 0;
-  const int st = iris::use_device(&dev, &n);
-  if (cus) *cus = n;
-  return st;
+int ready() {
+  int dev = 0, cus = 0;
+  return iris::use_device(&dev, &cus);
 }
 
 }  // namespace
@@ -245,8 +243,8 @@ int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const ir
       return st;
   if ((st = check_plain(dh, type, false, ld_dh, rows, cols, "dh"))) return st;
   if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = ready())) return st;
   iris::Fp8SwigluBwdArgs a{};
-  if ((st = ready(&a.cus))) return st;
   a.dh = dh;
   a.ld_dh = ld_dh;
   a.type = type;

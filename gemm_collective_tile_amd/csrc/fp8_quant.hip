@@ -12,10 +12,7 @@
 //          columns where three values per entry are alive); codes of 4 rows of
 //          one column are one 32-bit word of the transposed tile, which turns
 //          around in LDS and leaves in rows of 128 bytes.
-#include <algorithm>
-
 #include "fp8.hpp"
-#include "schedule.hpp"
 
 namespace iris {
 namespace {
@@ -82,18 +79,11 @@ struct TilePlace {
   uint32_t t;            // thread
   int r0, c0, ch, j;     // tile origin, piece and row group in it
   int nrows, ncols;      // of the matrix
-  // Tiles that run at a time cover a patch of 16 x 16: with whole rows of tiles
-  // the transposed rows written at a time would all start at the same few places
-  // modulo a power-of-two pitch, on a few of the memory's channels.
-  __device__ __forceinline__ TilePlace(uint32_t tile, int nrows, int ncols) : nrows(nrows), ncols(ncols) {
-    int rb, cb;
-    grouped((int)tile, (nrows + kTile - 1) / kTile, (ncols + kTile - 1) / kTile, 16, rb, cb);
-    r0 = rb * kTile;
-    c0 = cb * kTile;
-    // opaque, so that what hangs on it is computed again for every tile and not
-    // kept in registers across them
+  __device__ __forceinline__ TilePlace(int nrows, int ncols, FastDiv ncb) : nrows(nrows), ncols(ncols) {
+    const uint32_t rb = ncb.div(blockIdx.x);
+    r0 = (int)rb * kTile;
+    c0 = (int)(blockIdx.x - rb * ncb.d) * kTile;
     t = threadIdx.x;
-    asm volatile("" : "+v"(t));
     ch = t % L;
     j = t / L;
   }
@@ -178,13 +168,17 @@ __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlac
     __syncthreads();
   }
 #pragma unroll
-  for (int n = 0; n < N; ++n)
+  for (int n = 0; n < N; ++n) {
+    float s[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = scale_value((uint32_t)given);
+    if (given < 0) __builtin_memcpy(s, &lds.scale[n][C * p.ch], sizeof s);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = C * p.ch + c;
-      const float s = given < 0 ? lds.scale[n][col] : scale_value((uint32_t)given);
-      lds.turn[n][col][turn_word<C>(col, p.j)] = to_fp8x4(v[n][0][c], v[n][1][c], v[n][2][c], v[n][3][c], s);
+      lds.turn[n][col][turn_word<C>(col, p.j)] = to_fp8x4(v[n][0][c], v[n][1][c], v[n][2][c], v[n][3][c], s[c]);
     }
+  }
   __syncthreads();
   // 8 lanes write the 128 codes of a column
   const int piece = t % 8, valid = p.nrows - p.r0 - 16 * piece;
@@ -222,10 +216,10 @@ __device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace<C>& p, 
 
 // x -> rows and / or columns, or 128 x 128 blocks
 template <class T, bool WHOLE>
-__global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a) {
+__global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv ncb) {
   constexpr int C = 16;
   __shared__ TileLds<C, 1> lds;
-  const TilePlace<C> p(blockIdx.x, a.rows, a.cols);
+  const TilePlace<C> p(a.rows, a.cols, ncb);
   float all[1][4][C];
   float(&v)[4][C] = all[0];
   if constexpr (sizeof(T) == 1) {
@@ -291,15 +285,17 @@ struct BwdInputs {
 };
 
 // With s = sigma(g):  h = g s u,  dgate = dh u s (1 + g (1 - s)),  dup = dh g s,
-// at the kept 8-bit g and u. The three values per entry stay in registers until
-// both directions of blocks have their codes (96 a thread), which leaves room
-// for one workgroup per CU; so it walks tiles, and the next tile's loads are
-// under way while it works on one.
+// at the kept 8-bit g and u. A result stays in registers until both directions
+// of blocks have their codes. The inputs stay too, as they came; dgate and dup
+// are formed first and h, for which sigma is computed again, when their
+// registers are free: 113 a thread, so 4 waves fit a SIMD. All three at once
+// spill at that width (4096 x 11008: 143 us against 100), and with 2 waves a SIMD,
+// the next tile's loads under way, take 123.
 template <class T, bool WHOLE>
-__global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a) {
+__global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
   constexpr int C = 8;
   __shared__ TileLds<C, 2> lds;
-  const TilePlace<C> p(blockIdx.x, a.rows, a.cols);
+  const TilePlace<C> p(a.rows, a.cols, ncb);
   BwdInputs<T, C> in;
   in.template load<WHOLE>(a, p);
   {
@@ -350,8 +346,8 @@ uint32_t blocks_of(int n) { return (uint32_t)((n + kFp8Block - 1) / kFp8Block); 
 template <bool WHOLE>
 hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
+  const FastDiv d = FastDiv::make(nkb);
   if (a.block == 1 && !a.qt.codes) {
-    const FastDiv d = FastDiv::make(nkb);
     const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads)), block(kThreads);
     switch (a.x_type) {
       case T_FP16: hipLaunchKernelGGL((fp8_rows_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
@@ -362,10 +358,10 @@ hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
   }
   const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<16>::T);
   switch (a.x_type) {
-    case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16, WHOLE>), grid, block, 0, s, a); break;
-    case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16, WHOLE>), grid, block, 0, s, a); break;
-    case T_FP32: hipLaunchKernelGGL((fp8_tile_kernel<float, WHOLE>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((fp8_tile_kernel<uint8_t, WHOLE>), grid, block, 0, s, a); break;
+    case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
+    case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16, WHOLE>), grid, block, 0, s, a, d); break;
+    case T_FP32: hipLaunchKernelGGL((fp8_tile_kernel<float, WHOLE>), grid, block, 0, s, a, d); break;
+    default: hipLaunchKernelGGL((fp8_tile_kernel<uint8_t, WHOLE>), grid, block, 0, s, a, d); break;
   }
   return hipGetLastError();
 }
@@ -381,7 +377,8 @@ hipError_t swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
 template <class T, bool WHOLE>
 hipError_t swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
-  hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(blocks_of(a.rows) * nkb), dim3(TilePlace<8>::T), 0, s, a);
+  hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(blocks_of(a.rows) * nkb), dim3(TilePlace<8>::T), 0, s, a,
+                     FastDiv::make(nkb));
   return hipGetLastError();
 }
 
