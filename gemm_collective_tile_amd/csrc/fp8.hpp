@@ -21,8 +21,16 @@ struct Fp8MmArgs {
   int64_t ldc;            // elements
   int32_t vec;            // rows of C start at multiples of 16 bytes
   int32_t M, N, K;
+  int32_t splits, split_steps;  // set by launch_fp8_mm
 };
-hipError_t launch_fp8_mm(const Fp8MmArgs& a, hipStream_t s);
+// How a product runs: its tile, and over how many workgroups the contraction of
+// one tile is split (their sums go through ws_bytes of workspace).
+struct Fp8MmPlan {
+  int32_t tile = 256, splits = 1, split_steps = 0;
+  size_t ws_bytes = 0;
+};
+Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_mm(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t s);
 // at most kFp8FewRows rows of A
 constexpr int kFp8FewRows = 64;
 hipError_t launch_fp8_mm_few(const Fp8MmArgs& a, hipStream_t s);

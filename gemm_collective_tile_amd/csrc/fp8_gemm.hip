@@ -47,6 +47,8 @@
 //     449, with sixteen 506 (the patch's rows no longer stay in L2).
 //   * The loads into LDS are written as assembly, because the compiler would
 //     wait for all of them at the next LDS read.
+#include <algorithm>
+
 #include "fp8.hpp"
 #include "fp8_mma.hpp"
 #include "schedule.hpp"
@@ -56,6 +58,7 @@ namespace {
 
 constexpr int kBK = 128;
 constexpr int kGroupM = 8;     // tile rows of a patch that one XCD works on
+constexpr int kCus = 256;      // of the chip
 constexpr int kPatch = 32;     // tiles of a patch: the workgroups of an XCD
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -92,10 +95,9 @@ struct Slice {
   u32x4 a[T::FM][2], b[T::FN][2];
 };
 
-template <class OUT, int BM, int BN>
+template <bool EXACT, int BM, int BN>
 struct Work {
   using T = Tile<BM, BN>;
-  static constexpr bool EXACT = sizeof(OUT) == 4;
 
   const char* lds;
   i32x4 ra, rb;                       // codes of this tile's first rows
@@ -149,11 +151,11 @@ struct Work {
 };
 
 // multiplies one slice; `other` is what is done beside it, in n shares
-template <class OUT, int BM, int BN, class F>
-__device__ __forceinline__ void multiply(Work<OUT, BM, BN>& w, const Slice<Tile<BM, BN>>& f,
+template <bool EXACT, int BM, int BN, class F>
+__device__ __forceinline__ void multiply(Work<EXACT, BM, BN>& w, const Slice<Tile<BM, BN>>& f,
                                          f32x16 (&acc)[Tile<BM, BN>::FM][Tile<BM, BN>::FN], F other) {
   using T = Tile<BM, BN>;
-  if constexpr (!Work<OUT, BM, BN>::EXACT) {
+  if constexpr (!EXACT) {
 #pragma unroll
     for (int k = 0; k < T::NM; ++k) {
       const int i = k / T::FN, j = k % T::FN;
@@ -191,54 +193,6 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// The 16 columns n .. n + 15 of a row that lanes l and l ^ 32 hold between them:
-// v[d] are columns n + 8 d + 4 h .. + 3. All lanes call it.
-template <class OUT>
-__device__ __forceinline__ void put_16(const Fp8MmArgs& g, OUT* crow, bool on, int n, int h, float (&v)[2][4]) {
-  const bool whole = on && g.vec && n + 16 <= g.N;
-  if (g.accumulate) {
-#pragma unroll
-    for (int d = 0; d < 2; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = n + 8 * d + 4 * h + e;
-        if (on && c < g.N) v[d][e] += widen(crow[c]);
-      }
-  }
-  if constexpr (sizeof(OUT) == 4) {
-#pragma unroll
-    for (int d = 0; d < 2; ++d)
-      if (whole) *(f32x4*)(crow + n + 8 * d + 4 * h) = f32x4{v[d][0], v[d][1], v[d][2], v[d][3]};
-  } else {
-    // two columns per word; one swap per word gives each lane 8 neighbouring
-    // columns (the lower lanes the first 8), written at once
-    uint32_t w[2][2];
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      OUT o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) narrow(v[d][e], o[e]);
-      __builtin_memcpy(w[d], o, 8);
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const auto sw = __builtin_amdgcn_permlane32_swap(w[0][x], w[1][x], false, false);
-      w[0][x] = sw[0];
-      w[1][x] = sw[1];
-    }
-    if (whole) *(u32x4*)(crow + n + 8 * h) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
-  }
-  if (on && !whole) {
-#pragma unroll
-    for (int d = 0; d < 2; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = n + 8 * d + 4 * h + e;
-        if (c < g.N) narrow(v[d][e], crow[c]);
-      }
-  }
-}
-
 __device__ __forceinline__ uint32_t rotate(uint32_t word, uint32_t bits) {
   return __builtin_amdgcn_alignbit(word, word, bits);
 }
@@ -249,8 +203,10 @@ __device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t a, uint32_t b
 // shares [k n / N, (k + 1) n / N) of n things over N places
 #define IRIS_SHARE(x, n, k, N) for (int x = (k) * (n) / (N); x < ((k) + 1) * (n) / (N); ++x)
 
-template <class OUT, int BM, int BN>
-__global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
+// One tile of C, or, with g.splits > 1, of one split's sum over its share of k
+// (OUT is float then, C a workspace of g.splits matrices).
+template <class OUT, bool EXACT, int BM, int BN>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArgs g) {
   using T = Tile<BM, BN>;
   __shared__ __align__(16) char lds[T::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -258,15 +214,27 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
   int pm, pn;
   {
     // workgroups go to the XCDs in turn: each takes whole patches of 8 x 4 tiles
-    const int t = xcd_tile(kPatch, blockIdx.x % kXcds, blockIdx.x / kXcds);
-    if (t >= n_pm * n_pn) return;
+    int t = xcd_tile(kPatch, blockIdx.x % kXcds, blockIdx.x / kXcds);
+    const int tiles = n_pm * n_pn;
+    if (t >= tiles * g.splits) return;
+    if (g.splits > 1) {
+      const int split = t / tiles;
+      t -= split * tiles;
+      const int k0 = split * g.split_steps * kBK;
+      g.A.codes += k0;
+      g.B.codes += k0;
+      g.A.scales += split * g.split_steps;
+      g.B.scales += split * g.split_steps;
+      g.K = min(g.K - k0, g.split_steps * kBK);
+      g.C = (OUT*)g.C + (int64_t)split * g.M * g.ldc;
+    }
     grouped(t, n_pm, n_pn, kGroupM, pm, pn);
   }
   const int m0 = pm * BM, n0 = pn * BN;
   const int wm = (wave >> 1) * T::WM, wn = (wave & 1) * T::WN;
   const int r32 = lane & 31;
 
-  Work<OUT, BM, BN> w;
+  Work<EXACT, BM, BN> w;
   w.lds = lds;
   w.ra = buffer_words(g.A.codes + (int64_t)m0 * g.A.ld);
   w.rb = buffer_words(g.B.codes + (int64_t)n0 * g.B.ld);
@@ -349,7 +317,7 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) nb[j] = *(const uint32_t*)(psb[j] + t + 4);
     }
-    multiply<OUT, BM, BN>(w, f0, acc, [&](int k, int N) {
+    multiply<EXACT, BM, BN>(w, f0, acc, [&](int k, int N) {
       IRIS_SHARE(i, T::LA, k, N) w.load_a(i, k2, back, a_free);
       IRIS_SHARE(x, T::NR, k, N) w.read(x, 1, a_this, b_this, f1);
     });
@@ -370,7 +338,7 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) asm volatile("" : "+v"(nb[j]));
     __builtin_amdgcn_sched_barrier(0);
-    multiply<OUT, BM, BN>(w, f1, acc, [&](int k, int N) {
+    multiply<EXACT, BM, BN>(w, f1, acc, [&](int k, int N) {
       IRIS_SHARE(i, T::LB, k, N) w.load_b(i, k2, back, b_this);
       IRIS_SHARE(x, T::NR, k, N) w.read(x, 0, a_next, b_next, f0);
       // the next step's scale bytes, each behind its last use
@@ -388,55 +356,123 @@ __global__ __launch_bounds__(256, 1) void fp8_mm_kernel(Fp8MmArgs g) {
     a_free = a_was;
   }
 
-  // Epilogue. The last loads have to land before the LDS is used again.
+  // Epilogue, 32 rows of a wave at a time: the accumulators turn around in LDS
+  // (B is the first operand, so a lane holds row lane % 32 of each block and, for
+  // q = 0..3, its columns 8 q + 4 (lane / 32) .. + 3) and leave in whole lines,
+  // with the bias and the old values added before the one rounding. The last
+  // loads have to land before the LDS is used again.
   step_barrier<0>();
+  constexpr int V = 16 / (int)sizeof(OUT);            // columns a lane writes at once
+  constexpr int PITCH = T::WN + 4;                    // floats; keeps rows on different banks
+  constexpr int RPI = 64 * V / T::WN;                 // rows a wave writes at once
+  static_assert(4 * 32 * PITCH * 4 + 1024 <= T::LDS, "the turn does not fit");
   float* const bl = (float*)lds;
+  float* const strip = (float*)(lds + 1024) + wave * 32 * PITCH;
   bl[tid] = bias_v;
   __syncthreads();
-  // B is the first operand, so a lane holds row lane % 32 of each block and,
-  // for q = 0..3, its columns 8 q + 4 (lane / 32) .. + 3
-  const int h = lane >> 5;
+  const int c = V * (lane % (T::WN / V)), n = n0 + wn + c;
+  float bn[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) bn[e] = g.bias_along_m ? 0.0f : bl[wn + c + e];
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
-    const int m = m0 + wm + 32 * i + r32;
-    OUT* const crow = (OUT*)g.C + (int64_t)m * g.ldc;
-    const float bm = g.bias_along_m ? bl[wm + 32 * i + r32] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) {
+    for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        const int c = wn + 32 * j + 8 * q;   // 16 columns: 4 in this lane, 4 in lane ^ 32, twice
-        float v[2][4];
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          f32x4 bn = {bm, bm, bm, bm};
-          if (!g.bias_along_m) bn = *(const f32x4*)(bl + c + 8 * d + 4 * h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[d][e] = acc[i][j][4 * (q + d) + e] + bn[e];
-        }
-        put_16(g, crow, m < g.M, n0 + c, h, v);
-      }
+      for (int q = 0; q < 4; ++q)
+        *(f32x4*)(strip + r32 * PITCH + 32 * j + 8 * q + 4 * (lane >> 5)) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+    wait_lds();
+#pragma unroll 2
+    for (int r = 0; r < 32; r += RPI) {
+      const int row = r + lane / (T::WN / V), tm = wm + 32 * i + row, m = m0 + tm;
+      float v[V];
+      __builtin_memcpy(v, strip + row * PITCH + c, sizeof v);
+      if (m < g.M && n < g.N) put_row_piece((OUT*)g.C + (int64_t)m * g.ldc + n, g.N - n, g.vec, g.accumulate,
+                                            g.bias_along_m ? bl[tm] : 0.0f, bn, v);
     }
+    wait_lds();
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <class OUT, int BM, int BN>
+// C = the sum of the splits' matrices, in order, + bias (+ C)
+template <class OUT>
+__global__ __launch_bounds__(256) void fp8_mm_join_kernel(Fp8MmArgs g, const float* part, int64_t ldp, FastDiv pieces) {
+  constexpr int V = 4;
+  const uint32_t id = blockIdx.x * 256 + threadIdx.x, m = pieces.div(id);
+  const int n = V * (int)(id - m * pieces.d);
+  if ((int)m >= g.M) return;
+  const float* p = part + (int64_t)m * ldp + n;
+  float v[V] = {}, bn[V];
+#pragma unroll 4
+  for (int s = 0; s < g.splits; ++s) {
+    const f32x4 x = *(const f32x4*)(p + (int64_t)s * g.M * ldp);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] += x[e];
+  }
+  const OUT* const bias = (const OUT*)g.bias;
+#pragma unroll
+  for (int e = 0; e < V; ++e) bn[e] = bias && !g.bias_along_m && n + e < g.N ? widen(bias[n + e]) : 0.0f;
+  put_row_piece((OUT*)g.C + (int64_t)m * g.ldc + n, g.N - n, g.vec, g.accumulate,
+                bias && g.bias_along_m ? widen(bias[m]) : 0.0f, bn, v);
+}
+
+template <class OUT, bool EXACT, int BM, int BN>
 hipError_t launch(const Fp8MmArgs& a, hipStream_t s) {
-  const int64_t tiles = ((int64_t)a.M + BM - 1) / BM * (((int64_t)a.N + BN - 1) / BN);
+  const int64_t tiles = ((int64_t)a.M + BM - 1) / BM * (((int64_t)a.N + BN - 1) / BN) * a.splits;
   const int64_t round = kPatch * kXcds;
   const uint32_t grid = (uint32_t)((tiles + round - 1) / round * round);
-  hipLaunchKernelGGL((fp8_mm_kernel<OUT, BM, BN>), dim3(grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((fp8_mm_kernel<OUT, EXACT, BM, BN>), dim3(grid), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class OUT>
+hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t s) {
+  constexpr bool EXACT = sizeof(OUT) == 4;
+  Fp8MmArgs g = a;
+  g.splits = plan.splits;
+  g.split_steps = plan.split_steps;
+  if (plan.splits == 1)
+    return plan.tile == 256 ? launch<OUT, EXACT, 256, 256>(g, s) : launch<OUT, EXACT, 128, 128>(g, s);
+  const int64_t ldp = ((int64_t)a.N + 3) / 4 * 4;
+  g.C = ws;
+  g.ldc = ldp;
+  g.vec = 1;
+  g.bias = nullptr;
+  g.accumulate = 0;
+  hipError_t e = launch<float, EXACT, 128, 128>(g, s);
+  if (e != hipSuccess) return e;
+  g = a;
+  g.splits = plan.splits;
+  const uint32_t pieces = (uint32_t)(ldp / 4);
+  const uint32_t grid = (uint32_t)(((int64_t)a.M * pieces + 255) / 256);
+  hipLaunchKernelGGL((fp8_mm_join_kernel<OUT>), dim3(grid), dim3(256), 0, s, g, (const float*)ws, ldp,
+                     FastDiv::make(pieces));
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_fp8_mm(const Fp8MmArgs& a, hipStream_t s) {
-  if (a.M <= kFp8FewRows) return launch_fp8_mm_few(a, s);
+Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K) {
+  Fp8MmPlan p;
+  const int64_t big = (M + 255) / 256 * ((N + 255) / 256), small = (M + 127) / 128 * ((N + 127) / 128);
+  const int64_t steps = (K + kBK - 1) / kBK;
+  if (big >= kCus) return p;
+  p.tile = 128;
+  const int64_t split = std::max<int64_t>(1, std::min(2 * kCus / small, steps / 8));
+  p.split_steps = (int)((steps + split - 1) / split + 3) & ~3;
+  p.splits = p.split_steps > 0 ? (int)((steps + p.split_steps - 1) / p.split_steps) : 1;
+  if (p.splits > 1) p.ws_bytes = (size_t)p.splits * M * ((N + 3) / 4 * 4) * 4;
+  return p;
+}
+
+hipError_t launch_fp8_mm(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t s) {
   switch (a.c_type) {
-    case T_FP16: return launch<f16, 256, 256>(a, s);
-    case T_BF16: return launch<bf16, 256, 256>(a, s);
-    default: return launch<float, 256, 256>(a, s);
+    case T_FP16: return run<f16>(a, plan, ws, s);
+    case T_BF16: return run<bf16>(a, plan, ws, s);
+    default: return run<float>(a, plan, ws, s);
   }
 }
 

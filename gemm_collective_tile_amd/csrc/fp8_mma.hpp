@@ -48,7 +48,37 @@ __device__ __forceinline__ void wait_loads() {
 // until this wave's LDS reads are in registers
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// bias and old value, then the one rounding
+// V values of a row of C: biases and old values added, then the one rounding.
+// `left`: columns from here to the row's end (> 0). `vec`: rows of C start at
+// multiples of 16 bytes.
+template <int V, class OUT>
+__device__ __forceinline__ void put_row_piece(OUT* c, int left, int vec, int accumulate, float bm, const float (&bn)[V],
+                                              float (&v)[V]) {
+  constexpr int BYTES = V * (int)sizeof(OUT);
+  static_assert(BYTES == 16 || BYTES == 8, "");
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] += bn[e] + bm;
+  OUT o[V];
+  if (vec && left >= V) {
+    if (accumulate) {
+      __builtin_memcpy(o, __builtin_assume_aligned(c, BYTES), BYTES);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] += widen(o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) narrow(v[e], o[e]);
+    __builtin_memcpy(__builtin_assume_aligned(c, BYTES), o, BYTES);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < left) {
+        if (accumulate) v[e] += widen(c[e]);
+        narrow(v[e], c[e]);
+      }
+  }
+}
+
+// one value of C
 template <class OUT>
 __device__ __forceinline__ void put_output(OUT* c, float v, const OUT* bias, int64_t bias_at, int accumulate) {
   if (bias) v += widen(bias[bias_at]);

@@ -4,8 +4,13 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "fp8.hpp"
 
@@ -105,7 +110,62 @@ int ready() {
   return iris::use_device(&dev, &cus);
 }
 
+// ------------------------------------------------------------- workspace
+// The split products' sums, one buffer per (device, stream). Every split plan
+// fits kOwnBytes (at most 512 tiles of 128 x 128 fp32 sums), so a buffer never
+// grows and nothing waits for the stream. It needs no clearing.
+constexpr size_t kOwnBytes = (size_t)512 * 128 * 128 * 4;
+std::mutex g_mu;
+std::map<std::pair<int, void*>, void*> g_own;
+
+int own_workspace(int dev, void* stream, size_t need, void** out) {
+  try {
+    std::lock_guard<std::mutex> lk(g_mu);
+    void*& p = g_own[{dev, stream}];
+    if (!p) {
+      // allocating is no stream operation: allowed while a stream captures
+      hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+      (void)hipThreadExchangeStreamCaptureMode(&mode);
+      const hipError_t e = hipMalloc(&p, std::max(need, kOwnBytes));
+      (void)hipThreadExchangeStreamCaptureMode(&mode);
+      if (e != hipSuccess) {
+        p = nullptr;
+        return fail(IRIS_ERR_NO_MEMORY, "hipMalloc of a %zu-byte workspace failed: %s", kOwnBytes, hipGetErrorString(e));
+      }
+    }
+    *out = p;
+    return IRIS_OK;
+  } catch (const std::exception& e) {
+    return fail(IRIS_ERR_NO_MEMORY, "workspace: %s", e.what());
+  }
+}
+
+int check_mm_dims(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0)
+    return fail(IRIS_ERR_INVALID_ARG, "M, N, K must not be negative (got %lld, %lld, %lld)", (long long)M, (long long)N,
+                (long long)K);
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 21) || blocks(M) * blocks(N) > (1 << 30))
+    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N <= 2^30, K <= 2^21, 2^30 output blocks)");
+  return IRIS_OK;
+}
+
 }  // namespace
+
+namespace iris {
+// iris_finalize's share: frees the workspaces above once their streams are done
+int fp8_finalize() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  int status = IRIS_OK;
+  for (auto& kv : g_own) {
+    if (!kv.second) continue;
+    (void)hipSetDevice(kv.first.first);
+    (void)hipStreamSynchronize((hipStream_t)kv.first.second);
+    if (hipFree(kv.second) != hipSuccess) status = IRIS_ERR_HIP;
+  }
+  g_own.clear();
+  return status;
+}
+}  // namespace iris
 
 extern "C" {
 
@@ -145,24 +205,16 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
 }
 
 size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  if (check_mm_dims(M, N, K) || M <= iris::kFp8FewRows || N == 0) return 0;
+  return iris::fp8_mm_plan(M, N, K).ws_bytes;
 }
 
 int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B, const void* bias,
                 int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace, size_t workspace_bytes,
                 void* stream) {
   iris::set_error(IRIS_OK, "");
-  (void)workspace;
-  (void)workspace_bytes;
-  int st;
-  if (M < 0 || N < 0 || K < 0)
-    return fail(IRIS_ERR_INVALID_ARG, "M, N, K must not be negative (got %lld, %lld, %lld)", (long long)M, (long long)N,
-                (long long)K);
-  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 21) || blocks(M) * blocks(N) > (1 << 30))
-    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N <= 2^30, K <= 2^21, 2^30 output blocks)");
+  int st = check_mm_dims(M, N, K);
+  if (st) return st;
   if (flags & ~(IRIS_FLAG_BIAS_ALONG_M | IRIS_FLAG_ACCUMULATE))
     return fail(IRIS_ERR_CONFIG, "unknown flag bits 0x%x", flags);
   if ((st = check_plain(C, c_type, true, ldc, M, N, "C")) || (st = check_blocks1(A, M, K, "A")) ||
@@ -174,7 +226,14 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
     return fail(IRIS_ERR_ALIGNMENT, "B: scales must be 4-byte aligned and ld_scales a multiple of 4");
   if (bias && (uintptr_t)bias % type_bytes(c_type) != 0) return fail(IRIS_ERR_ALIGNMENT, "bias is not aligned to its type");
   if (M == 0 || N == 0) return IRIS_OK;
-  if ((st = ready())) return st;
+  iris::Fp8MmPlan plan;
+  if (M > iris::kFp8FewRows) plan = iris::fp8_mm_plan(M, N, K);
+  if (workspace && workspace_bytes < plan.ws_bytes)
+    return fail(IRIS_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, plan.ws_bytes);
+  if (workspace && (uintptr_t)workspace % 256 != 0) return fail(IRIS_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  int dev = 0, cus = 0;
+  if ((st = iris::use_device(&dev, &cus))) return st;
+  if (plan.ws_bytes > 0 && !workspace && (st = own_workspace(dev, stream, plan.ws_bytes, &workspace))) return st;
   iris::Fp8MmArgs a{};
   a.A = mat(A);
   a.B = mat(B);
@@ -189,7 +248,9 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
-  return launched(iris::launch_fp8_mm(a, (hipStream_t)stream), "iris_fp8_mm");
+  const hipError_t e = M <= iris::kFp8FewRows ? iris::launch_fp8_mm_few(a, (hipStream_t)stream)
+                                              : iris::launch_fp8_mm(a, plan, workspace, (hipStream_t)stream);
+  return launched(e, "iris_fp8_mm");
 }
 
 int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept, const void* gate,

@@ -727,6 +727,7 @@ int copy_ptrs(const void* const* arr, int n, const char* name) {
 
 // ====================================================================== ABI
 namespace iris {
+int fp8_finalize();  // beside the 8-bit operators
 // Records the message for iris_last_error_message from the library's other
 // translation units; returns status.
 int set_error(int status, const char* msg) {
@@ -1284,8 +1285,8 @@ const char* iris_status_str(int32_t s) {
 const char* iris_last_error_message(void) { return g_msg.c_str(); }
 
 int iris_finalize(void) {
+  int status = iris::fp8_finalize();
   std::lock_guard<std::mutex> lk(g_mu);
-  int status = IRIS_OK;
   for (auto& kv : g_ws) {
     if (kv.second.ptr) {
       (void)hipSetDevice(kv.first.first);

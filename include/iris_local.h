@@ -335,9 +335,13 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
  * The product of a layer is A = activations, B = weights (out, in); the
  * input's gradient A = output gradients, B = transposed weights; the weight's
  * gradient A = transposed output gradients, B = transposed activations.
- * workspace: as for the ops above (NULL: the library's own), at least
- * iris_fp8_mm_workspace_size() bytes, 256-byte aligned and zero-filled before
- * its first use. One workspace may not serve two ops at the same time.
+ * workspace: for the sums of a contraction that is split over workgroups (few
+ * output tiles): at least iris_fp8_mm_workspace_size() bytes (0: none needed),
+ * 256-byte aligned, contents of no account; not the workspace of an op above,
+ * which has to stay zeroed. NULL: the library's own, 32 MiB per (device,
+ * stream), allocated by the first call that needs it (also during a graph
+ * capture, whose replays then use it) and freed by iris_finalize(). One
+ * workspace may not serve two calls at the same time.
  */
 int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B,
                 const void* bias, int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace,
