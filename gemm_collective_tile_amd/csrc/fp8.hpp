@@ -29,7 +29,7 @@ struct Fp8MmPlan {
   int32_t tile = 256, splits = 1, split_steps = 0;
   size_t ws_bytes = 0;
 };
-Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K);
+Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32);
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t s);
 // at most kFp8FewRows rows of A
 constexpr int kFp8FewRows = 64;

@@ -206,7 +206,7 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
 
 size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_mm_dims(M, N, K) || M <= iris::kFp8FewRows || N == 0) return 0;
-  return iris::fp8_mm_plan(M, N, K).ws_bytes;
+  return std::max(iris::fp8_mm_plan(M, N, K, false).ws_bytes, iris::fp8_mm_plan(M, N, K, true).ws_bytes);
 }
 
 int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B, const void* bias,
@@ -227,7 +227,7 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   if (bias && (uintptr_t)bias % type_bytes(c_type) != 0) return fail(IRIS_ERR_ALIGNMENT, "bias is not aligned to its type");
   if (M == 0 || N == 0) return IRIS_OK;
   iris::Fp8MmPlan plan;
-  if (M > iris::kFp8FewRows) plan = iris::fp8_mm_plan(M, N, K);
+  if (M > iris::kFp8FewRows) plan = iris::fp8_mm_plan(M, N, K, c_type == IRIS_TYPE_FP32);
   if (workspace && workspace_bytes < plan.ws_bytes)
     return fail(IRIS_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, plan.ws_bytes);
   if (workspace && (uintptr_t)workspace % 256 != 0) return fail(IRIS_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
