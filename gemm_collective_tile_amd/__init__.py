@@ -210,7 +210,7 @@ def _stream(stream):
     if stream is None:
         # the current stream's handle; building the torch.cuda.Stream object
         # around it costs 3 us a call on the host
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -469,37 +469,31 @@ def iris_fp8_empty(rows: int, cols: int, block: int = 1, device=None) -> Fp8:
     return Fp8(codes[:, :cols], scales.view(torch.float8_e8m0fnu)[:, :nb], block)
 
 
-def _want_fp8(q, shape, name: str, allow_none=False):
-    """Pointer to q's C struct after its shape (and, last, its device) check."""
-    if q is None:
-        if allow_none:
-            return None
-        raise ValueError(f"{name} is required")
-    if not isinstance(q, Fp8):
-        raise TypeError(f"{name} must be an Fp8 matrix")
+# These run once per call in front of a 2 us launch, so they do little more than
+# the comparisons themselves.
+
+def _fp8(q, shape, name: str):
+    """q's C struct, after the check of its kind, shape and (last) device."""
+    if q.__class__ is not Fp8:
+        raise TypeError(f"{name} must be an Fp8 matrix") if q is not None else ValueError(f"{name} is required")
     if q.shape != shape:
         raise ValueError(f"{name} has shape {q.shape}, expected {shape}")
-    return q
-
-
-def _fp8_ptr(q, name: str):
-    if q is None:
-        return None
     if not q._on_gpu:
         raise ValueError(f"{name} must be on a GPU")
     return q._p
 
 
-def _plain(t, name: str, dtypes):
+def _plain(t, name: str, kinds, rows: int, cols: int):
     """(pointer, type, row pitch) of a row-major matrix with any row pitch."""
-    kind = dtypes.get(t.dtype)
+    kind = kinds.get(t.dtype)
     if kind is None:
-        raise TypeError(f"{name} must be one of {', '.join(str(d)[6:] for d in dtypes)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise TypeError(f"{name} must be one of {', '.join(str(d)[6:] for d in kinds)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    return t.data_ptr(), kind, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), kind, (ld if rows > 1 else cols)
 
 
 _FP8_HALVES = {torch.float16: 1, torch.bfloat16: 2}
@@ -509,17 +503,17 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
     """x (rows, cols) to 8 bits: q (rows, cols) with blocks along its rows and /
     or q_t (cols, rows), x transposed, both in one pass. x is a float16, bfloat16
     or float32 tensor, or an Fp8 matrix (then only q_t, blocks of 1 x 128)."""
-    if isinstance(x, Fp8):
-        rows, cols = x.shape
+    from8 = x.__class__ is Fp8
+    shape = x.shape if from8 else _shape2(x, "x")
+    rows, cols = shape
+    qp = None if q is None else _fp8(q, (rows, cols), "q")
+    qtp = None if q_t is None else _fp8(q_t, (cols, rows), "q_t")
+    if from8:
+        ptr, kind, ld, x8 = None, 0, 0, _fp8(x, shape, "x")
     else:
-        rows, cols = _shape2(x, "x")
-    _want_fp8(q, (rows, cols), "q", True)
-    _want_fp8(q_t, (cols, rows), "q_t", True)
-    if isinstance(x, Fp8):
-        ptr, kind, ld, x8 = None, 0, 0, _fp8_ptr(x, "x")
-    else:
-        (ptr, kind, ld), x8 = _plain(x, "x", _FP8_TYPES), None
-    st = _lib.iris_fp8_quantize(_fp8_ptr(q, "q"), _fp8_ptr(q_t, "q_t"), ptr, kind, ld, x8, rows, cols, _stream(stream))
+        ptr, kind, ld = _plain(x, "x", _FP8_TYPES, rows, cols)
+        x8 = None
+    st = _lib.iris_fp8_quantize(qp, qtp, ptr, kind, ld, x8, rows, cols, _stream(stream))
     if st:
         _check(st)
 
@@ -527,13 +521,14 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
 def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, workspace=None, stream=None) -> None:
     """C = A @ B^T + bias (+ C with accumulate): A (M, K) Fp8 with blocks of
     1 x 128, B (N, K) Fp8, C (M, N) float16, bfloat16 or float32, bias of C's type."""
-    if not isinstance(A, Fp8) or not isinstance(B, Fp8):
+    if A.__class__ is not Fp8 or B.__class__ is not Fp8:
         raise TypeError("A and B must be Fp8 matrices")
     M, K = A.shape
     N = B.shape[0]
     if B.shape[1] != K:
         raise ValueError(f"B has shape {B.shape}, expected ({N}, {K})")
-    _want_shape(C, (M, N), "C")
+    if not isinstance(C, torch.Tensor) or C.shape != (M, N):
+        _want_shape(C, (M, N), "C")
     flags = IRIS_FLAG_ACCUMULATE if accumulate else 0
     bias_ptr = None
     if bias is not None:
@@ -544,13 +539,14 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
             raise ValueError("bias must be contiguous")
         if _bias_along_m(config):
             flags |= IRIS_FLAG_BIAS_ALONG_M
+    ptr, kind, ld = _plain(C, "C", _FP8_TYPES, M, N)
+    if bias is not None:
+        if not bias.is_cuda:
+            raise ValueError("bias must be on a GPU")
         bias_ptr = bias.data_ptr()
-    ptr, kind, ld = _plain(C, "C", _FP8_TYPES)
-    if bias is not None and not bias.is_cuda:
-        raise ValueError("bias must be on a GPU")
     ws, wsb = _ws(workspace)
-    st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8_ptr(A, "A"), _fp8_ptr(B, "B"), bias_ptr, M, N, K, flags, ws, wsb,
-                          _stream(stream))
+    st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8(A, A.shape, "A"), _fp8(B, B.shape, "B"), bias_ptr, M, N, K, flags, ws,
+                          wsb, _stream(stream))
     if st:
         _check(st)
 
@@ -559,17 +555,18 @@ def iris_fp8_swiglu(h: Fp8, gate, up, gate_kept: Optional[Fp8] = None, up_kept: 
                     stream=None) -> None:
     """h = silu(gate) * up in 8 bits; gate, up (rows, cols) float16 or bfloat16
     (views of one matrix will do); gate_kept and up_kept receive them in 8 bits."""
-    rows, cols = _shape2(gate, "gate")
-    _want_shape(up, (rows, cols), "up")
+    shape = rows, cols = tuple(_shape2(gate, "gate"))
+    if not isinstance(up, torch.Tensor) or up.shape != shape:
+        _want_shape(up, shape, "up")
     if up.dtype != gate.dtype:
         raise TypeError("gate and up must have one dtype")
-    _want_fp8(h, (rows, cols), "h")
-    _want_fp8(gate_kept, (rows, cols), "gate_kept", up_kept is None)
-    _want_fp8(up_kept, (rows, cols), "up_kept", gate_kept is None)
-    gp, kind, gld = _plain(gate, "gate", _FP8_HALVES)
-    up_, _, uld = _plain(up, "up", _FP8_HALVES)
-    st = _lib.iris_fp8_swiglu(_fp8_ptr(h, "h"), _fp8_ptr(gate_kept, "gate_kept"), _fp8_ptr(up_kept, "up_kept"), gp,
-                              up_, kind, gld, uld, rows, cols, _stream(stream))
+    hp = _fp8(h, shape, "h")
+    kept = gate_kept is not None or up_kept is not None
+    gkp = _fp8(gate_kept, shape, "gate_kept") if kept else None
+    ukp = _fp8(up_kept, shape, "up_kept") if kept else None
+    gp, kind, gld = _plain(gate, "gate", _FP8_HALVES, rows, cols)
+    up_ptr, _, uld = _plain(up, "up", _FP8_HALVES, rows, cols)
+    st = _lib.iris_fp8_swiglu(hp, gkp, ukp, gp, up_ptr, kind, gld, uld, rows, cols, _stream(stream))
     if st:
         _check(st)
 
@@ -579,16 +576,14 @@ def iris_fp8_swiglu_bwd(dgate: Fp8, dup: Fp8, dh, gate_kept: Fp8, up_kept: Fp8, 
     """Backward pass of iris_fp8_swiglu at the kept gate and up: dgate, dup
     (rows, cols) and, if given, dgate_t, dup_t and the recomputed h_t (cols,
     rows), all in 8 bits; dh (rows, cols) float16 or bfloat16."""
-    rows, cols = _shape2(dh, "dh")
-    for q, name in ((dgate, "dgate"), (dup, "dup"), (gate_kept, "gate_kept"), (up_kept, "up_kept")):
-        _want_fp8(q, (rows, cols), name)
-    for q, name in ((dgate_t, "dgate_t"), (dup_t, "dup_t"), (h_t, "h_t")):
-        _want_fp8(q, (cols, rows), name, True)
-    ptr, kind, ld = _plain(dh, "dh", _FP8_HALVES)
-    st = _lib.iris_fp8_swiglu_bwd(_fp8_ptr(dgate, "dgate"), _fp8_ptr(dup, "dup"), _fp8_ptr(dgate_t, "dgate_t"),
-                                  _fp8_ptr(dup_t, "dup_t"), _fp8_ptr(h_t, "h_t"), ptr, kind, ld,
-                                  _fp8_ptr(gate_kept, "gate_kept"), _fp8_ptr(up_kept, "up_kept"), rows, cols,
-                                  _stream(stream))
+    shape = rows, cols = tuple(_shape2(dh, "dh"))
+    turned = (cols, rows)
+    st = _lib.iris_fp8_swiglu_bwd(
+        _fp8(dgate, shape, "dgate"), _fp8(dup, shape, "dup"),
+        None if dgate_t is None else _fp8(dgate_t, turned, "dgate_t"),
+        None if dup_t is None else _fp8(dup_t, turned, "dup_t"), None if h_t is None else _fp8(h_t, turned, "h_t"),
+        *_plain(dh, "dh", _FP8_HALVES, rows, cols), _fp8(gate_kept, shape, "gate_kept"),
+        _fp8(up_kept, shape, "up_kept"), rows, cols, _stream(stream))
     if st:
         _check(st)
 
