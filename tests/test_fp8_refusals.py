@@ -1,0 +1,187 @@
+"""What the 8-bit operators refuse, before any GPU call: the binding's checks
+(TypeError, ValueError) on CPU tensors, the library's status codes on
+placeholder pointers that are never read."""
+import ctypes
+
+import pytest
+import torch
+
+import gemm_collective_tile_amd as il
+from gemm_collective_tile_amd import _Fp8, _lib
+
+P, ODD = 0x100000, 0x100008
+
+
+def empty(rows, cols, block=1):
+    return il.iris_fp8_empty(rows, cols, block, device="cpu")
+
+
+# ------------------------------------------------------------------- binding
+
+def test_fp8_handle_refuses():
+    codes, scales = torch.zeros((4, 256), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8)
+    il.Fp8(codes, scales)
+    il.Fp8(codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu))
+    for bad in ((codes.float(), scales, 1), (codes, scales.float(), 1), (codes.to(torch.int8), scales, 1)):
+        with pytest.raises(TypeError):
+            il.Fp8(*bad)
+    for bad in ((codes, scales[:, :1], 1), (codes, scales[:2], 1), (codes, scales, 64), (codes, scales, 128),
+                (codes.reshape(2, 2, 256), scales, 1), (codes.t(), scales, 1), (codes[:, :40].contiguous()[:, :37], scales[:, :1], 1)):
+        with pytest.raises(ValueError):
+            il.Fp8(*bad)
+    tight = torch.zeros(16 * 3 + 5, dtype=torch.uint8).as_strided((4, 5), (16, 1))
+    with pytest.raises(ValueError, match="next multiple of 16"):
+        il.Fp8(tight, torch.zeros((4, 1), dtype=torch.uint8))
+
+
+def test_empty_lays_rows_out():
+    q = empty(5, 130, 128)
+    assert q.codes.stride() == (144, 1) and q.scales.shape == (1, 2) and q.scales.dtype == torch.float8_e8m0fnu
+    assert empty(300, 1000).scales.stride() == (8, 1)
+    for rows, cols in ((0, 9), (9, 0), (0, 0)):
+        assert empty(rows, cols).shape == (rows, cols)
+
+
+def expect(kind, text, fn, *args, **kw):
+    with pytest.raises(kind, match=text):
+        fn(*args, **kw)
+
+
+def test_quantize_refuses():
+    x = torch.zeros((6, 200), dtype=torch.float16)
+    f = il.iris_fp8_quantize
+    expect(ValueError, "expected", f, x, empty(6, 201))
+    expect(ValueError, "expected", f, x, None, empty(6, 200))
+    expect(TypeError, "Fp8", f, x, torch.zeros((6, 200), dtype=torch.uint8))
+    expect(ValueError, "2-D", f, x[0], empty(6, 200))
+    expect(ValueError, "on a GPU", f, x, empty(6, 200))
+    expect(TypeError, "must be one of", _on_gpu_checks, f, x.double())
+    expect(ValueError, "contiguous along", _on_gpu_checks, f, torch.zeros((200, 6), dtype=torch.float16).t())
+
+
+def _on_gpu_checks(f, x):
+    f(x)      # no outputs: the plain matrix's own checks come first
+
+
+def test_mm_refuses():
+    A, B, C = empty(6, 200), empty(9, 200), torch.zeros((6, 9), dtype=torch.float16)
+    f = il.iris_fp8_mm
+    expect(ValueError, "B has shape", f, C, A, empty(9, 199))
+    expect(ValueError, "C has shape", f, C[:, :8], A, B)
+    expect(TypeError, "Fp8", f, C, torch.zeros(6, 200), B)
+    expect(ValueError, "bias has", f, C, A, B, torch.zeros(8, dtype=torch.float16))
+    expect(TypeError, "bias must be", f, C, A, B, torch.zeros(9))
+    expect(ValueError, "bias has", f, C, A, B, torch.zeros(9, dtype=torch.float16),
+           config=il.Config(flags=il.IRIS_FLAG_BIAS_ALONG_M))
+    expect(TypeError, "C must be one of", f, C.double(), A, B)
+    expect(ValueError, "contiguous along", f, torch.zeros((9, 6)).t(), A, B)
+    expect(ValueError, "on a GPU", f, C, A, B)
+
+
+def test_swiglu_refuses():
+    g, h = torch.zeros((6, 200), dtype=torch.float16), empty(6, 200)
+    f = il.iris_fp8_swiglu
+    expect(ValueError, "up has shape", f, h, g, g[:, :199])
+    expect(TypeError, "one dtype", f, h, g, g.bfloat16())
+    expect(ValueError, "h has shape", f, empty(6, 199), g, g)
+    expect(ValueError, "on a GPU", f, h, g, g, h)
+    b = il.iris_fp8_swiglu_bwd
+    expect(ValueError, "dgate has shape", b, empty(6, 199), h, g, h, h)
+    expect(ValueError, "on a GPU", b, h, h, g, h, h)
+    expect(ValueError, "is required", b, None, h, g, h, h)
+
+
+# ------------------------------------------------------------------- library
+
+def st(status):
+    return il.STATUS[status]
+
+
+def m8(codes=P, scales=P, ld=1024, lds=8, block=1):
+    return ctypes.pointer(_Fp8(codes, scales, ld, lds, block))
+
+
+def quant(q=None, qt=None, x=P, kind=1, ldx=1024, x8=None, rows=512, cols=1000):
+    return st(_lib.iris_fp8_quantize(q, qt, x, kind, ldx, x8, rows, cols, None))
+
+
+def test_library_quantize_refuses():
+    assert quant() == "IRIS_ERR_INVALID_ARG"                                   # no output
+    assert quant(m8(), x=None) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(), kind=9) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(), ldx=999) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(), x=P + 1) == "IRIS_ERR_ALIGNMENT"
+    assert quant(m8(codes=ODD)) == "IRIS_ERR_ALIGNMENT"
+    assert quant(m8(ld=1023 + 9)) == "IRIS_ERR_ALIGNMENT"
+    assert quant(m8(ld=992)) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(lds=7)) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(block=3)) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(codes=None)) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(), m8(block=128, ld=512)) == "IRIS_ERR_INVALID_ARG"        # two kinds of block
+    assert quant(m8(), rows=-1) == "IRIS_ERR_INVALID_ARG"
+    assert quant(m8(), rows=1 << 31) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(m8(ld=1 << 23)) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(m8(), ldx=1 << 23) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(m8(), x8=m8()) == "IRIS_ERR_INVALID_ARG"                      # x and x8
+    assert quant(m8(), x=None, x8=m8()) == "IRIS_ERR_UNSUPPORTED"              # 8 bits to rows
+    assert quant(None, m8(block=128, ld=512), x=None, x8=m8()) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(None, m8(ld=512), x=None, x8=m8(block=128)) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(m8(), rows=0) == "IRIS_OK" and quant(m8(), cols=0) == "IRIS_OK"
+
+
+def mm(C=P, kind=1, ldc=512, A=None, B=None, bias=None, M=512, N=512, K=1000, flags=0, ws=None, wsb=0):
+    return st(_lib.iris_fp8_mm(C, kind, ldc, A or m8(), B or m8(block=128), bias, M, N, K, flags, ws, wsb, None))
+
+
+def test_library_mm_refuses():
+    assert mm(C=None) == "IRIS_ERR_INVALID_ARG"
+    assert mm(kind=4) == "IRIS_ERR_INVALID_ARG"
+    assert mm(ldc=511) == "IRIS_ERR_INVALID_ARG"
+    assert mm(C=P + 1) == "IRIS_ERR_ALIGNMENT"
+    assert mm(bias=P + 1) == "IRIS_ERR_ALIGNMENT"
+    assert mm(A=m8(block=128)) == "IRIS_ERR_UNSUPPORTED"
+    assert mm(A=m8(scales=P + 2)) == "IRIS_ERR_ALIGNMENT"
+    assert mm(B=m8(lds=10, block=128)) == "IRIS_ERR_ALIGNMENT"
+    assert mm(B=m8(ld=960)) == "IRIS_ERR_INVALID_ARG"
+    assert mm(flags=1) == "IRIS_ERR_CONFIG"
+    assert mm(M=-1) == "IRIS_ERR_INVALID_ARG"
+    assert mm(M=1 << 31) == "IRIS_ERR_UNSUPPORTED"
+    assert mm(K=1 << 22, A=m8(ld=1 << 22, lds=1 << 16), B=m8(ld=1 << 22, lds=1 << 16)) == "IRIS_ERR_UNSUPPORTED"
+    assert mm(M=0) == "IRIS_OK" and mm(N=0) == "IRIS_OK"
+    need = il.iris_fp8_mm_workspace_size(256, 512, 11008)
+    assert need > 0
+    wide = dict(A=m8(ld=11008, lds=88), B=m8(ld=11008, lds=88, block=128), M=256, K=11008)
+    assert mm(ws=P, wsb=0, **wide) == "IRIS_ERR_WORKSPACE"
+    assert mm(ws=P + 64, wsb=need, **wide) == "IRIS_ERR_ALIGNMENT"
+
+
+def test_workspace_sizes():
+    f = il.iris_fp8_mm_workspace_size
+    assert f(1, 4096, 4096) == 0 and f(64, 4096, 11008) == 0      # few rows: no split
+    assert f(8192, 8192, 8192) == 0                               # tiles enough
+    assert f(-1, 2, 3) == 0 and f(0, 0, 0) == 0
+    for m in (65, 100, 129, 300, 513, 1000, 2500):
+        for n in (1, 64, 130, 1376, 4096, 11008):
+            for k in (0, 100, 1000, 4096, 11008, 100000):
+                assert f(m, n, k) <= 512 * 128 * 128 * 4, (m, n, k)
+
+
+def test_library_activation_refuses():
+    def fwd(h=None, gk=None, uk=None, gate=P, up=P, kind=1, lg=1024, lu=1024, rows=512, cols=1000):
+        return st(_lib.iris_fp8_swiglu(h or m8(), gk, uk, gate, up, kind, lg, lu, rows, cols, None))
+    assert fwd(gk=m8()) == "IRIS_ERR_INVALID_ARG"
+    assert fwd(kind=3) == "IRIS_ERR_INVALID_ARG"
+    assert fwd(up=None) == "IRIS_ERR_INVALID_ARG"
+    assert fwd(lg=999) == "IRIS_ERR_INVALID_ARG"
+    assert fwd(h=m8(block=128)) == "IRIS_ERR_UNSUPPORTED"
+    assert fwd(rows=0) == "IRIS_OK"
+
+    def bwd(dg=None, du=None, dgt=None, dut=None, ht=None, dh=P, kind=1, ld=1024, gk=None, uk=None, rows=512, cols=1000):
+        return st(_lib.iris_fp8_swiglu_bwd(dg or m8(), du or m8(), dgt, dut, ht, dh, kind, ld, gk or m8(), uk or m8(),
+                                           rows, cols, None))
+    assert bwd(dh=None) == "IRIS_ERR_INVALID_ARG"
+    assert bwd(kind=3) == "IRIS_ERR_INVALID_ARG"
+    assert bwd(dgt=m8(ld=496)) == "IRIS_ERR_INVALID_ARG"          # shorter than its 512 columns
+    assert bwd(ht=m8(block=128, ld=512)) == "IRIS_ERR_UNSUPPORTED"
+    assert bwd(gk=m8(codes=ODD)) == "IRIS_ERR_ALIGNMENT"
+    assert bwd(cols=0) == "IRIS_OK"
