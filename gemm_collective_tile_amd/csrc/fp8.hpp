@@ -12,16 +12,16 @@ enum Fp8Type : int32_t { T_FP16 = 1, T_BF16 = 2, T_FP32 = 3, T_FP8 = 4 };
 
 struct Fp8MmArgs {
   Fp8Mat A, B;
-  int32_t b_block;        // rows of B per scale row: 1 or 128
   const void* bias;       // in C's type, or NULL
-  int32_t bias_along_m;
-  int32_t accumulate;     // add to C's old values
   void* C;
-  int32_t c_type;
-  int64_t ldc;            // elements
-  int32_t vec;            // rows of C start at multiples of 16 bytes
+  int32_t ldc;            // elements
   int32_t M, N, K;
   int32_t splits, split_steps;  // set by launch_fp8_mm
+  uint8_t b_block;        // rows of B per scale row: 1 or 128
+  uint8_t bias_along_m;
+  uint8_t accumulate;     // add to C's old values
+  uint8_t vec;            // rows of C start at multiples of 16 bytes
+  uint8_t c_type;
 };
 // How a product runs: its tile, and over how many workgroups the contraction of
 // one tile is split (their sums go through ws_bytes of workspace).
@@ -37,7 +37,7 @@ hipError_t launch_fp8_mm_few(const Fp8MmArgs& a, hipStream_t s);
 
 struct Fp8QuantArgs {
   const void* x;          // fp16, bf16 or fp32 values with a row pitch of ldx elements
-  int64_t ldx;
+  int32_t ldx;
   Fp8Mat x8;              // or 8-bit values with 1 x 128 blocks (x_type T_FP8)
   int32_t x_type;
   int32_t block;          // 1: blocks of 1 x 128, 128: of 128 x 128
@@ -49,7 +49,7 @@ hipError_t launch_fp8_quantize(const Fp8QuantArgs& a, hipStream_t s);
 
 struct Fp8SwigluArgs {
   const void *gate, *up;
-  int64_t ld_gate, ld_up;
+  int32_t ld_gate, ld_up;
   int32_t type, vec;
   Fp8Mat h, gate8, up8;   // gate8, up8: codes NULL: not wanted
   int32_t rows, cols;
@@ -58,7 +58,7 @@ hipError_t launch_fp8_swiglu(const Fp8SwigluArgs& a, hipStream_t s);
 
 struct Fp8SwigluBwdArgs {
   const void* dh;
-  int64_t ld_dh;
+  int32_t ld_dh;
   int32_t type, vec;
   Fp8Mat gate8, up8, dgate, dup, dgate_t, dup_t, h_t;  // the transposed ones: codes NULL: not wanted
   int32_t rows, cols;

@@ -25,11 +25,13 @@ namespace iris {
 constexpr int kFp8Block = 128;
 
 // A block-scaled matrix: `ld` bytes from one row of codes to the next, `lds`
-// from one row of scales to the next.
+// from one row of scales to the next (pitches are at most 2^22; kernels' arguments
+// are kept short, the host writes them for every launch: 0.6 us for 200 bytes
+// more).
 struct Fp8Mat {
   uint8_t* codes;
   uint8_t* scales;
-  int64_t ld, lds;
+  int32_t ld, lds;
 };
 
 struct bf16 {

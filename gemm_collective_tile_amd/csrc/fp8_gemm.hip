@@ -77,16 +77,26 @@ __device__ __forceinline__ i32x4 buffer_words(const void* p) {
                (int)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu), (int)0xfffffff0u, kRsrcWord3};
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int SA_, int SB_>
 struct Tile {
+  static constexpr int SA = SA_, SB = SB_;             // LDS stages of A and of B
   static constexpr int WM = BM / 2, WN = BN / 2;       // a wave's part
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int A_STAGE = BM * kBK, B_STAGE = BN * kBK;
-  static constexpr int B_AT = 3 * A_STAGE;             // LDS: [A stages | B stages]
-  static constexpr int LDS = B_AT + 2 * B_STAGE;
+  static constexpr int B_AT = SA * A_STAGE;            // LDS: [A stages | B stages]
+  static constexpr int LDS = B_AT + SB * B_STAGE;
   static constexpr int LA = BM / 32, LB = BN / 32;     // loads of 1 KB per wave and step
   static constexpr int NM = FM * FN;                   // 32 x 32 blocks per wave
   static constexpr int NR = 2 * (FM + FN);             // operand reads per slice
+  // Beside slice 0 of step t go A's loads of step t + SA - 1, beside slice 1 B's
+  // of step t + SB. Between the two, step t + 1 has to have landed: the loads
+  // that were issued since its last one and may still be under way.
+  static constexpr int under_way() {
+    const int a = 2 * (2 - SA), b = 2 * (1 - SB) + 1;   // when A's and B's of step t + 1 went out, in half steps
+    int n = 0;
+    for (int h = (a > b ? a : b) + 1; h <= 0; ++h) n += h % 2 == 0 ? LA : LB;
+    return n;
+  }
 };
 
 // one slice's operands: two pieces per 32-row block
@@ -95,9 +105,9 @@ struct Slice {
   u32x4 a[T::FM][2], b[T::FN][2];
 };
 
-template <bool EXACT, int BM, int BN>
+template <class T_>
 struct Work {
-  using T = Tile<BM, BN>;
+  using T = T_;
 
   const char* lds;
   i32x4 ra, rb;                       // codes of this tile's first rows
@@ -151,10 +161,8 @@ struct Work {
 };
 
 // multiplies one slice; `other` is what is done beside it, in n shares
-template <bool EXACT, int BM, int BN, class F>
-__device__ __forceinline__ void multiply(Work<EXACT, BM, BN>& w, const Slice<Tile<BM, BN>>& f,
-                                         f32x16 (&acc)[Tile<BM, BN>::FM][Tile<BM, BN>::FN], F other) {
-  using T = Tile<BM, BN>;
+template <bool EXACT, class T, class F>
+__device__ __forceinline__ void multiply(Work<T>& w, const Slice<T>& f, f32x16 (&acc)[T::FM][T::FN], F other) {
   if constexpr (!EXACT) {
 #pragma unroll
     for (int k = 0; k < T::NM; ++k) {
@@ -205,9 +213,9 @@ __device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t a, uint32_t b
 
 // One tile of C, or, with g.splits > 1, of one split's sum over its share of k
 // (OUT is float then, C a workspace of g.splits matrices).
-template <class OUT, bool EXACT, int BM, int BN>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArgs g) {
-  using T = Tile<BM, BN>;
+template <class OUT, bool EXACT, int BM, int BN, int SA, int SB>
+__global__ __launch_bounds__(256) void fp8_mm_kernel(Fp8MmArgs g) {
+  using T = Tile<BM, BN, SA, SB>;
   __shared__ __align__(16) char lds[T::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_pm = (g.M + BM - 1) / BM, n_pn = (g.N + BN - 1) / BN;
@@ -234,7 +242,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
   const int wm = (wave >> 1) * T::WM, wn = (wave & 1) * T::WN;
   const int r32 = lane & 31;
 
-  Work<EXACT, BM, BN> w;
+  Work<T> w;
   w.lds = lds;
   w.ra = buffer_words(g.A.codes + (int64_t)m0 * g.A.ld);
   w.rb = buffer_words(g.B.codes + (int64_t)n0 * g.B.ld);
@@ -288,14 +296,18 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) w.sb[j] = rotate(*(const uint32_t*)psb[j], turn_bits(0));
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < T::SB || t < T::SA - 1; ++t) {
       const uint32_t k = at_k(t), back = w.back(k, g.K);
+      if (t < T::SA - 1) {
 #pragma unroll
-      for (int i = 0; i < T::LA; ++i) w.load_a(i, k, back, t * T::A_STAGE);
+        for (int i = 0; i < T::LA; ++i) w.load_a(i, k, back, t * T::A_STAGE);
+      }
+      if (t < T::SB) {
 #pragma unroll
-      for (int i = 0; i < T::LB; ++i) w.load_b(i, k, back, t * T::B_STAGE);
+        for (int i = 0; i < T::LB; ++i) w.load_b(i, k, back, t * T::B_STAGE);
+      }
     }
-    step_barrier<T::LA + T::LB>();
+    step_barrier<(T::SA - 2) * T::LA + (T::SB - 1) * T::LB>();
     if (tail && nk == 1) {
       w.cut(lds, tail, 0, 0, tid);
       __syncthreads();
@@ -304,10 +316,9 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
     for (int x = 0; x < T::NR; ++x) w.read(x, 0, 0, 0, f0);
   }
   uint32_t na[T::FM] = {}, nb[T::FN] = {};
-  uint32_t a_this = 0, a_next = T::A_STAGE, a_free = 2 * T::A_STAGE;
+  uint32_t a_free = (T::SA - 1) * T::A_STAGE, a_this = 0, a_next = T::A_STAGE, b_this = 0, b_next = T::B_STAGE;
   for (int t = 0; t < nk; ++t) {
-    const uint32_t b_this = t & 1 ? T::B_STAGE : 0, b_next = T::B_STAGE - b_this;
-    const uint32_t k2 = at_k(t + 2), back = w.back(k2, g.K);
+    const uint32_t ka = at_k(t + T::SA - 1), kb = at_k(t + T::SB), back_a = w.back(ka, g.K), back_b = w.back(kb, g.K);
     const uint32_t new_word = (t & 3) == 3 ? ~0u : 0u;
     const uint32_t bits = turn_bits(t + 1);
     __builtin_amdgcn_sched_barrier(0);
@@ -317,8 +328,8 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) nb[j] = *(const uint32_t*)(psb[j] + t + 4);
     }
-    multiply<EXACT, BM, BN>(w, f0, acc, [&](int k, int N) {
-      IRIS_SHARE(i, T::LA, k, N) w.load_a(i, k2, back, a_free);
+    multiply<EXACT>(w, f0, acc, [&](int k, int N) {
+      IRIS_SHARE(i, T::LA, k, N) w.load_a(i, ka, back_a, a_free);
       IRIS_SHARE(x, T::NR, k, N) w.read(x, 1, a_this, b_this, f1);
     });
     // the matrix instructions above stay above (the compiler would move them
@@ -327,7 +338,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
     for (int i = 0; i < T::FM; ++i)
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) asm volatile("" : "+a"(acc[i][j]));
-    step_barrier<T::LA>();
+    step_barrier<T::under_way()>();
     if (tail && t + 2 == nk) {
       w.cut(lds, tail, a_next, b_next, tid);
       __syncthreads();
@@ -338,8 +349,8 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) asm volatile("" : "+v"(nb[j]));
     __builtin_amdgcn_sched_barrier(0);
-    multiply<EXACT, BM, BN>(w, f1, acc, [&](int k, int N) {
-      IRIS_SHARE(i, T::LB, k, N) w.load_b(i, k2, back, b_this);
+    multiply<EXACT>(w, f1, acc, [&](int k, int N) {
+      IRIS_SHARE(i, T::LB, k, N) w.load_b(i, kb, back_b, b_this);
       IRIS_SHARE(x, T::NR, k, N) w.read(x, 0, a_next, b_next, f0);
       // the next step's scale bytes, each behind its last use
       const int last = k - (N - T::NM);
@@ -350,10 +361,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void fp8_mm_kernel(Fp8MmArg
       for (int j = 0; j < T::FN; ++j)
         if (last == T::NM - 1) w.sb[j] = choose(new_word, rotate(nb[j], bits), w.sb[j] >> 8);
     });
-    const uint32_t a_was = a_this;
+    a_free = a_this;
     a_this = a_next;
-    a_next = a_free;
-    a_free = a_was;
+    a_next = a_next == (T::SA - 1) * T::A_STAGE ? 0 : a_next + T::A_STAGE;
+    b_this = b_next;
+    b_next = b_next == (T::SB - 1) * T::B_STAGE ? 0 : b_next + T::B_STAGE;
   }
 
   // Epilogue, 32 rows of a wave at a time: the accumulators turn around in LDS
@@ -419,12 +431,12 @@ __global__ __launch_bounds__(256) void fp8_mm_join_kernel(Fp8MmArgs g, const flo
                 bias && g.bias_along_m ? widen(bias[m]) : 0.0f, bn, v);
 }
 
-template <class OUT, bool EXACT, int BM, int BN>
+template <class OUT, bool EXACT, int BM, int BN, int SA, int SB>
 hipError_t launch(const Fp8MmArgs& a, hipStream_t s) {
   const int64_t tiles = ((int64_t)a.M + BM - 1) / BM * (((int64_t)a.N + BN - 1) / BN) * a.splits;
   const int64_t round = kPatch * kXcds;
   const uint32_t grid = (uint32_t)((tiles + round - 1) / round * round);
-  hipLaunchKernelGGL((fp8_mm_kernel<OUT, EXACT, BM, BN>), dim3(grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((fp8_mm_kernel<OUT, EXACT, BM, BN, SA, SB>), dim3(grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -435,14 +447,14 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
   g.splits = plan.splits;
   g.split_steps = plan.split_steps;
   if (plan.splits == 1)
-    return plan.tile == 256 ? launch<OUT, EXACT, 256, 256>(g, s) : launch<OUT, EXACT, 128, 128>(g, s);
+    return plan.tile == 256 ? launch<OUT, EXACT, 256, 256, 3, 2>(g, s) : launch<OUT, EXACT, 128, 128, 3, 2>(g, s);
   const int64_t ldp = ((int64_t)a.N + 3) / 4 * 4;
   g.C = ws;
-  g.ldc = ldp;
+  g.ldc = (int32_t)ldp;
   g.vec = 1;
   g.bias = nullptr;
   g.accumulate = 0;
-  hipError_t e = launch<float, EXACT, 128, 128>(g, s);
+  hipError_t e = launch<float, EXACT, 128, 128, 3, 2>(g, s);
   if (e != hipSuccess) return e;
   g = a;
   g.splits = plan.splits;

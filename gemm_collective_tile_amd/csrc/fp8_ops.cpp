@@ -102,7 +102,7 @@ bool rows16(const void* x, int64_t ld, int32_t type) {
 
 Fp8Mat mat(const iris_fp8_t* q) {
   if (!q) return Fp8Mat{};
-  return Fp8Mat{(uint8_t*)q->codes, (uint8_t*)q->scales, q->ld, q->ld_scales};
+  return Fp8Mat{(uint8_t*)q->codes, (uint8_t*)q->scales, (int32_t)q->ld, (int32_t)q->ld_scales};
 }
 
 int ready() {
@@ -191,7 +191,7 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
   } else {
     if ((st = check_plain(x, x_type, true, ldx, rows, cols, "x"))) return st;
     a.x = x;
-    a.ldx = ldx;
+    a.ldx = (int32_t)ldx;
     a.x_type = x_type;
     a.vec = rows16(x, ldx, x_type);
   }
@@ -237,13 +237,13 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   iris::Fp8MmArgs a{};
   a.A = mat(A);
   a.B = mat(B);
-  a.b_block = B->block;
+  a.b_block = (uint8_t)B->block;
   a.bias = bias;
   a.bias_along_m = (flags & IRIS_FLAG_BIAS_ALONG_M) ? 1 : 0;
   a.accumulate = (flags & IRIS_FLAG_ACCUMULATE) ? 1 : 0;
   a.C = C;
-  a.c_type = c_type;
-  a.ldc = ldc;
+  a.c_type = (uint8_t)c_type;
+  a.ldc = (int32_t)ldc;
   a.vec = rows16(C, ldc, c_type);
   a.M = (int)M;
   a.N = (int)N;
@@ -271,8 +271,8 @@ int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris
   iris::Fp8SwigluArgs a{};
   a.gate = gate;
   a.up = up;
-  a.ld_gate = ld_gate;
-  a.ld_up = ld_up;
+  a.ld_gate = (int32_t)ld_gate;
+  a.ld_up = (int32_t)ld_up;
   a.type = type;
   a.vec = rows16(gate, ld_gate, type) && rows16(up, ld_up, type);
   a.h = mat(h);
@@ -307,7 +307,7 @@ int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const ir
   if ((st = ready())) return st;
   iris::Fp8SwigluBwdArgs a{};
   a.dh = dh;
-  a.ld_dh = ld_dh;
+  a.ld_dh = (int32_t)ld_dh;
   a.type = type;
   a.vec = rows16(dh, ld_dh, type);
   a.gate8 = mat(gate_kept);

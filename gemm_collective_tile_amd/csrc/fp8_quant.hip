@@ -46,25 +46,33 @@ __device__ __forceinline__ void put_row_block(const Fp8Mat& q, const RowPlace& p
 }
 
 template <class T, bool WHOLE>
-__global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8QuantArgs a, FastDiv nkb) {
-  const RowPlace p(a.rows, nkb);
+__global__ __launch_bounds__(kThreads) void fp8_rows_kernel(const T* x, int ldx, int rows, int cols, Fp8Mat q, FastDiv nkb) {
+  const RowPlace p(rows, nkb);
   float v[16];
-  load_piece<WHOLE>((const T*)a.x + (int64_t)p.row * a.ldx, 0, p.col, a.cols, p.on, v);
-  put_row_block<WHOLE>(a.q, p, a.cols, v);
+  load_piece<WHOLE>(x + (int64_t)p.row * ldx, 0, p.col, cols, p.on, v);
+  put_row_block<WHOLE>(q, p, cols, v);
 }
 
-template <class T, bool WHOLE>
-__global__ __launch_bounds__(kThreads) void fp8_swiglu_kernel(Fp8SwigluArgs a, FastDiv nkb) {
-  const RowPlace p(a.rows, nkb);
+// KEPT: what the kernel is given of the matrices that keep gate and up (an empty
+// struct if they are not wanted)
+struct Kept {
+  Fp8Mat gate, up;
+};
+struct NotKept {};
+
+template <class T, bool WHOLE, class KEPT>
+__global__ __launch_bounds__(kThreads) void fp8_swiglu_kernel(const T* gate, const T* up, int ld_gate, int ld_up, int rows,
+                                                              int cols, Fp8Mat out, FastDiv nkb, KEPT kept) {
+  const RowPlace p(rows, nkb);
   float g[16], u[16], h[16];
-  load_piece<WHOLE>((const T*)a.gate + (int64_t)p.row * a.ld_gate, 0, p.col, a.cols, p.on, g);
-  load_piece<WHOLE>((const T*)a.up + (int64_t)p.row * a.ld_up, 0, p.col, a.cols, p.on, u);
+  load_piece<WHOLE>(gate + (int64_t)p.row * ld_gate, 0, p.col, cols, p.on, g);
+  load_piece<WHOLE>(up + (int64_t)p.row * ld_up, 0, p.col, cols, p.on, u);
 #pragma unroll
   for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
-  put_row_block<WHOLE>(a.h, p, a.cols, h);
-  if (a.gate8.codes) {
-    put_row_block<WHOLE>(a.gate8, p, a.cols, g);
-    put_row_block<WHOLE>(a.up8, p, a.cols, u);
+  put_row_block<WHOLE>(out, p, cols, h);
+  if constexpr (sizeof(KEPT) == sizeof(Kept)) {
+    put_row_block<WHOLE>(kept.gate, p, cols, g);
+    put_row_block<WHOLE>(kept.up, p, cols, u);
   }
 }
 
@@ -349,11 +357,14 @@ hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
   const FastDiv d = FastDiv::make(nkb);
   if (a.block == 1 && !a.qt.codes) {
     const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads)), block(kThreads);
+#define ROWS(T) \
+  hipLaunchKernelGGL((fp8_rows_kernel<T, WHOLE>), grid, block, 0, s, (const T*)a.x, a.ldx, a.rows, a.cols, a.q, d)
     switch (a.x_type) {
-      case T_FP16: hipLaunchKernelGGL((fp8_rows_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
-      case T_BF16: hipLaunchKernelGGL((fp8_rows_kernel<bf16, WHOLE>), grid, block, 0, s, a, d); break;
-      default: hipLaunchKernelGGL((fp8_rows_kernel<float, WHOLE>), grid, block, 0, s, a, d); break;
+      case T_FP16: ROWS(f16); break;
+      case T_BF16: ROWS(bf16); break;
+      default: ROWS(float); break;
     }
+#undef ROWS
     return hipGetLastError();
   }
   const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<16>::T);
@@ -370,7 +381,13 @@ template <class T, bool WHOLE>
 hipError_t swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
   const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads));
-  hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE>), grid, dim3(kThreads), 0, s, a, FastDiv::make(nkb));
+  const FastDiv d = FastDiv::make(nkb);
+  if (a.gate8.codes)
+    hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE, Kept>), grid, dim3(kThreads), 0, s, (const T*)a.gate, (const T*)a.up,
+                       a.ld_gate, a.ld_up, a.rows, a.cols, a.h, d, Kept{a.gate8, a.up8});
+  else
+    hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE, NotKept>), grid, dim3(kThreads), 0, s, (const T*)a.gate,
+                       (const T*)a.up, a.ld_gate, a.ld_up, a.rows, a.cols, a.h, d, NotKept{});
   return hipGetLastError();
 }
 
