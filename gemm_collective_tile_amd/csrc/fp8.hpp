@@ -26,7 +26,7 @@ struct Fp8MmArgs {
 // How a product runs: its tile, and over how many workgroups the contraction of
 // one tile is split (their sums go through ws_bytes of workspace).
 struct Fp8MmPlan {
-  int32_t tile = 256, splits = 1, split_steps = 0;
+  int32_t bm = 256, bn = 256, splits = 1, split_steps = 0;
   size_t ws_bytes = 0;
 };
 Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32);

@@ -77,9 +77,9 @@ __device__ __forceinline__ i32x4 buffer_words(const void* p) {
                (int)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu), (int)0xfffffff0u, kRsrcWord3};
 }
 
-template <int BM, int BN, int SA_, int SB_>
+template <int BM, int BN>
 struct Tile {
-  static constexpr int SA = SA_, SB = SB_;             // LDS stages of A and of B
+  static constexpr int SA = 3, SB = 2;                 // LDS stages of A and of B
   static constexpr int WM = BM / 2, WN = BN / 2;       // a wave's part
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int A_STAGE = BM * kBK, B_STAGE = BN * kBK;
@@ -213,9 +213,9 @@ __device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t a, uint32_t b
 
 // One tile of C, or, with g.splits > 1, of one split's sum over its share of k
 // (OUT is float then, C a workspace of g.splits matrices).
-template <class OUT, bool EXACT, int BM, int BN, int SA, int SB>
+template <class OUT, bool EXACT, int BM, int BN>
 __global__ __launch_bounds__(256) void fp8_mm_kernel(Fp8MmArgs g) {
-  using T = Tile<BM, BN, SA, SB>;
+  using T = Tile<BM, BN>;
   __shared__ __align__(16) char lds[T::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_pm = (g.M + BM - 1) / BM, n_pn = (g.N + BN - 1) / BN;
@@ -431,13 +431,20 @@ __global__ __launch_bounds__(256) void fp8_mm_join_kernel(Fp8MmArgs g, const flo
                 bias && g.bias_along_m ? widen(bias[m]) : 0.0f, bn, v);
 }
 
-template <class OUT, bool EXACT, int BM, int BN, int SA, int SB>
+template <class OUT, bool EXACT, int BM, int BN>
 hipError_t launch(const Fp8MmArgs& a, hipStream_t s) {
   const int64_t tiles = ((int64_t)a.M + BM - 1) / BM * (((int64_t)a.N + BN - 1) / BN) * a.splits;
   const int64_t round = kPatch * kXcds;
   const uint32_t grid = (uint32_t)((tiles + round - 1) / round * round);
-  hipLaunchKernelGGL((fp8_mm_kernel<OUT, EXACT, BM, BN, SA, SB>), dim3(grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((fp8_mm_kernel<OUT, EXACT, BM, BN>), dim3(grid), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+
+template <class OUT, bool EXACT>
+hipError_t small_tile(const Fp8MmArgs& a, const Fp8MmPlan& plan, hipStream_t s) {
+  return plan.bn == 128   ? launch<OUT, EXACT, 128, 128>(a, s)
+         : plan.bm == 128 ? launch<OUT, EXACT, 128, 64>(a, s)
+                          : launch<OUT, EXACT, 64, 64>(a, s);
 }
 
 template <class OUT>
@@ -447,14 +454,14 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
   g.splits = plan.splits;
   g.split_steps = plan.split_steps;
   if (plan.splits == 1)
-    return plan.tile == 256 ? launch<OUT, EXACT, 256, 256, 3, 2>(g, s) : launch<OUT, EXACT, 128, 128, 3, 2>(g, s);
+    return plan.bm == 256 ? launch<OUT, EXACT, 256, 256>(g, s) : small_tile<OUT, EXACT>(g, plan, s);
   const int64_t ldp = ((int64_t)a.N + 3) / 4 * 4;
   g.C = ws;
   g.ldc = (int32_t)ldp;
   g.vec = 1;
   g.bias = nullptr;
   g.accumulate = 0;
-  hipError_t e = launch<float, EXACT, 128, 128, 3, 2>(g, s);
+  hipError_t e = small_tile<float, EXACT>(g, plan, s);
   if (e != hipSuccess) return e;
   g = a;
   g.splits = plan.splits;
@@ -467,34 +474,50 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
 
 }  // namespace
 
-// The plan with the least predicted time. Times in us, measured on MI355X (16-bit
-// C / fp32 C): a step of k takes a CU 1.55 / 2.85 on a 256 x 256 tile, 0.58 /
-// 0.95 on one 128 x 128 tile and 1.1 / 1.8 on two at a time; a workgroup's start
-// and epilogue take 6; splitting the contraction costs a launch (3) and each
-// split's sums written and read (3 TB/s at these sizes). So 128 x 128 wins where
-// there are too few large tiles for the CUs: 512 x 4096 x 4096 takes 24.5 us
-// with it and 52 with 256 x 256, 2048 x 11008 x 4096 104 and 115, 4096 x 4096 x
-// 11008 186 and 152. Splitting wins where there are too few small ones as well:
-// 256 x 4096 x 11008 takes 28 us in four splits and 54 in one.
+// The plan with the least predicted time, from times in us measured on MI355X: a
+// step of k on a tile with a CU to itself and on two tiles that share one, for
+// 16-bit and for fp32 C; a workgroup's start and epilogue. Splitting the
+// contraction costs a launch (2.5) and each split's sums written and read (5
+// TB/s at these sizes, in the last-level cache). What it decides, kernel times:
+//   300 x 800 x 800      256: 35 us   128: 8.6   128 x 64: 7.1   64: 5.8
+//   512 x 4096 x 4096         52          24.6             20.8      20.6
+//   2048 x 4096 x 4096        60          41.8
+//   2048 x 11008 x 4096      115         104
+//   4096 x 4096 x 11008      152         186
+//   100 x 800 x 4096     64: 15.9 in one, 12.8 in two, 9.2 in four splits
+// More LDS stages (five of each operand) leave all of these as they are: small
+// tiles are bound by the chain of a step (operand read, product, barrier),
+// larger ones by a CU's load path, 55 GB/s.
 Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32) {
-  const double step256 = fp32 ? 2.85 : 1.55, step128 = fp32 ? 0.95 : 0.58, step128x2 = fp32 ? 1.8 : 1.1, ends = 6.0;
-  const int64_t big = (M + 255) / 256 * ((N + 255) / 256), small = (M + 127) / 128 * ((N + 127) / 128);
-  const int64_t steps = (K + kBK - 1) / kBK;
+  static const struct {
+    int bm, bn;
+    double alone[2], shared[2], ends;
+  } tiles[] = {{128, 128, {0.60, 0.95}, {1.15, 1.80}, 4.5},
+               {128, 64, {0.46, 0.78}, {0.74, 1.16}, 4.0},
+               {64, 64, {0.42, 0.61}, {0.55, 0.87}, 3.0}};
+  const double step256 = fp32 ? 2.85 : 1.55, ends256 = 6.0;
+  const int64_t big = (M + 255) / 256 * ((N + 255) / 256), steps = (K + kBK - 1) / kBK;
   Fp8MmPlan best;
-  double least = (double)((big + kCus - 1) / kCus) * (steps * step256 + ends);
-  for (int64_t want = 1; want <= 16 && (want == 1 || small * want <= 2 * kCus); ++want) {
-    const int64_t share = want == 1 ? steps : ((steps + want - 1) / want + 3) & ~(int64_t)3;
-    const int64_t n = share > 0 ? (steps + share - 1) / share : 1;   // splits
-    if (n != want) continue;
-    const double wgs = (double)small * n;
-    double t = wgs <= kCus ? share * step128 + ends : std::max(1.0, wgs / (2 * kCus)) * (share * step128x2 + ends);
-    if (n > 1) t += 3.0 + (double)n * M * N * 8 / 3e6;
-    if (t >= least) continue;
-    least = t;
-    best.tile = 128;
-    best.splits = (int)n;
-    best.split_steps = (int)share;
-    best.ws_bytes = n > 1 ? (size_t)n * M * ((N + 3) / 4 * 4) * 4 : 0;
+  double least = (double)((big + kCus - 1) / kCus) * (steps * step256 + ends256);
+  for (const auto& tile : tiles) {
+    const int64_t n_tiles = (M + tile.bm - 1) / tile.bm * ((N + tile.bn - 1) / tile.bn);
+    for (int64_t want = 1; want <= 16 && (want == 1 || n_tiles * want <= 2 * kCus); ++want) {
+      // shares are whole words of scale bytes
+      const int64_t share = want == 1 ? steps : ((steps + want - 1) / want + 3) & ~(int64_t)3;
+      const int64_t n = share > 0 ? (steps + share - 1) / share : 1;   // splits
+      if (n != want) continue;
+      const double wgs = (double)n_tiles * n;
+      double t = wgs <= kCus ? share * tile.alone[fp32] + tile.ends
+                             : std::max(1.0, wgs / (2 * kCus)) * (share * tile.shared[fp32] + tile.ends);
+      if (n > 1) t += 2.5 + (double)n * M * N * 8 / 5e6;
+      if (t >= least) continue;
+      least = t;
+      best.bm = tile.bm;
+      best.bn = tile.bn;
+      best.splits = (int)n;
+      best.split_steps = (int)share;
+      best.ws_bytes = n > 1 ? (size_t)n * M * ((N + 3) / 4 * 4) * 4 : 0;
+    }
   }
   return best;
 }

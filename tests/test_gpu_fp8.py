@@ -213,6 +213,54 @@ def test_mm(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,block", [("fp16", 128), ("bf16", 1), ("fp32", 1)])
+@pytest.mark.parametrize("M,N,K", [(3900, 4000, 2100), (1900, 2100, 1500), (1000, 1300, 2000), (500, 1000, 700)])
+def test_mm_of_each_tile(M, N, K, dtype, block):
+    """Sizes that the plan gives 256 x 256, 128 x 128, 128 x 64 and 64 x 64 tiles, ragged in all three lengths."""
+    note(f"mm tiles {M}x{N}x{K} {dtype}")
+    A, B = made(sample(M, K, 1)), made(sample(N, K, 2, 0.0) / np.sqrt(K), block)
+    a, b = ref.values(*parts(A)), ref.values(*parts(B), block)
+    C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+    il.iris_fp8_mm(C, A, B)
+    check_product(C, a, b, None, None, dtype, (M, N, K, dtype))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Matrices of more than 4 GiB: their last rows are what the same rows alone give."""
+    rows, cols = 270_000, 16_384                      # 4.4e9 values
+    note("offsets past 32 bits: quantize")
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[:1000].normal_()
+    x[-1000:].normal_()
+    x[1000:-1000] = 0.5
+    q, qt = il.iris_fp8_empty(rows, cols), il.iris_fp8_empty(cols, rows)
+    il.iris_fp8_quantize(x, q, qt)
+    last = 304                                        # from a multiple of 128 on
+    start = rows - last
+    start -= start % 128
+    p, pt = il.iris_fp8_empty(rows - start, cols), il.iris_fp8_empty(cols, rows - start)
+    il.iris_fp8_quantize(x[start:], p, pt)
+    for big, small in ((q.codes[start:], p.codes), (q.scales[start:], p.scales), (qt.codes[:, start:], pt.codes),
+                       (qt.scales[:, start // 128:], pt.scales)):
+        assert torch.equal(big.contiguous().view(torch.uint8), small.contiguous().view(torch.uint8))
+    del qt, pt, x
+    note("offsets past 32 bits: mm")
+    B = made(sample(72, cols, 2) / 128, 128)
+    C, tail = (torch.empty((n, 72), dtype=torch.float16, device="cuda") for n in (rows, rows - start))
+    il.iris_fp8_mm(C, q, B)
+    il.iris_fp8_mm(tail, p, B)
+    check = C[start:].float()
+    assert torch.allclose(check, tail.float(), rtol=2.0 ** -9, atol=2.0 ** -9 * float(check.abs().max()))
+    few = torch.empty((40, rows), dtype=torch.bfloat16, device="cuda")
+    part = torch.empty((40, rows - start), dtype=torch.bfloat16, device="cuda")
+    a = made(sample(40, cols, 3))
+    il.iris_fp8_mm(few, a, q)                         # as the many rows of B
+    il.iris_fp8_mm(part, a, p)
+    assert torch.equal(few[:, start:], part)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 300, 257), (20, 130, 520), (70, 200, 300), (260, 390, 260), (600, 512, 384)])
 def test_mm_accumulate_bias_along_m_and_pitch(M, N, K):
     for dtype in DT:
