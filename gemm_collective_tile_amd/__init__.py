@@ -206,11 +206,14 @@ def _cfg(config) -> Optional[ctypes.pointer]:
     return ctypes.pointer(config._c())
 
 
+# The current stream's handle; building the torch.cuda.Stream object around it
+# costs 3 us a call on the host.
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream):
     if stream is None:
-        # the current stream's handle; building the torch.cuda.Stream object
-        # around it costs 3 us a call on the host
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -504,8 +507,9 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
     or q_t (cols, rows), x transposed, both in one pass. x is a float16, bfloat16
     or float32 tensor, or an Fp8 matrix (then only q_t, blocks of 1 x 128)."""
     from8 = x.__class__ is Fp8
-    shape = x.shape if from8 else _shape2(x, "x")
-    rows, cols = shape
+    if not from8 and (not isinstance(x, torch.Tensor) or x.dim() != 2):
+        _shape2(x, "x")
+    shape = rows, cols = x.shape
     qp = None if q is None else _fp8(q, (rows, cols), "q")
     qtp = None if q_t is None else _fp8(q_t, (cols, rows), "q_t")
     if from8:
@@ -513,7 +517,8 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
     else:
         ptr, kind, ld = _plain(x, "x", _FP8_TYPES, rows, cols)
         x8 = None
-    st = _lib.iris_fp8_quantize(qp, qtp, ptr, kind, ld, x8, rows, cols, _stream(stream))
+    st = _lib.iris_fp8_quantize(qp, qtp, ptr, kind, ld, x8, rows, cols,
+                                _current_stream(_current_device()) if stream is None else _stream(stream))
     if st:
         _check(st)
 
@@ -544,9 +549,9 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
         if not bias.is_cuda:
             raise ValueError("bias must be on a GPU")
         bias_ptr = bias.data_ptr()
-    ws, wsb = _ws(workspace)
+    ws, wsb = (None, 0) if workspace is None else _ws(workspace)
     st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8(A, A.shape, "A"), _fp8(B, B.shape, "B"), bias_ptr, M, N, K, flags, ws,
-                          wsb, _stream(stream))
+                          wsb, _current_stream(_current_device()) if stream is None else _stream(stream))
     if st:
         _check(st)
 
@@ -555,7 +560,9 @@ def iris_fp8_swiglu(h: Fp8, gate, up, gate_kept: Optional[Fp8] = None, up_kept: 
                     stream=None) -> None:
     """h = silu(gate) * up in 8 bits; gate, up (rows, cols) float16 or bfloat16
     (views of one matrix will do); gate_kept and up_kept receive them in 8 bits."""
-    shape = rows, cols = tuple(_shape2(gate, "gate"))
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
+        _shape2(gate, "gate")
+    shape = rows, cols = gate.shape
     if not isinstance(up, torch.Tensor) or up.shape != shape:
         _want_shape(up, shape, "up")
     if up.dtype != gate.dtype:
@@ -566,7 +573,8 @@ def iris_fp8_swiglu(h: Fp8, gate, up, gate_kept: Optional[Fp8] = None, up_kept: 
     ukp = _fp8(up_kept, shape, "up_kept") if kept else None
     gp, kind, gld = _plain(gate, "gate", _FP8_HALVES, rows, cols)
     up_ptr, _, uld = _plain(up, "up", _FP8_HALVES, rows, cols)
-    st = _lib.iris_fp8_swiglu(hp, gkp, ukp, gp, up_ptr, kind, gld, uld, rows, cols, _stream(stream))
+    st = _lib.iris_fp8_swiglu(hp, gkp, ukp, gp, up_ptr, kind, gld, uld, rows, cols,
+                              _current_stream(_current_device()) if stream is None else _stream(stream))
     if st:
         _check(st)
 
@@ -576,7 +584,9 @@ def iris_fp8_swiglu_bwd(dgate: Fp8, dup: Fp8, dh, gate_kept: Fp8, up_kept: Fp8, 
     """Backward pass of iris_fp8_swiglu at the kept gate and up: dgate, dup
     (rows, cols) and, if given, dgate_t, dup_t and the recomputed h_t (cols,
     rows), all in 8 bits; dh (rows, cols) float16 or bfloat16."""
-    shape = rows, cols = tuple(_shape2(dh, "dh"))
+    if not isinstance(dh, torch.Tensor) or dh.dim() != 2:
+        _shape2(dh, "dh")
+    shape = rows, cols = dh.shape
     turned = (cols, rows)
     st = _lib.iris_fp8_swiglu_bwd(
         _fp8(dgate, shape, "dgate"), _fp8(dup, shape, "dup"),
