@@ -26,13 +26,26 @@ struct Fp8MmArgs {
 // How a product runs: its tile, and over how many workgroups the contraction of
 // one tile is split (their sums go through ws_bytes of workspace).
 struct Fp8MmPlan {
-  int32_t bm = 256, bn = 256, splits = 1, split_steps = 0;
+  int32_t bm = 256, bn = 256, splits = 1, split_steps = 0;   // bm 0: the kernel for few rows
   size_t ws_bytes = 0;
 };
 Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32);
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t s);
-// at most kFp8FewRows rows of A
-constexpr int kFp8FewRows = 64;
+constexpr int kFp8Cus = 256;   // compute units of the chip
+// Few rows of A (at most kFp8FewRows): blocks of 16 rows of B for a workgroup. From
+// 17 rows of A on its time goes with what a CU loads, B's rows and A's once
+// for every workgroup, so the least of (workgroups a CU gets) * (blocks of both).
+constexpr int kFp8AlwaysFew = 64, kFp8FewRows = 96;
+inline int64_t fp8_few_loads(int64_t M, int64_t N, int nb) {
+  return ((N + 16 * nb - 1) / (16 * nb) + kFp8Cus - 1) / kFp8Cus * (16 * nb + M);
+}
+inline int fp8_few_blocks(int64_t M, int64_t N) {
+  int best = 1;
+  if (M > 16)
+    for (int nb = 2; nb <= 3; ++nb)
+      if (fp8_few_loads(M, N, nb) < fp8_few_loads(M, N, best)) best = nb;
+  return best;
+}
 hipError_t launch_fp8_mm_few(const Fp8MmArgs& a, hipStream_t s);
 
 struct Fp8QuantArgs {

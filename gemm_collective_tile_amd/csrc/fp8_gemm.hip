@@ -58,7 +58,6 @@ namespace {
 
 constexpr int kBK = 128;
 constexpr int kGroupM = 8;     // tile rows of a patch that one XCD works on
-constexpr int kCus = 256;      // of the chip
 constexpr int kPatch = 32;     // tiles of a patch: the workgroups of an XCD
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -485,6 +484,12 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
 //   2048 x 11008 x 4096      115         104
 //   4096 x 4096 x 11008      152         186
 //   100 x 800 x 4096     64: 15.9 in one, 12.8 in two, 9.2 in four splits
+// Up to 96 rows of A the kernel for few rows competes, by what a CU loads at 66 GB/s
+// (with its occupied CUs; the chains above hide none of it):
+//   65 x 4096 x 4096     few 8.6, tiles 12.5      96 x 11008 x 4096 (fp32)   16.2, 26.8
+//   65 x 800 x 11008         14.0       11.9      96 x 2048 x 8192           14.5, 13.4
+// From 97 rows on its gain is gone (128 x 8192 x 8192: 23.8, 24.2; 128 x 4096 x 11008:
+// 24.9, 22.5), and up to 64 rows it loses by 4 % at most but where B has few rows.
 // More LDS stages (five of each operand) leave all of these as they are: small
 // tiles are bound by the chain of a step (operand read, product, barrier),
 // larger ones by a CU's load path, 55 GB/s.
@@ -498,17 +503,21 @@ Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32) {
   const double step256 = fp32 ? 2.85 : 1.55, ends256 = 6.0;
   const int64_t big = (M + 255) / 256 * ((N + 255) / 256), steps = (K + kBK - 1) / kBK;
   Fp8MmPlan best;
-  double least = (double)((big + kCus - 1) / kCus) * (steps * step256 + ends256);
+  if (M <= kFp8AlwaysFew) {
+    best.bm = 0;
+    return best;
+  }
+  double least = (double)((big + kFp8Cus - 1) / kFp8Cus) * (steps * step256 + ends256);
   for (const auto& tile : tiles) {
     const int64_t n_tiles = (M + tile.bm - 1) / tile.bm * ((N + tile.bn - 1) / tile.bn);
-    for (int64_t want = 1; want <= 16 && (want == 1 || n_tiles * want <= 2 * kCus); ++want) {
+    for (int64_t want = 1; want <= 16 && (want == 1 || n_tiles * want <= 2 * kFp8Cus); ++want) {
       // shares are whole words of scale bytes
       const int64_t share = want == 1 ? steps : ((steps + want - 1) / want + 3) & ~(int64_t)3;
       const int64_t n = share > 0 ? (steps + share - 1) / share : 1;   // splits
       if (n != want) continue;
       const double wgs = (double)n_tiles * n;
-      double t = wgs <= kCus ? share * tile.alone[fp32] + tile.ends
-                             : std::max(1.0, wgs / (2 * kCus)) * (share * tile.shared[fp32] + tile.ends);
+      double t = wgs <= kFp8Cus ? share * tile.alone[fp32] + tile.ends
+                             : std::max(1.0, wgs / (2 * kFp8Cus)) * (share * tile.shared[fp32] + tile.ends);
       if (n > 1) t += 2.5 + (double)n * M * N * 8 / 5e6;
       if (t >= least) continue;
       least = t;
@@ -518,6 +527,10 @@ Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32) {
       best.split_steps = (int)share;
       best.ws_bytes = n > 1 ? (size_t)n * M * ((N + 3) / 4 * 4) * 4 : 0;
     }
+  }
+  if (M <= kFp8FewRows && fp8_few_loads(M, N, fp8_few_blocks(M, N)) * K / 66e3 + 2.5 < least) {
+    best = {};
+    best.bm = 0;
   }
   return best;
 }

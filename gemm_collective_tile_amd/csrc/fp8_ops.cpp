@@ -205,7 +205,7 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
 }
 
 size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (check_mm_dims(M, N, K) || M <= iris::kFp8FewRows || N == 0) return 0;
+  if (check_mm_dims(M, N, K) || M == 0 || N == 0) return 0;
   return std::max(iris::fp8_mm_plan(M, N, K, false).ws_bytes, iris::fp8_mm_plan(M, N, K, true).ws_bytes);
 }
 
@@ -226,8 +226,7 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
     return fail(IRIS_ERR_ALIGNMENT, "B: scales must be 4-byte aligned and ld_scales a multiple of 4");
   if (bias && (uintptr_t)bias % type_bytes(c_type) != 0) return fail(IRIS_ERR_ALIGNMENT, "bias is not aligned to its type");
   if (M == 0 || N == 0) return IRIS_OK;
-  iris::Fp8MmPlan plan;
-  if (M > iris::kFp8FewRows) plan = iris::fp8_mm_plan(M, N, K, c_type == IRIS_TYPE_FP32);
+  const iris::Fp8MmPlan plan = iris::fp8_mm_plan(M, N, K, c_type == IRIS_TYPE_FP32);
   if (workspace && workspace_bytes < plan.ws_bytes)
     return fail(IRIS_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, plan.ws_bytes);
   if (workspace && (uintptr_t)workspace % 256 != 0) return fail(IRIS_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
@@ -248,7 +247,7 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
-  const hipError_t e = M <= iris::kFp8FewRows ? iris::launch_fp8_mm_few(a, (hipStream_t)stream)
+  const hipError_t e = plan.bm == 0 ? iris::launch_fp8_mm_few(a, (hipStream_t)stream)
                                               : iris::launch_fp8_mm(a, plan, workspace, (hipStream_t)stream);
   return launched(e, "iris_fp8_mm");
 }

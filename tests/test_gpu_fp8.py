@@ -226,6 +226,26 @@ def test_mm_of_each_tile(M, N, K, dtype, block):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,block", [("fp16", 128), ("bf16", 1), ("fp32", 128)])
+@pytest.mark.parametrize("M", [1, 20, 48, 63, 66, 90])
+def test_mm_of_few_rows_and_many_columns(M, dtype, block):
+    """One, two and three blocks of 16 columns a workgroup, ragged in all lengths;
+    up to 64 rows a column's result is the same whatever the number of columns."""
+    for N, K in ((300, 1100), (4101, 1100), (8205, 1100), (8205, 129), (4101, 100)):
+        note(f"mm few rows {M}x{N}x{K} {dtype}")
+        A, B = made(sample(M, K, 1)), made(sample(N, K, 2, 0.0) / np.sqrt(K), block)
+        a, b = ref.values(*parts(A)), ref.values(*parts(B), block)
+        C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+        il.iris_fp8_mm(C, A, B)
+        check_product(C, a, b, None, None, dtype, (M, N, K, dtype))
+        if K == 1100 and M <= 64:
+            part = il.Fp8(B.codes[:256], B.scales[:256 if block == 1 else 2], block)
+            D = torch.empty((M, 256), dtype=DT[dtype], device="cuda")
+            il.iris_fp8_mm(D, A, part)
+            assert torch.equal(C[:, :256], D)
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """Matrices of more than 4 GiB: their last rows are what the same rows alone give."""
     rows, cols = 270_000, 16_384                      # 4.4e9 values
