@@ -278,8 +278,8 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  * no counterpart on the pages.
  *
  * A block-scaled matrix holds e4m3 codes (OCP FP8: no infinity, 0x7f and 0xff
- * are NaN, largest value 448) and power-of-two scales: scale byte s stands
- * for 2^(s-127), and an entry's value is code * scale. Blocks run along the
+ * are NaN, largest value 448) and power-of-two scales: scale byte s, 1 to 254,
+ * stands for 2^(s-127), and an entry's value is code * scale. Blocks run along the
  * row, which is always the direction a product contracts: `block` 1 gives
  * every 1 x 128 entries a scale (activations, gradients), 128 every 128 x 128
  * (weights). The last block of a row or column may be shorter; any number of
@@ -295,6 +295,13 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  * caller. Unlike above, plain matrices (x, C, gate, up, dh) may have any row
  * pitch >= their columns and need only the alignment of their type; rows that
  * start at multiples of 16 bytes are faster.
+ * Limits (IRIS_ERR_UNSUPPORTED beyond): row pitches of codes, scales and plain
+ * matrices up to 2^22, rows and columns up to 2^30 with fewer than 2^31 blocks of
+ * 128 along either direction, K of a product up to 2^21 and up to 2^30 output
+ * blocks of 128 x 128. Matrices may exceed 4 GiB.
+ * Every result is the same from call to call. A product's last bits may differ
+ * with its shape, which chooses the order of its sums; up to 64 rows of A a
+ * column's result does not depend on N.
  */
 typedef struct iris_fp8 {
   void* codes;
@@ -341,7 +348,8 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
  * which has to stay zeroed. NULL: the library's own, 32 MiB per (device,
  * stream), allocated by the first call that needs it (also during a graph
  * capture, whose replays then use it) and freed by iris_finalize(). One
- * workspace may not serve two calls at the same time.
+ * workspace may not serve two calls at the same time: graphs captured on one
+ * stream that replay side by side need one each.
  */
 int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B,
                 const void* bias, int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace,
