@@ -62,7 +62,8 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 // once; |value / scale| <= 448 but for infinities and NaN, which give NaN codes).
 __device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d, float scale) {
   typedef short i16x2 __attribute__((ext_vector_type(2)));
-  i16x2 w = {0, 0};
+  i16x2 w;
+  asm("" : "=v"(w));   // both halves are written below
   w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
   return __builtin_bit_cast(uint32_t, w);
@@ -91,6 +92,13 @@ __device__ __forceinline__ void narrow(float v, bf16& o) {
   o.bits = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// all bits where `on`, and not a condition to the compiler, which would branch on it
+__device__ __forceinline__ uint32_t on_mask(bool on) {
+  uint32_t m = on ? ~0u : 0u;
+  asm("" : "+v"(m));
+  return m;
+}
+
 // C consecutive values of a row, as they came. WHOLE: the row's pieces are whole
 // and 16-byte aligned; otherwise they are read value by value. A piece at
 // `col` has its values from cols - col on as zeros; nothing past the row's
@@ -114,12 +122,12 @@ struct Piece {
       // branch between the loads
       static_assert(N % 4 == 0, "piece shorter than a 16-byte load");
       on = on && col < cols;
-      const uint32_t at = (row + (col < cols ? col : 0)) * (uint32_t)sizeof(T);
+      const uint32_t at = (row + (col < cols ? col : 0)) * (uint32_t)sizeof(T), m = on_mask(on);
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
         const u32x4 v = ld16((const char*)x + at + 16 * i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * i + e] = on ? v[e] : 0u;
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e] & m;
       }
     } else {
       T t[C];
@@ -157,11 +165,11 @@ __device__ __forceinline__ void load_codes(const uint8_t* x, uint32_t row, int c
     }
   }
 }
-// their values; all zeros where `on` is false
+// their values; all zeros where the mask is
 template <int C>
-__device__ __forceinline__ void decode(const uint32_t (&w)[C / 4], float scale, bool on, float (&v)[C]) {
+__device__ __forceinline__ void decode(const uint32_t (&w)[C / 4], float scale, uint32_t on, float (&v)[C]) {
 #pragma unroll
-  for (int i = 0; i < C / 4; ++i) from_fp8x4(on ? w[i] : 0u, scale, v + 4 * i);
+  for (int i = 0; i < C / 4; ++i) from_fp8x4(w[i] & on, scale, v + 4 * i);
 }
 
 // C codes to a row, none past its last column
@@ -188,6 +196,11 @@ __device__ __forceinline__ void encode_piece(const float (&v)[C], float scale, u
 // Largest magnitudes, as bits. v_max3_f32 takes two values at once and their
 // magnitudes for free; an infinity (or a signalling NaN) leaves something that
 // is not finite, and only then are the values looked at one by one.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float m;
+  asm("v_max_f32 %0, |%1|, |%2|" : "=v"(m) : "v"(a), "v"(b));
+  return m;
+}
 __device__ __forceinline__ float max_abs(float m, float a, float b) {
   asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(m) : "v"(a), "v"(b));
   return m;
@@ -196,9 +209,9 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 
 template <int C>
 __device__ __forceinline__ uint32_t piece_amax(const float (&v)[C]) {
-  float f = 0.0f;
+  float f = max_abs(v[0], v[1]);
 #pragma unroll
-  for (int i = 0; i < C; i += 2) f = max_abs(f, v[i], v[i + 1]);
+  for (int i = 2; i < C; i += 2) f = max_abs(f, v[i], v[i + 1]);
   uint32_t m = __builtin_bit_cast(uint32_t, f);
   if (__builtin_expect(m >= kInfBits, 0)) {
     m = 0;

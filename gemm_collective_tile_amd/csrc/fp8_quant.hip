@@ -148,7 +148,7 @@ __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlac
       uint32_t m[C], top = 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        m[c] = __builtin_bit_cast(uint32_t, max_abs(max_abs(0.0f, v[n][0][c], v[n][1][c]), v[n][2][c], v[n][3][c]));
+        m[c] = __builtin_bit_cast(uint32_t, max_abs(max_abs(v[n][0][c], v[n][1][c]), v[n][2][c], v[n][3][c]));
         top = max(top, m[c]);
       }
       if (__builtin_expect(top >= kInfBits, 0)) {
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv n
       s[i] = scale_value(b);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) decode<C>(w[i], s[i], p.on(i) && p.col() < p.cols(), v[i]);
+    for (int i = 0; i < 4; ++i) decode<C>(w[i], s[i], on_mask(p.on(i) && p.col() < p.cols()), v[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -327,15 +327,15 @@ __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs
     float v[2][4][C];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool on = p.on(i) && p.col() < p.cols();
+      const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
       float g[C], u[C];
       decode<C>(in.g[i], scale_value(in.sg[i]), on, g);
       decode<C>(in.u[i], scale_value(in.su[i]), on, u);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const float d = in.d[i].value(c), s = sigmoid(g[c]);
-        v[0][i][c] = d * u[c] * (s * (1.0f + g[c] * (1.0f - s)));
-        v[1][i][c] = d * (g[c] * s);
+        const float d = in.d[i].value(c), s = sigmoid(g[c]), gs = g[c] * s;
+        v[0][i][c] = d * u[c] * __builtin_fmaf(gs, 1.0f - s, s);
+        v[1][i][c] = d * gs;
       }
       put_row<WHOLE>(a.dgate, p, i, v[0][i], -1);
       put_row<WHOLE>(a.dup, p, i, v[1][i], -1);
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs
     float v[1][4][C];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool on = p.on(i) && p.col() < p.cols();
+      const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
 #pragma unroll
       for (int k = 0; k < C / 4; ++k) asm volatile("" : "+v"(in.g[i][k]), "+v"(in.u[i][k]));
       float g[C], u[C];
