@@ -147,29 +147,25 @@ __device__ __forceinline__ void load_piece(const T* x, uint32_t row, int col, in
   for (int i = 0; i < C; ++i) v[i] = p.value(i);
 }
 
-// C consecutive codes (C = 8 or 16). Rows of codes start at multiples of 16
-// bytes, which are allocated up to the next one, so a piece is one load. Codes
-// past the row's last one become zeros.
-template <bool WHOLE, int C>
-__device__ __forceinline__ void load_codes(const uint8_t* x, uint32_t row, int col, int cols, uint32_t (&w)[C / 4]) {
+// 8 consecutive codes. Rows of codes start at multiples of 16 bytes, which are
+// allocated up to the next one, so a piece is one load. Codes past the row's
+// last one become zeros.
+template <bool WHOLE>
+__device__ __forceinline__ void load_codes(const uint8_t* x, uint32_t row, int col, int cols, uint32_t (&w)[2]) {
   const uint8_t* p = x + (row + (col < cols ? col : 0));
-  if constexpr (C == 16)
-    *(u32x4*)w = *(const u32x4*)p;
-  else
-    *(u32x2*)w = *(const u32x2*)p;
+  *(u32x2*)w = *(const u32x2*)p;
   if constexpr (!WHOLE) {
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int n = cols - col - 4 * i;   // codes of this word inside the row
       w[i] = n >= 4 ? w[i] : (n <= 0 ? 0u : w[i] & ((1u << (8 * n)) - 1u));
     }
   }
 }
 // their values; all zeros where the mask is
-template <int C>
-__device__ __forceinline__ void decode(const uint32_t (&w)[C / 4], float scale, uint32_t on, float (&v)[C]) {
-#pragma unroll
-  for (int i = 0; i < C / 4; ++i) from_fp8x4(w[i] & on, scale, v + 4 * i);
+__device__ __forceinline__ void decode(const uint32_t (&w)[2], float scale, uint32_t on, float (&v)[8]) {
+  from_fp8x4(w[0] & on, scale, v);
+  from_fp8x4(w[1] & on, scale, v + 4);
 }
 
 // C codes to a row, none past its last column
@@ -243,23 +239,20 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
   return m;
 }
 
-// For C numbers, the largest over the lanes l, l + L, l + 2 L, ... of the wave
-// (L = 128 / C). One swap of two registers' halves and one maximum reduce both
-// registers; what is left in m[0 .. C / 4 - 1] is that of the numbers
-// C / 2 * (lane / 32) + C / 4 * (lane / 16 % 2) + 0 .. C / 4 - 1.
-template <int C>
-__device__ __forceinline__ void stride_max(uint32_t (&m)[C]) {
-  static_assert(C == 8 || C == 16, "");
+// For 8 numbers, the largest over the lanes l, l + 16, l + 32, l + 48 of the wave.
+// One swap of two registers' halves and one maximum reduce both registers; what
+// is left in m[0] and m[1] is that of the numbers 4 * (lane / 32) +
+// 2 * (lane / 16 % 2) + 0 and 1.
+__device__ __forceinline__ void stride_max(uint32_t (&m)[8]) {
 #pragma unroll
-  for (int c = 0; c < C / 2; ++c) {
-    const auto r = __builtin_amdgcn_permlane32_swap(m[c], m[c + C / 2], false, false);
+  for (int c = 0; c < 4; ++c) {
+    const auto r = __builtin_amdgcn_permlane32_swap(m[c], m[c + 4], false, false);
     m[c] = max((uint32_t)r[0], (uint32_t)r[1]);
   }
 #pragma unroll
-  for (int c = 0; c < C / 4; ++c) {
-    const auto r = __builtin_amdgcn_permlane16_swap(m[c], m[c + C / 4], false, false);
+  for (int c = 0; c < 2; ++c) {
+    const auto r = __builtin_amdgcn_permlane16_swap(m[c], m[c + 2], false, false);
     m[c] = max((uint32_t)r[0], (uint32_t)r[1]);
-    if constexpr (C == 16) m[c] = max_dpp<0x128>(m[c]);  // lane ^ 8
   }
 }
 

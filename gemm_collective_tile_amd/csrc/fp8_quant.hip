@@ -8,8 +8,9 @@
 //          8 lanes of a block agree on its scale by exchanging lanes.
 //   tiles  blocks along the columns too (a transposed output, or 128 x 128
 //          blocks). A workgroup takes a 128 x 128 tile, so that every block of
-//          either direction lies in it. A thread holds 4 rows x 16 columns (8
-//          columns where three values per entry are alive); codes of 4 rows of
+//          either direction lies in it. A thread holds 4 rows x 8 columns (with
+//          16 columns and half the threads 4096 x 4096 of 8 bits takes 8.5 us
+//          instead of 8.2, 1 x 4096 3.6 instead of 3.3); codes of 4 rows of
 //          one column are one 32-bit word of the transposed tile, which turns
 //          around in LDS and leaves in rows of 128 bytes.
 #include "fp8.hpp"
@@ -86,11 +87,11 @@ __global__ __launch_bounds__(kThreads) void fp8_swiglu_kernel(const T* gate, con
 
 // ------------------------------------------------------------------ tiles
 
-// Tile of 128 x 128 held by T threads: thread t has columns C * (t % L) .. + C
-// of rows 4 * (t / L) .. + 4, L = 128 / C lanes side by side.
-template <int C>
+// Tile of 128 x 128 held by T threads: thread t has columns kPiece * (t % L) .. + kPiece
+// of rows 4 * (t / L) .. + 4, L = 128 / kPiece lanes side by side.
+constexpr int kPiece = 8;   // columns of a thread
 struct TilePlace {
-  static constexpr int L = kTile / C;
+  static constexpr int L = kTile / kPiece;
   static constexpr int T = L * (kTile / 4);
   uint32_t t;            // thread
   int r0, c0, ch, j;     // tile origin, piece and row group in it
@@ -106,7 +107,7 @@ struct TilePlace {
   // row i of this thread (rows past the end read the last one), whether it is there
   __device__ __forceinline__ uint32_t row(int i) const { return (uint32_t)min(4 * j + i, nrows - 1 - r0); }
   __device__ __forceinline__ bool on(int i) const { return r0 + 4 * j + i < nrows; }
-  __device__ __forceinline__ int col() const { return C * ch; }
+  __device__ __forceinline__ int col() const { return kPiece * ch; }
   __device__ __forceinline__ int cols() const { return ncols - c0; }
   // Addresses: the tile's corner, the same in all threads, and a 32-bit offset
   // from it (pitches are under 2^22, so a tile's rows lie within 2^31 bytes)
@@ -117,9 +118,9 @@ struct TilePlace {
 __device__ __forceinline__ uint32_t offset(uint32_t row, int64_t ld) { return __umul24(row, (uint32_t)ld); }
 
 // LDS of N tiles' turn: the transposed codes and the columns' scales
-template <int C, int N>
+template <int N>
 struct TileLds {
-  static constexpr int WAVES = TilePlace<C>::T / 64;
+  static constexpr int WAVES = TilePlace::T / 64;
   alignas(16) uint32_t turn[N][kTile][kTile / 4];  // [column][word of 4 rows], swizzled
   alignas(16) uint32_t part[N][WAVES][kTile];      // a wave's largest magnitude of each column
   alignas(16) float scale[N][kTile];
@@ -128,52 +129,66 @@ struct TileLds {
 // The 16-byte pieces of a column's 128 transposed codes are permuted by the
 // column, so that the words that a wave writes for its L pieces of columns and
 // the pieces that it reads back spread over the banks.
-template <int C>
 __device__ __forceinline__ int turn_word(int col, int word) {
-  return (((word >> 2) ^ (col / C)) & 7) * 4 + (word & 3);
+  return (((word >> 2) ^ (col / kPiece)) & 7) * 4 + (word & 3);
+}
+
+// the first n (< 16) bytes to a multiple of 16
+__device__ __forceinline__ void put_bytes(uint8_t* to, u32x4 w, int n) {
+  if (n <= 0) return;
+  if (n & 8) {
+    *(u32x2*)to = u32x2{w[0], w[1]};
+    w = u32x4{w[2], w[3], 0, 0};
+    to += 8;
+  }
+  if (n & 4) {
+    *(uint32_t*)to = w[0];
+    w[0] = w[1];
+    to += 4;
+  }
+  if (n & 2) {
+    *(uint16_t*)to = (uint16_t)w[0];
+    w[0] >>= 16;
+    to += 2;
+  }
+  if (n & 1) *to = (uint8_t)w[0];
 }
 
 // Writes the transposed codes and scales of N tiles of values (of those whose
 // codes are not NULL). All threads of the workgroup call it; the LDS may be the
 // one of an earlier call. given >= 0: the scale byte of every block (128 x 128
 // blocks), already written.
-template <int C, int N>
-__device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlace<C>& p, const float (&v)[N][4][C],
-                                           int given, TileLds<C, N>& lds) {
-  constexpr int T = TilePlace<C>::T, L = TilePlace<C>::L;
+template <int N>
+__device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlace& p, const float (&v)[N][4][kPiece],
+                                           int given, TileLds<N>& lds) {
+  constexpr int T = TilePlace::T;
   const int t = p.t;
   if (given < 0) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      uint32_t m[C], top = 0;
+      uint32_t m[kPiece], top = 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < kPiece; ++c) {
         m[c] = __builtin_bit_cast(uint32_t, max_abs(max_abs(v[n][0][c], v[n][1][c]), v[n][2][c], v[n][3][c]));
         top = max(top, m[c]);
       }
       if (__builtin_expect(top >= kInfBits, 0)) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
+        for (int c = 0; c < kPiece; ++c) {
           m[c] = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) m[c] = max(m[c], finite_bits(v[n][i][c]));
         }
       }
-      stride_max<C>(m);
-      if (L == 16 || (t & 8) == 0) {
-        uint32_t* const to = &lds.part[n][t / 64][C * p.ch + C / 2 * (t >> 5 & 1) + C / 4 * (t >> 4 & 1)];
-        if constexpr (C == 16)
-          *(u32x4*)to = u32x4{m[0], m[1], m[2], m[3]};
-        else
-          *(u32x2*)to = u32x2{m[0], m[1]};
-      }
+      stride_max(m);
+      *(u32x2*)&lds.part[n][t / 64][kPiece * p.ch + 4 * (t >> 5 & 1) + 2 * (t >> 4 & 1)] = u32x2{m[0], m[1]};
     }
     __syncthreads();
     if (t < N * kTile) {
       const int n = t / kTile, c = t % kTile;
       uint32_t a = 0;
 #pragma unroll
-      for (int w = 0; w < TileLds<C, N>::WAVES; ++w) a = max(a, lds.part[n][w][c]);
+      for (int w = 0; w < TileLds<N>::WAVES; ++w) a = max(a, lds.part[n][w][c]);
       const uint32_t b = scale_byte(a);
       lds.scale[n][c] = scale_value(b);
 #pragma unroll
@@ -185,14 +200,14 @@ __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlac
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    float s[C];
+    float s[kPiece];
 #pragma unroll
-    for (int c = 0; c < C; ++c) s[c] = scale_value((uint32_t)given);
-    if (given < 0) __builtin_memcpy(s, &lds.scale[n][C * p.ch], sizeof s);
+    for (int c = 0; c < kPiece; ++c) s[c] = scale_value((uint32_t)given);
+    if (given < 0) __builtin_memcpy(s, &lds.scale[n][kPiece * p.ch], sizeof s);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = C * p.ch + c;
-      lds.turn[n][col][turn_word<C>(col, p.j)] = to_fp8x4(v[n][0][c], v[n][1][c], v[n][2][c], v[n][3][c], s[c]);
+    for (int c = 0; c < kPiece; ++c) {
+      const int col = kPiece * p.ch + c;
+      lds.turn[n][col][turn_word(col, p.j)] = to_fp8x4(v[n][0][c], v[n][1][c], v[n][2][c], v[n][3][c], s[c]);
     }
   }
   __syncthreads();
@@ -205,27 +220,26 @@ __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlac
 #pragma unroll
     for (int k = 0; k < kTile * 8 / T; ++k) {
       const int col = k * (T / 8) + t / 8;
-      const uint32_t* const w = &lds.turn[n][col][turn_word<C>(col, 4 * piece)];
+      const uint32_t* const w = &lds.turn[n][col][turn_word(col, 4 * piece)];
       if (col >= p.cols()) continue;
       uint8_t* const to = corner + (offset(col, qt[n].ld) + 16 * piece);
       if (valid >= 16) {
         *(u32x4*)to = *(const u32x4*)w;
       } else {
-#pragma unroll 1
-        for (int i = 0; i < valid; ++i) to[i] = ((const uint8_t*)w)[i];
+        put_bytes(to, *(const u32x4*)w, valid);
       }
     }
   }
 }
 
 // a thread's piece of its row i, blocks along the rows
-template <bool WHOLE, int C>
-__device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace<C>& p, int i, const float (&v)[C], int given) {
-  const uint32_t s = given < 0 ? scale_byte(group_max<TilePlace<C>::L>(piece_amax(v))) : (uint32_t)given;
-  uint32_t w[C / 4];
+template <bool WHOLE>
+__device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace& p, int i, const float (&v)[kPiece], int given) {
+  const uint32_t s = given < 0 ? scale_byte(group_max<TilePlace::L>(piece_amax(v))) : (uint32_t)given;
+  uint32_t w[kPiece / 4];
   encode_piece(v, scale_value(s), w);
   if (p.on(i)) {
-    store_codes<WHOLE, C>(p.corner(q.codes, q.ld), offset(p.row(i), q.ld), p.col(), p.cols(), w);
+    store_codes<WHOLE, kPiece>(p.corner(q.codes, q.ld), offset(p.row(i), q.ld), p.col(), p.cols(), w);
     if (given < 0 && p.ch == 0) p.scales(q)[offset(p.row(i), q.lds)] = (uint8_t)s;
   }
 }
@@ -237,23 +251,22 @@ __device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace<C>& p, 
 // and store in step: what one waits for is not hidden by another. 128 x 128 is the
 // least tile that holds whole blocks of both directions.
 template <class T, bool WHOLE>
-__global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv ncb) {
-  constexpr int C = 16;
-  __shared__ TileLds<C, 1> lds;
-  const TilePlace<C> p(a.rows, a.cols, ncb);
-  float all[1][4][C];
-  float(&v)[4][C] = all[0];
+__global__ __launch_bounds__(TilePlace::T) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv ncb) {
+  __shared__ TileLds<1> lds;
+  const TilePlace p(a.rows, a.cols, ncb);
+  float all[1][4][kPiece];
+  float(&v)[4][kPiece] = all[0];
   if constexpr (sizeof(T) == 1) {
-    uint32_t w[4][C / 4];
+    uint32_t w[4][kPiece / 4];
     float s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      load_codes<WHOLE, C>(p.corner(a.x8.codes, a.x8.ld), offset(p.row(i), a.x8.ld), p.col(), p.cols(), w[i]);
+      load_codes<WHOLE>(p.corner(a.x8.codes, a.x8.ld), offset(p.row(i), a.x8.ld), p.col(), p.cols(), w[i]);
       const uint8_t b = p.scales(a.x8)[offset(p.row(i), a.x8.lds)];
       s[i] = scale_value(b);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) decode<C>(w[i], s[i], on_mask(p.on(i) && p.col() < p.cols()), v[i]);
+    for (int i = 0; i < 4; ++i) decode(w[i], s[i], on_mask(p.on(i) && p.col() < p.cols()), v[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -268,7 +281,7 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv n
     if ((threadIdx.x & 63) == 0) lds.part[0][0][threadIdx.x / 64] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < TileLds<C, 1>::WAVES; ++w) m = max(m, lds.part[0][0][w]);
+    for (int w = 0; w < TileLds<1>::WAVES; ++w) m = max(m, lds.part[0][0][w]);
     given = (int)scale_byte(m);
     if (threadIdx.x == 0) {
       if (a.q.codes) a.q.scales[(int64_t)(p.r0 / kTile) * a.q.lds + p.c0 / kTile] = (uint8_t)given;
@@ -281,24 +294,24 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8QuantArgs a, FastDiv n
   }
   if (a.qt.codes) {
     const Fp8Mat qt[1] = {a.qt};
-    put_turned<C, 1>(qt, p, all, given, lds);
+    put_turned<1>(qt, p, all, given, lds);
   }
 }
 
 // One tile's inputs as they came, and their loads.
-template <class T, int C>
+template <class T>
 struct BwdInputs {
-  Piece<T, C> d[4];
-  uint32_t g[4][C / 4], u[4][C / 4];
+  Piece<T, kPiece> d[4];
+  uint32_t g[4][kPiece / 4], u[4][kPiece / 4];
   uint8_t sg[4], su[4];
   template <bool WHOLE>
-  __device__ __forceinline__ void load(const Fp8SwigluBwdArgs& a, const TilePlace<C>& p) {
+  __device__ __forceinline__ void load(const Fp8SwigluBwdArgs& a, const TilePlace& p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t row = p.row(i);
       d[i].template load<WHOLE>(p.corner((const T*)a.dh, a.ld_dh), offset(row, a.ld_dh), p.col(), p.cols(), p.on(i));
-      load_codes<WHOLE, C>(p.corner(a.gate8.codes, a.gate8.ld), offset(row, a.gate8.ld), p.col(), p.cols(), g[i]);
-      load_codes<WHOLE, C>(p.corner(a.up8.codes, a.up8.ld), offset(row, a.up8.ld), p.col(), p.cols(), u[i]);
+      load_codes<WHOLE>(p.corner(a.gate8.codes, a.gate8.ld), offset(row, a.gate8.ld), p.col(), p.cols(), g[i]);
+      load_codes<WHOLE>(p.corner(a.up8.codes, a.up8.ld), offset(row, a.up8.ld), p.col(), p.cols(), u[i]);
       sg[i] = p.scales(a.gate8)[offset(row, a.gate8.lds)];
       su[i] = p.scales(a.up8)[offset(row, a.up8.lds)];
     }
@@ -318,21 +331,20 @@ struct BwdInputs {
 // fp16 12 us, a round of 88 workgroups.
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
-  constexpr int C = 8;
-  __shared__ TileLds<C, 2> lds;
-  const TilePlace<C> p(a.rows, a.cols, ncb);
-  BwdInputs<T, C> in;
+  __shared__ TileLds<2> lds;
+  const TilePlace p(a.rows, a.cols, ncb);
+  BwdInputs<T> in;
   in.template load<WHOLE>(a, p);
   {
-    float v[2][4][C];
+    float v[2][4][kPiece];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
-      float g[C], u[C];
-      decode<C>(in.g[i], scale_value(in.sg[i]), on, g);
-      decode<C>(in.u[i], scale_value(in.su[i]), on, u);
+      float g[kPiece], u[kPiece];
+      decode(in.g[i], scale_value(in.sg[i]), on, g);
+      decode(in.u[i], scale_value(in.su[i]), on, u);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < kPiece; ++c) {
         const float d = in.d[i].value(c), s = sigmoid(g[c]), gs = g[c] * s;
         v[0][i][c] = d * u[c] * __builtin_fmaf(gs, 1.0f - s, s);
         v[1][i][c] = d * gs;
@@ -343,25 +355,70 @@ __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs
     }
     if (a.dgate_t.codes || a.dup_t.codes) {
       const Fp8Mat qt[2] = {a.dgate_t, a.dup_t};
-      put_turned<C, 2>(qt, p, v, -1, lds);
+      put_turned<2>(qt, p, v, -1, lds);
     }
   }
   if (a.h_t.codes) {
-    float v[1][4][C];
+    float v[1][4][kPiece];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
 #pragma unroll
-      for (int k = 0; k < C / 4; ++k) asm volatile("" : "+v"(in.g[i][k]), "+v"(in.u[i][k]));
-      float g[C], u[C];
-      decode<C>(in.g[i], scale_value(in.sg[i]), on, g);
-      decode<C>(in.u[i], scale_value(in.su[i]), on, u);
+      for (int k = 0; k < kPiece / 4; ++k) asm volatile("" : "+v"(in.g[i][k]), "+v"(in.u[i][k]));
+      float g[kPiece], u[kPiece];
+      decode(in.g[i], scale_value(in.sg[i]), on, g);
+      decode(in.u[i], scale_value(in.su[i]), on, u);
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[0][i][c] = g[c] * sigmoid(g[c]) * u[c];
+      for (int c = 0; c < kPiece; ++c) v[0][i][c] = g[c] * sigmoid(g[c]) * u[c];
       __builtin_amdgcn_sched_barrier(0);
     }
     const Fp8Mat qt[1] = {a.h_t};
-    put_turned<C, 1>(qt, p, v, -1, *(TileLds<C, 1>*)&lds);
+    put_turned<1>(qt, p, v, -1, *(TileLds<1>*)&lds);
+  }
+}
+
+// One result of a tile: dgate, dup or h
+template <int PART, class T, bool WHOLE>
+__device__ __forceinline__ void swiglu_bwd_part(const Fp8SwigluBwdArgs& a, const TilePlace& p, TileLds<1>& lds) {
+  const Fp8Mat qt[1] = {PART == 0 ? a.dgate_t : PART == 1 ? a.dup_t : a.h_t};
+  if (PART == 2 && !qt[0].codes) return;
+  BwdInputs<T> in;
+  in.template load<WHOLE>(a, p);
+  float v[1][4][kPiece];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
+    float g[kPiece], u[kPiece];
+    decode(in.g[i], scale_value(in.sg[i]), on, g);
+    if constexpr (PART != 1) decode(in.u[i], scale_value(in.su[i]), on, u);
+#pragma unroll
+    for (int c = 0; c < kPiece; ++c) {
+      const float s = sigmoid(g[c]), gs = g[c] * s;
+      if constexpr (PART == 0) v[0][i][c] = in.d[i].value(c) * u[c] * __builtin_fmaf(gs, 1.0f - s, s);
+      if constexpr (PART == 1) v[0][i][c] = in.d[i].value(c) * gs;
+      if constexpr (PART == 2) v[0][i][c] = gs * u[c];
+    }
+    if constexpr (PART < 2) put_row<WHOLE>(PART == 0 ? a.dgate : a.dup, p, i, v[0][i], -1);
+  }
+  if (qt[0].codes) put_turned<1>(qt, p, v, -1, lds);
+}
+
+// The same with a workgroup for each result of a tile (blockIdx.y), for matrices of
+// few tiles: the vector units of one CU take 4.4 us for all three of a tile while
+// others are idle. In fp16, one workgroup a tile and three:
+//     16 x 1376    7.9 us   5.0        2048 x 1920   12.7   12.5
+//   1001 x 1376   11.6      9.1        2048 x 2688   17.5   15.3
+//   1024 x 2048   10.4      8.6        2048 x 4096   18.6   19.7
+// so as long as four workgroups a CU hold them all.
+constexpr uint32_t kPartsTiles = 4 * kFp8Cus / 3;
+template <class T, bool WHOLE>
+__global__ __launch_bounds__(512) void fp8_swiglu_bwd_parts_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
+  __shared__ TileLds<1> lds;
+  const TilePlace p(a.rows, a.cols, ncb);
+  switch (blockIdx.y) {
+    case 0: swiglu_bwd_part<0, T, WHOLE>(a, p, lds); break;
+    case 1: swiglu_bwd_part<1, T, WHOLE>(a, p, lds); break;
+    default: swiglu_bwd_part<2, T, WHOLE>(a, p, lds); break;
   }
 }
 
@@ -384,7 +441,7 @@ hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
 #undef ROWS
     return hipGetLastError();
   }
-  const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace<16>::T);
+  const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace::T);
   switch (a.x_type) {
     case T_FP16: hipLaunchKernelGGL((fp8_tile_kernel<f16, WHOLE>), grid, block, 0, s, a, d); break;
     case T_BF16: hipLaunchKernelGGL((fp8_tile_kernel<bf16, WHOLE>), grid, block, 0, s, a, d); break;
@@ -411,8 +468,12 @@ hipError_t swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
 template <class T, bool WHOLE>
 hipError_t swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
-  hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(blocks_of(a.rows) * nkb), dim3(TilePlace<8>::T), 0, s, a,
-                     FastDiv::make(nkb));
+  const uint32_t tiles = blocks_of(a.rows) * nkb;
+  const dim3 block(TilePlace::T);
+  if (tiles <= kPartsTiles)
+    hipLaunchKernelGGL((fp8_swiglu_bwd_parts_kernel<T, WHOLE>), dim3(tiles, 3), block, 0, s, a, FastDiv::make(nkb));
+  else
+    hipLaunchKernelGGL((fp8_swiglu_bwd_kernel<T, WHOLE>), dim3(tiles), block, 0, s, a, FastDiv::make(nkb));
   return hipGetLastError();
 }
 
