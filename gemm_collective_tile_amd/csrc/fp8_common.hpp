@@ -17,6 +17,7 @@
 // overflowed gradient shows in every sum that it enters and its neighbours in
 // the block keep their precision.
 #pragma once
+#include <type_traits>
 
 #include "device_common.hpp"
 
@@ -99,10 +100,16 @@ __device__ __forceinline__ uint32_t on_mask(bool on) {
   return m;
 }
 
+// 16 bytes at any multiple of 2 or 4
+typedef uint32_t u32x4_at_2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at_4 __attribute__((ext_vector_type(4), aligned(4)));
+
 // C consecutive values of a row, as they came. WHOLE: the row's pieces are whole
-// and 16-byte aligned; otherwise they are read value by value. A piece at
-// `col` has its values from cols - col on as zeros; nothing past the row's
-// last value is read. `row` is the offset of the row's first value from `x`.
+// and 16-byte aligned. A piece at `col` has its values from cols - col on as zeros.
+// `row` is the offset of the row's first value from `x`, `more`: another row of the
+// matrix follows, at least C values on, so that a ragged piece may be read whole
+// (into that row, in the matrix's own memory) and cut. Only the last row's ragged
+// piece is read value by value: nothing past the matrix's last value is read.
 template <class T, int C>
 struct Piece {
   static constexpr int N = C * (int)sizeof(T) / 4;
@@ -116,33 +123,54 @@ struct Piece {
     }
   }
   template <bool WHOLE>
-  __device__ __forceinline__ void load(const T* x, uint32_t row, int col, int cols, bool on) {
+  __device__ __forceinline__ void load(const T* x, uint32_t row, int col, int cols, bool on, bool more) {
+    // a piece that is off reads another one of the row and drops it: no branch
+    // between the loads
+    static_assert(N % 4 == 0, "piece shorter than a 16-byte load");
+    on = on && col < cols;
+    const uint32_t at = row + (col < cols ? col : 0), m = on_mask(on);
+    const char* const first = (const char*)x + at * (uint32_t)sizeof(T);
     if constexpr (WHOLE) {
-      // a piece that is off reads another one of the row and drops it: no
-      // branch between the loads
-      static_assert(N % 4 == 0, "piece shorter than a 16-byte load");
-      on = on && col < cols;
-      const uint32_t at = (row + (col < cols ? col : 0)) * (uint32_t)sizeof(T), m = on_mask(on);
-#pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        const u32x4 v = ld16((const char*)x + at + 16 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e] & m;
-      }
+      take<u32x4>(first);
     } else {
-      T t[C];
+      const int n = cols - (col < cols ? col : 0);   // values up to the row's end
+      if (n >= C || more) {
+        take<std::conditional_t<sizeof(T) == 2, u32x4_at_2, u32x4_at_4>>(first);
+      } else {
+        T t[C];
 #pragma unroll
-      for (int i = 0; i < C; ++i) t[i] = x[row + min(col + i, cols - 1)];
+        for (int i = 0; i < C; ++i) t[i] = x[at + min(i, n - 1)];
+        __builtin_memcpy(w, t, sizeof t);
+      }
+      if (n < C) {
+        constexpr int E = 4 / sizeof(T);
 #pragma unroll
-      for (int i = 0; i < C; ++i) t[i] = on && col + i < cols ? t[i] : T{};
-      __builtin_memcpy(w, t, sizeof t);
+        for (int i = 0; i < N; ++i) {
+          const int k = n - E * i;   // values of this word inside the row
+          w[i] &= k >= E ? ~0u : (k <= 0 ? 0u : 0xffffu);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] &= m;
+  }
+
+ private:
+  template <class U>
+  __device__ __forceinline__ void take(const char* x) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 v = *(const U*)(x + 16 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e];
     }
   }
 };
 template <bool WHOLE, int C, class T>
-__device__ __forceinline__ void load_piece(const T* x, uint32_t row, int col, int cols, bool on, float (&v)[C]) {
+__device__ __forceinline__ void load_piece(const T* x, uint32_t row, int col, int cols, bool on, bool more,
+                                           float (&v)[C]) {
   Piece<T, C> p;
-  p.template load<WHOLE>(x, row, col, cols, on);
+  p.template load<WHOLE>(x, row, col, cols, on, more);
 #pragma unroll
   for (int i = 0; i < C; ++i) v[i] = p.value(i);
 }
@@ -168,7 +196,31 @@ __device__ __forceinline__ void decode(const uint32_t (&w)[2], float scale, uint
   from_fp8x4(w[1] & on, scale, v + 4);
 }
 
-// C codes to a row, none past its last column
+// the first n of at most 16 bytes to a multiple of 16 (n <= 0: none)
+__device__ __forceinline__ void put_bytes(uint8_t* to, u32x4 w, int n) {
+  if (n >= 16) {
+    *(u32x4*)to = w;
+    return;
+  }
+  if (n <= 0) return;
+  if (n & 8) {
+    *(u32x2*)to = u32x2{w[0], w[1]};
+    w = u32x4{w[2], w[3], 0, 0};
+    to += 8;
+  }
+  if (n & 4) {
+    *(uint32_t*)to = w[0];
+    w[0] = w[1];
+    to += 4;
+  }
+  if (n & 2) {
+    *(uint16_t*)to = (uint16_t)w[0];
+    w[0] >>= 16;
+    to += 2;
+  }
+  if (n & 1) *to = (uint8_t)w[0];
+}
+// C codes (8 or 16) to a row, none past its last column
 template <bool WHOLE, int C>
 __device__ __forceinline__ void store_codes(uint8_t* x, uint32_t row, int col, int cols, const uint32_t (&w)[C / 4]) {
   if (WHOLE ? col < cols : col + C <= cols) {
@@ -177,9 +229,9 @@ __device__ __forceinline__ void store_codes(uint8_t* x, uint32_t row, int col, i
     else
       *(u32x2*)(x + (row + col)) = *(const u32x2*)w;
   } else if constexpr (!WHOLE) {
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (col + i < cols) x[row + col + i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    u32x4 v{w[0], w[1], 0, 0};
+    if constexpr (C == 16) v = *(const u32x4*)w;
+    put_bytes(x + (row + col), v, cols - col);
   }
 }
 

@@ -25,7 +25,7 @@ constexpr int kTile = 128;
 // blocks (row, kb) are numbered along the rows; 8 lanes work on each
 struct RowPlace {
   int row, kb, col;
-  bool on;
+  bool on, below;   // the row is there, another one follows
   __device__ __forceinline__ RowPlace(int rows, FastDiv nkb) {
     const uint32_t b = blockIdx.x * (kThreads / 8) + threadIdx.x / 8;
     const int r = (int)nkb.div(b);
@@ -33,7 +33,9 @@ struct RowPlace {
     col = kb * kFp8Block + 16 * (threadIdx.x & 7);
     on = r < rows;
     row = min(r, rows - 1);
+    below = r < rows - 1;
   }
+  __device__ __forceinline__ bool more(int ld) const { return below && ld >= 16; }
 };
 
 template <bool WHOLE>
@@ -54,7 +56,7 @@ template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(const T* x, int ldx, int rows, int cols, Fp8Mat q, FastDiv nkb) {
   const RowPlace p(rows, nkb);
   float v[16];
-  load_piece<WHOLE>(x + (int64_t)p.row * ldx, 0, p.col, cols, p.on, v);
+  load_piece<WHOLE>(x + (int64_t)p.row * ldx, 0, p.col, cols, p.on, p.more(ldx), v);
   put_row_block<WHOLE>(q, p, cols, v);
 }
 
@@ -74,8 +76,8 @@ __global__ __launch_bounds__(kThreads) void fp8_swiglu_kernel(const T* gate, con
                                                               int cols, Fp8Mat out, FastDiv nkb, KEPT kept) {
   const RowPlace p(rows, nkb);
   float g[16], u[16], h[16];
-  load_piece<WHOLE>(gate + (int64_t)p.row * ld_gate, 0, p.col, cols, p.on, g);
-  load_piece<WHOLE>(up + (int64_t)p.row * ld_up, 0, p.col, cols, p.on, u);
+  load_piece<WHOLE>(gate + (int64_t)p.row * ld_gate, 0, p.col, cols, p.on, p.more(ld_gate), g);
+  load_piece<WHOLE>(up + (int64_t)p.row * ld_up, 0, p.col, cols, p.on, p.more(ld_up), u);
 #pragma unroll
   for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
   put_row_block<WHOLE>(out, p, cols, h);
@@ -107,6 +109,8 @@ struct TilePlace {
   // row i of this thread (rows past the end read the last one), whether it is there
   __device__ __forceinline__ uint32_t row(int i) const { return (uint32_t)min(4 * j + i, nrows - 1 - r0); }
   __device__ __forceinline__ bool on(int i) const { return r0 + 4 * j + i < nrows; }
+  // another row of the matrix follows, a piece on or more
+  __device__ __forceinline__ bool more(int i, int ld) const { return r0 + 4 * j + i < nrows - 1 && ld >= kPiece; }
   __device__ __forceinline__ int col() const { return kPiece * ch; }
   __device__ __forceinline__ int cols() const { return ncols - c0; }
   // Addresses: the tile's corner, the same in all threads, and a 32-bit offset
@@ -131,27 +135,6 @@ struct TileLds {
 // the pieces that it reads back spread over the banks.
 __device__ __forceinline__ int turn_word(int col, int word) {
   return (((word >> 2) ^ (col / kPiece)) & 7) * 4 + (word & 3);
-}
-
-// the first n (< 16) bytes to a multiple of 16
-__device__ __forceinline__ void put_bytes(uint8_t* to, u32x4 w, int n) {
-  if (n <= 0) return;
-  if (n & 8) {
-    *(u32x2*)to = u32x2{w[0], w[1]};
-    w = u32x4{w[2], w[3], 0, 0};
-    to += 8;
-  }
-  if (n & 4) {
-    *(uint32_t*)to = w[0];
-    w[0] = w[1];
-    to += 4;
-  }
-  if (n & 2) {
-    *(uint16_t*)to = (uint16_t)w[0];
-    w[0] >>= 16;
-    to += 2;
-  }
-  if (n & 1) *to = (uint8_t)w[0];
 }
 
 // Writes the transposed codes and scales of N tiles of values (of those whose
@@ -223,11 +206,7 @@ __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlac
       const uint32_t* const w = &lds.turn[n][col][turn_word(col, 4 * piece)];
       if (col >= p.cols()) continue;
       uint8_t* const to = corner + (offset(col, qt[n].ld) + 16 * piece);
-      if (valid >= 16) {
-        *(u32x4*)to = *(const u32x4*)w;
-      } else {
-        put_bytes(to, *(const u32x4*)w, valid);
-      }
+      put_bytes(to, *(const u32x4*)w, valid);
     }
   }
 }
@@ -270,7 +249,7 @@ __global__ __launch_bounds__(TilePlace::T) void fp8_tile_kernel(Fp8QuantArgs a, 
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      load_piece<WHOLE>(p.corner((const T*)a.x, a.ldx), offset(p.row(i), a.ldx), p.col(), p.cols(), p.on(i), v[i]);
+      load_piece<WHOLE>(p.corner((const T*)a.x, a.ldx), offset(p.row(i), a.ldx), p.col(), p.cols(), p.on(i), p.more(i, a.ldx), v[i]);
   }
   int given = -1;
   if (a.block == kTile) {
@@ -309,7 +288,8 @@ struct BwdInputs {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t row = p.row(i);
-      d[i].template load<WHOLE>(p.corner((const T*)a.dh, a.ld_dh), offset(row, a.ld_dh), p.col(), p.cols(), p.on(i));
+      d[i].template load<WHOLE>(p.corner((const T*)a.dh, a.ld_dh), offset(row, a.ld_dh), p.col(), p.cols(), p.on(i),
+                                  p.more(i, a.ld_dh));
       load_codes<WHOLE>(p.corner(a.gate8.codes, a.gate8.ld), offset(row, a.gate8.ld), p.col(), p.cols(), g[i]);
       load_codes<WHOLE>(p.corner(a.up8.codes, a.up8.ld), offset(row, a.up8.ld), p.col(), p.cols(), u[i]);
       sg[i] = p.scales(a.gate8)[offset(row, a.gate8.lds)];

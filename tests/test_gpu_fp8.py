@@ -131,6 +131,26 @@ def test_quantize_pitch_and_offset(pitch, offset):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [1, 7, 8, 9, 15, 17, 30, 31, 113, 121, 127, 129, 143])
+def test_quantize_ragged_rows_keep_their_neighbours_out(cols, dtype):
+    """A ragged piece may be read with what follows its row, which has no say in the
+    row's scale or codes: rows alternate between ordinary and 1000 times larger values."""
+    for rows, pitch, offset in ((1, cols, 1), (2, cols, 0), (131, cols, 0), (131, cols + 3, 1), (130, cols + 16, 2)):
+        note(f"quantize ragged {rows}x{cols} {dtype} pitch {pitch} offset {offset}")
+        v = sample(rows, cols, cols * 31 + rows)
+        v[1::2] *= 1000.0
+        x, xv = on_gpu(v, dtype, pitch, offset)
+        q, qt = fresh(rows, cols), fresh(cols, rows)
+        il.iris_fp8_quantize(x, q)
+        check_quantized(q, xv, 1, "rows")
+        q = fresh(rows, cols)
+        il.iris_fp8_quantize(x, q, qt)
+        check_quantized(q, xv, 1, "rows of both")
+        check_quantized(qt, np.ascontiguousarray(xv.T), 1, "columns")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DT))
 def test_quantize_special_values(dtype):
     """Infinities, NaN, blocks of nothing else, zeros of both signs, the largest and the smallest values, ties."""
     top = float(torch.finfo(DT[dtype]).max)
