@@ -20,7 +20,6 @@ struct Fp8MmArgs {
   uint8_t b_block;        // rows of B per scale row: 1 or 128
   uint8_t bias_along_m;
   uint8_t accumulate;     // add to C's old values
-  uint8_t vec;            // rows of C start at multiples of 16 bytes
   uint8_t c_type;
 };
 // How a product runs: its tile, and over how many workgroups the contraction of

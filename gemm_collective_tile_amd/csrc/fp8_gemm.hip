@@ -400,7 +400,7 @@ __global__ __launch_bounds__(256) void fp8_mm_kernel(Fp8MmArgs g) {
       const int row = r + lane / (T::WN / V), tm = wm + 32 * i + row, m = m0 + tm;
       float v[V];
       __builtin_memcpy(v, strip + row * PITCH + c, sizeof v);
-      if (m < g.M && n < g.N) put_row_piece((OUT*)g.C + (int64_t)m * g.ldc + n, g.N - n, g.vec, g.accumulate,
+      if (m < g.M && n < g.N) put_row_piece((OUT*)g.C + (int64_t)m * g.ldc + n, g.N - n, g.accumulate,
                                             g.bias_along_m ? bl[tm] : 0.0f, bn, v);
     }
     wait_lds();
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(256) void fp8_mm_join_kernel(Fp8MmArgs g, const flo
   const OUT* const bias = (const OUT*)g.bias;
 #pragma unroll
   for (int e = 0; e < V; ++e) bn[e] = bias && !g.bias_along_m && n + e < g.N ? widen(bias[n + e]) : 0.0f;
-  put_row_piece((OUT*)g.C + (int64_t)m * g.ldc + n, g.N - n, g.vec, g.accumulate,
+  put_row_piece((OUT*)g.C + (int64_t)m * g.ldc + n, g.N - n, g.accumulate,
                 bias && g.bias_along_m ? widen(bias[m]) : 0.0f, bn, v);
 }
 
@@ -457,7 +457,6 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
   const int64_t ldp = ((int64_t)a.N + 3) / 4 * 4;
   g.C = ws;
   g.ldc = (int32_t)ldp;
-  g.vec = 1;
   g.bias = nullptr;
   g.accumulate = 0;
   hipError_t e = small_tile<float, EXACT>(g, plan, s);

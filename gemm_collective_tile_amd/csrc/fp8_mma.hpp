@@ -49,25 +49,26 @@ __device__ __forceinline__ void wait_loads() {
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // V values of a row of C: biases and old values added, then the one rounding.
-// `left`: columns from here to the row's end (> 0). `vec`: rows of C start at
-// multiples of 16 bytes.
+// `left`: columns from here to the row's end (> 0). C has its type's alignment
+// only, which one wide access of a piece does not mind (C with 8191 columns, 8192 deep:
+// 485 us value by value, 436 so).
 template <int V, class OUT>
-__device__ __forceinline__ void put_row_piece(OUT* c, int left, int vec, int accumulate, float bm, const float (&bn)[V],
+__device__ __forceinline__ void put_row_piece(OUT* c, int left, int accumulate, float bm, const float (&bn)[V],
                                               float (&v)[V]) {
   constexpr int BYTES = V * (int)sizeof(OUT);
   static_assert(BYTES == 16 || BYTES == 8, "");
 #pragma unroll
   for (int e = 0; e < V; ++e) v[e] += bn[e] + bm;
   OUT o[V];
-  if (vec && left >= V) {
+  if (left >= V) {
     if (accumulate) {
-      __builtin_memcpy(o, __builtin_assume_aligned(c, BYTES), BYTES);
+      __builtin_memcpy(o, c, BYTES);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] += widen(o[e]);
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) narrow(v[e], o[e]);
-    __builtin_memcpy(__builtin_assume_aligned(c, BYTES), o, BYTES);
+    __builtin_memcpy(c, o, BYTES);
   } else {
 #pragma unroll
     for (int e = 0; e < V; ++e)

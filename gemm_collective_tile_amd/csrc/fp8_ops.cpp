@@ -243,7 +243,6 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   a.C = C;
   a.c_type = (uint8_t)c_type;
   a.ldc = (int32_t)ldc;
-  a.vec = rows16(C, ldc, c_type);
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
