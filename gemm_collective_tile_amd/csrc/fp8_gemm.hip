@@ -472,54 +472,84 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
 
 }  // namespace
 
-// The plan with the least predicted time, from times in us measured on MI355X: a
-// step of k on a tile with a CU to itself and on two tiles that share one, for
-// 16-bit and for fp32 C; a workgroup's start and epilogue. Splitting the
-// contraction costs a launch (2.5) and each split's sums written and read (5
-// TB/s at these sizes, in the last-level cache). What it decides, kernel times:
-//   300 x 800 x 800      256: 35 us   128: 8.6   128 x 64: 7.1   64: 5.8
-//   512 x 4096 x 4096         52          24.6             20.8      20.6
-//   2048 x 4096 x 4096        60          41.8
-//   2048 x 11008 x 4096      115         104
-//   4096 x 4096 x 11008      152         186
-//   100 x 800 x 4096     64: 15.9 in one, 12.8 in two, 9.2 in four splits
-// Up to 96 rows of A the kernel for few rows competes, by what a CU loads at 66 GB/s
-// (with its occupied CUs; the chains above hide none of it):
+// The plan with the least predicted time, in us, from times measured on MI355X: a
+// step of k on a tile that has a CU to itself, with 2 and with 4 (64 x 64 only, by
+// their LDS) on each CU, and a workgroup's start and epilogue. Workgroups beyond
+// what the chip holds make further rounds; the last, partial one starts as CUs
+// fall free, so half its ends are hidden. Between 1 and 2 (2 and 4) a CU a step's
+// time rises at once by 0.4 of the way, then evenly. Splitting the contraction
+// costs a launch (2.5) and each split's sums written and read (5 TB/s at these sizes,
+// in the last-level cache). What it decides, kernel times, bf16 unless named:
+//                              256     128 x 128   128 x 64   64 x 64
+//   128 x 1024 x 1024          18.0        8.2        6.6       5.7
+//   2048 x 1024 x 4096         54.8       27.1       22.4      21.2
+//   2176 x 2048 x 4096         55.2       35.6       44.8      45.8
+//   2048 x 4096 x 2048         36.6       23.5       29.2      33.3
+//   2176 x 4096 x 2048 fp32    63.5       50.3       52.4      52.7
+//   4096 x 2048 x 4096         61.9       40.9       53.3      59.4
+//   5328 x 5536 x 416          35.9       36.9       47.5      45.6
+// and splits of 64 x 64 tiles:   1      2      4
+//   256 x 1024 x 4096           16.9   12.7   10.9
+//   784 x 389 x 5242            23.9   18.6   14.5
+//   182 x 4704 x 9980           37.3   29.5   28.9
+//   2048 x 1024 x 4096          21.2   26.5   33.5
+// The least sum of regrets over 42 such sizes leaves the choice 2 % from the best tile.
+// More LDS stages (five of each operand) leave all of these as they are.
+// Up to 96 rows of A the kernel for few rows competes, by what a CU loads at 66 GB/s:
 //   65 x 4096 x 4096     few 8.6, tiles 12.5      96 x 11008 x 4096 (fp32)   16.2, 26.8
 //   65 x 800 x 11008         14.0       11.9      96 x 2048 x 8192           14.5, 13.4
 // From 97 rows on its gain is gone (128 x 8192 x 8192: 23.8, 24.2; 128 x 4096 x 11008:
 // 24.9, 22.5), and up to 64 rows it loses by 4 % at most but where B has few rows.
-// More LDS stages (five of each operand) leave all of these as they are: small
-// tiles are bound by the chain of a step (operand read, product, barrier),
-// larger ones by a CU's load path, 55 GB/s.
+namespace {
+struct TileTimes {
+  int bm, bn, levels;       // levels: 1, 2, 4 tiles on a CU
+  double step[2][3], ends[2];   // of 16-bit and of fp32 C
+};
+constexpr TileTimes kTileTimes[] = {
+    {256, 256, 1, {{1.55}, {2.92}}, {11.0, 16.0}},
+    {128, 128, 2, {{0.66, 1.08}, {1.00, 1.90}}, {5.5, 6.5}},
+    {128, 64, 2, {{0.57, 0.75}, {0.80, 1.16}}, {3.6, 4.4}},
+    {64, 64, 3, {{0.43, 0.56, 0.815}, {0.61, 0.80, 1.26}}, {3.2, 4.0}},
+};
+
+// workgroups of `share` steps each
+double predicted(const TileTimes& t, int64_t wgs, int64_t share, bool fp32) {
+  const double* const step = t.step[fp32];
+  const double ends = t.ends[fp32];
+  const int64_t held = (int64_t)kFp8Cus << (t.levels - 1), rest = wgs % held;
+  double us = (double)(wgs / held) * (share * step[t.levels - 1] + ends);
+  if (rest > 0) {
+    int level = 0;
+    while (rest > (int64_t)kFp8Cus << level) ++level;
+    const double half = (double)((int64_t)kFp8Cus << level) / 2;
+    const double s = level == 0 ? step[0] : step[level - 1] + (step[level] - step[level - 1]) * (0.4 + 0.6 * (rest - half) / half);
+    us += share * s + (wgs > held && t.levels > 1 ? ends / 2 : ends);
+  }
+  return us;
+}
+}  // namespace
+
 Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32) {
-  static const struct {
-    int bm, bn;
-    double alone[2], shared[2], ends;
-  } tiles[] = {{128, 128, {0.60, 0.95}, {1.15, 1.80}, 4.5},
-               {128, 64, {0.46, 0.78}, {0.74, 1.16}, 4.0},
-               {64, 64, {0.42, 0.61}, {0.55, 0.87}, 3.0}};
-  const double step256 = fp32 ? 2.85 : 1.55, ends256 = 6.0;
-  const int64_t big = (M + 255) / 256 * ((N + 255) / 256), steps = (K + kBK - 1) / kBK;
   Fp8MmPlan best;
   if (M <= kFp8AlwaysFew) {
     best.bm = 0;
     return best;
   }
-  double least = (double)((big + kFp8Cus - 1) / kFp8Cus) * (steps * step256 + ends256);
-  for (const auto& tile : tiles) {
+  const int64_t steps = (K + kBK - 1) / kBK;
+  double least = 0;
+  for (const TileTimes& tile : kTileTimes) {
     const int64_t n_tiles = (M + tile.bm - 1) / tile.bm * ((N + tile.bn - 1) / tile.bn);
-    for (int64_t want = 1; want <= 16 && (want == 1 || n_tiles * want <= 2 * kFp8Cus); ++want) {
+    const int64_t held = (int64_t)kFp8Cus << (tile.levels - 1);
+    // 256 x 256 tiles are for large products and never split
+    for (int64_t want = 1; want == 1 || (want <= 16 && tile.levels > 1 && n_tiles * want <= held); ++want) {
       // shares are whole words of scale bytes
       const int64_t share = want == 1 ? steps : ((steps + want - 1) / want + 3) & ~(int64_t)3;
       const int64_t n = share > 0 ? (steps + share - 1) / share : 1;   // splits
       if (n != want) continue;
-      const double wgs = (double)n_tiles * n;
-      double t = wgs <= kFp8Cus ? share * tile.alone[fp32] + tile.ends
-                             : std::max(1.0, wgs / (2 * kFp8Cus)) * (share * tile.shared[fp32] + tile.ends);
-      if (n > 1) t += 2.5 + (double)n * M * N * 8 / 5e6;
-      if (t >= least) continue;
-      least = t;
+      double us = predicted(tile, n_tiles * n, share, fp32);
+      if (n > 1) us += 2.5 + (double)n * M * N * 8 / 5e6;
+      if (least > 0 && us >= least) continue;
+      least = us;
       best.bm = tile.bm;
       best.bn = tile.bn;
       best.splits = (int)n;

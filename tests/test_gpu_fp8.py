@@ -266,6 +266,19 @@ def test_mm_of_few_rows_and_many_columns(M, dtype, block):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,block", [("fp16", 128), ("bf16", 1), ("fp32", 1)])
+@pytest.mark.parametrize("M,N,K", [(2100, 2010, 300), (2054, 1936, 333), (857, 304, 4496), (130, 1000, 21000)])
+def test_mm_of_more_tiles_than_units_and_of_splits(M, N, K, dtype, block):
+    """128 x 128 tiles, two and four tiles a compute unit, and contractions in several parts."""
+    note(f"mm rounds {M}x{N}x{K} {dtype}")
+    A, B = made(sample(M, K, 1)), made(sample(N, K, 2, 0.0) / np.sqrt(K), block)
+    a, b = ref.values(*parts(A)), ref.values(*parts(B), block)
+    C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+    il.iris_fp8_mm(C, A, B)
+    check_product(C, a, b, None, None, dtype, (M, N, K, dtype))
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """Matrices of more than 4 GiB: their last rows are what the same rows alone give."""
     rows, cols = 270_000, 16_384                      # 4.4e9 values
