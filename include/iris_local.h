@@ -285,7 +285,8 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  * (weights). The last block of a row or column may be shorter; any number of
  * rows and columns >= 0 is served.
  *   codes      device, 16-byte aligned; row r starts at codes + r * ld, ld a
- *              multiple of 16 and >= the number of columns. The bytes of a
+ *              multiple of 16 (better 128: products run up to a quarter faster)
+ *              and >= the number of columns. The bytes of a
  *              row up to the next multiple of 16 are allocated; nothing is
  *              written past the last column and what is there is ignored.
  *   scales     device; block (i, j) is at scales + i * ld_scales + j. Operands

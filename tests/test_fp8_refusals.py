@@ -34,6 +34,11 @@ def test_fp8_handle_refuses():
         il.Fp8(tight, torch.zeros((4, 1), dtype=torch.uint8))
 
 
+def test_empty_gives_long_rows_whole_lines():
+    assert empty(3, 513).codes.stride() == (640, 1) and empty(3, 512).codes.stride() == (512, 1)
+    assert empty(2, 4095).codes.stride() == (4096, 1) and empty(2, 511).codes.stride() == (512, 1)
+
+
 def test_empty_lays_rows_out():
     q = empty(5, 130, 128)
     assert q.codes.stride() == (144, 1) and q.scales.shape == (1, 2) and q.scales.dtype == torch.float8_e8m0fnu
