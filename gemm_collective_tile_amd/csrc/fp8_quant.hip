@@ -365,20 +365,28 @@ __device__ __forceinline__ void swiglu_bwd_part(const Fp8SwigluBwdArgs& a, const
   BwdInputs<T> in;
   in.template load<WHOLE>(a, p);
   float v[1][4][kPiece];
+  // a wave has 16 rows: none of them there, nothing to form (1 x 11008: 4.1 us, otherwise 6.5)
+  if (p.r0 + 16 * __builtin_amdgcn_readfirstlane(p.t / 64) < p.nrows) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
-    float g[kPiece], u[kPiece];
-    decode(in.g[i], scale_value(in.sg[i]), on, g);
-    if constexpr (PART != 1) decode(in.u[i], scale_value(in.su[i]), on, u);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t on = on_mask(p.on(i) && p.col() < p.cols());
+      float g[kPiece], u[kPiece];
+      decode(in.g[i], scale_value(in.sg[i]), on, g);
+      if constexpr (PART != 1) decode(in.u[i], scale_value(in.su[i]), on, u);
 #pragma unroll
-    for (int c = 0; c < kPiece; ++c) {
-      const float s = sigmoid(g[c]), gs = g[c] * s;
-      if constexpr (PART == 0) v[0][i][c] = in.d[i].value(c) * u[c] * __builtin_fmaf(gs, 1.0f - s, s);
-      if constexpr (PART == 1) v[0][i][c] = in.d[i].value(c) * gs;
-      if constexpr (PART == 2) v[0][i][c] = gs * u[c];
+      for (int c = 0; c < kPiece; ++c) {
+        const float s = sigmoid(g[c]), gs = g[c] * s;
+        if constexpr (PART == 0) v[0][i][c] = in.d[i].value(c) * u[c] * __builtin_fmaf(gs, 1.0f - s, s);
+        if constexpr (PART == 1) v[0][i][c] = in.d[i].value(c) * gs;
+        if constexpr (PART == 2) v[0][i][c] = gs * u[c];
+      }
+      if constexpr (PART < 2) put_row<WHOLE>(PART == 0 ? a.dgate : a.dup, p, i, v[0][i], -1);
     }
-    if constexpr (PART < 2) put_row<WHOLE>(PART == 0 ? a.dgate : a.dup, p, i, v[0][i], -1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < kPiece; ++c) v[0][i][c] = 0.0f;
   }
   if (qt[0].codes) put_turned<1>(qt, p, v, -1, lds);
 }
