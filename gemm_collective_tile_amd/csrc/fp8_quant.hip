@@ -50,8 +50,8 @@ __device__ __forceinline__ void put_row_block(const Fp8Mat& q, const RowPlace& p
 
 // Bound by memory where the matrix is large: 8192 x 16384 in bf16 69.7 us, 5.8 TB/s
 // read and written (a 1 GiB copy runs at 5.1); 2048 x 4096 5.4 us; one row of
-// 4096 1.6 us, of which the launch is all. One block a thread group and no loop:
-// the many short workgroups keep more loads under way than a loop would.
+// 4096 1.6 us, of which the launch is all. Eight lanes a block and no loop, so that
+// every load of a round of workgroups is under way at once.
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(const T* x, int ldx, int rows, int cols, Fp8Mat q, FastDiv nkb) {
   const RowPlace p(rows, nkb);
@@ -225,8 +225,8 @@ __device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace& p, int
 
 // x -> rows and / or columns, or 128 x 128 blocks. Both directions of 8192 x 16384
 // in bf16 112 us, 4.8 TB/s (a 1 GiB copy: 5.1); 4096 x 11008 40 us; 128 x 128 blocks
-// of 11008 x 4096 in fp32, both directions, 54 us, 5.0 TB/s; 8 bits turned around,
-// 4096 x 4096, 9.9 us. The small ones are one round of workgroups, which load, turn
+// of 11008 x 4096 in fp32, both directions, 53 us, 5.1 TB/s; 8 bits turned around,
+// 4096 x 4096, 8.2 us. The small ones are one round of workgroups, which load, turn
 // and store in step: what one waits for is not hidden by another. 128 x 128 is the
 // least tile that holds whole blocks of both directions.
 template <class T, bool WHOLE>
@@ -305,10 +305,9 @@ struct BwdInputs {
 // registers are free: 113 a thread, so 4 waves fit a SIMD. All three at once
 // spill at that width (4096 x 11008: 143 us against 100), and with 2 waves a SIMD,
 // the next tile's loads under way, take 123; 6 waves a SIMD, the results formed one
-// at a time, 164. 4096 x 11008 in bf16: 101 us, 4.0 TB/s: the vector units are
-// busy two thirds of the time (41 instructions a value, two of them exp and two
-// rcp) and 4 waves a SIMD hide the rest of the waiting only in part; 1001 x 1376 in
-// fp16 12 us, a round of 88 workgroups.
+// at a time, 164. 4096 x 11008 in bf16: 100 us, 4.1 TB/s; its loads and stores with
+// nothing formed between them take 88, the vector units are busy two thirds of the
+// time (40 instructions a value, two of them exp and two rcp).
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs a, FastDiv ncb) {
   __shared__ TileLds<2> lds;

@@ -295,7 +295,7 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  * The structs are read before the call returns; the buffers belong to the
  * caller. Unlike above, plain matrices (x, C, gate, up, dh) may have any row
  * pitch >= their columns and need only the alignment of their type; rows that
- * start at multiples of 16 bytes are faster.
+ * start at multiples of 16 bytes are a little faster.
  * Limits (IRIS_ERR_UNSUPPORTED beyond): row pitches of codes, scales and plain
  * matrices up to 2^22, rows and columns up to 2^30 with fewer than 2^31 blocks of
  * 128 along either direction, K of a product up to 2^21 and up to 2^30 output
