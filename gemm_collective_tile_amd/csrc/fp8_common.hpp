@@ -124,16 +124,16 @@ struct Piece {
   }
   template <bool WHOLE>
   __device__ __forceinline__ void load(const T* x, uint32_t row, int col, int cols, bool on, bool more) {
-    // a piece that is off reads another one of the row and drops it: no branch
+    // a piece that is off reads the row's first one and drops it: no branch
     // between the loads
     static_assert(N % 4 == 0, "piece shorter than a 16-byte load");
     on = on && col < cols;
-    const uint32_t at = row + (col < cols ? col : 0), m = on_mask(on);
+    const uint32_t at = row + (on ? col : 0), m = on_mask(on);
     const char* const first = (const char*)x + at * (uint32_t)sizeof(T);
     if constexpr (WHOLE) {
       take<u32x4>(first);
     } else {
-      const int n = cols - (col < cols ? col : 0);   // values up to the row's end
+      const int n = cols - (on ? col : 0);   // values up to the row's end
       if (n >= C || more) {
         take<std::conditional_t<sizeof(T) == 2, u32x4_at_2, u32x4_at_4>>(first);
       } else {
