@@ -393,9 +393,9 @@ __device__ __forceinline__ void swiglu_bwd_part(const Fp8SwigluBwdArgs& a, const
 // The same with a workgroup for each result of a tile (blockIdx.y), for matrices of
 // few tiles: the vector units of one CU take 4.4 us for all three of a tile while
 // others are idle. In fp16, one workgroup a tile and three:
-//     16 x 1376    7.9 us   5.0        2048 x 1920   12.7   12.5
-//   1001 x 1376   11.6      9.1        2048 x 2688   17.5   15.3
-//   1024 x 2048   10.4      8.6        2048 x 4096   18.6   19.7
+//     16 x 1376    7.9 us   4.3        2048 x 1920   12.7   12.4
+//   1001 x 1376   11.6      8.2        2048 x 2688   17.5   15.3
+//   1024 x 2048   10.4      8.4        2048 x 4096   18.6   19.7
 // so as long as four workgroups a CU hold them all.
 constexpr uint32_t kPartsTiles = 4 * kFp8Cus / 3;
 template <class T, bool WHOLE>
