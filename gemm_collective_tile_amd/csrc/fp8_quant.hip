@@ -121,7 +121,8 @@ struct TilePlace {
 };
 __device__ __forceinline__ uint32_t offset(uint32_t row, int64_t ld) { return __umul24(row, (uint32_t)ld); }
 
-// LDS of N tiles' turn: the transposed codes and the columns' scales
+// LDS of up to N tiles' turn: the transposed codes and the columns' scales. The
+// three arrays share no byte: put_turned relies on it from one call to the next.
 template <int N>
 struct TileLds {
   static constexpr int WAVES = TilePlace::T / 64;
@@ -138,12 +139,15 @@ __device__ __forceinline__ int turn_word(int col, int word) {
 }
 
 // Writes the transposed codes and scales of N tiles of values (of those whose
-// codes are not NULL). All threads of the workgroup call it; the LDS may be the
-// one of an earlier call. given >= 0: the scale byte of every block (128 x 128
-// blocks), already written.
-template <int N>
+// codes are not NULL). All threads of the workgroup call it. given < 0: the LDS
+// may be the one of an earlier call, as the same TileLds<L>: waves that are still
+// there read `turn` only, which this call writes behind its second barrier, and
+// `part` and `scale`, which it writes before, lie outside it. given >= 0: the scale
+// byte of every block (128 x 128 blocks), already written, and no call came before.
+template <int N, int L>
 __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlace& p, const float (&v)[N][4][kPiece],
-                                           int given, TileLds<N>& lds) {
+                                           int given, TileLds<L>& lds) {
+  static_assert(N <= L, "more tiles than the LDS holds");
   constexpr int T = TilePlace::T;
   const int t = p.t;
   if (given < 0) {
@@ -171,7 +175,7 @@ __device__ __forceinline__ void put_turned(const Fp8Mat (&qt)[N], const TilePlac
       const int n = t / kTile, c = t % kTile;
       uint32_t a = 0;
 #pragma unroll
-      for (int w = 0; w < TileLds<N>::WAVES; ++w) a = max(a, lds.part[n][w][c]);
+      for (int w = 0; w < TileLds<L>::WAVES; ++w) a = max(a, lds.part[n][w][c]);
       const uint32_t b = scale_byte(a);
       lds.scale[n][c] = scale_value(b);
 #pragma unroll
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(TilePlace::T) void fp8_tile_kernel(Fp8QuantArgs a, 
   }
   if (a.qt.codes) {
     const Fp8Mat qt[1] = {a.qt};
-    put_turned<1>(qt, p, all, given, lds);
+    put_turned(qt, p, all, given, lds);
   }
 }
 
@@ -334,7 +338,7 @@ __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs
     }
     if (a.dgate_t.codes || a.dup_t.codes) {
       const Fp8Mat qt[2] = {a.dgate_t, a.dup_t};
-      put_turned<2>(qt, p, v, -1, lds);
+      put_turned(qt, p, v, -1, lds);
     }
   }
   if (a.h_t.codes) {
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(512, 4) void fp8_swiglu_bwd_kernel(Fp8SwigluBwdArgs
       __builtin_amdgcn_sched_barrier(0);
     }
     const Fp8Mat qt[1] = {a.h_t};
-    put_turned<1>(qt, p, v, -1, *(TileLds<1>*)&lds);
+    put_turned(qt, p, v, -1, lds);
   }
 }
 
@@ -387,7 +391,7 @@ __device__ __forceinline__ void swiglu_bwd_part(const Fp8SwigluBwdArgs& a, const
 #pragma unroll
       for (int c = 0; c < kPiece; ++c) v[0][i][c] = 0.0f;
   }
-  if (qt[0].codes) put_turned<1>(qt, p, v, -1, lds);
+  if (qt[0].codes) put_turned(qt, p, v, -1, lds);
 }
 
 // The same with a workgroup for each result of a tile (blockIdx.y), for matrices of

@@ -517,6 +517,46 @@ def check_gradient(q, want, size, what):
     assert_untouched(q, what)
 
 
+def from_gpu(x):
+    """An Fp8 operand of x's values, made by the library (whose codes other tests compare bit for bit)."""
+    q = il.iris_fp8_empty(*x.shape)
+    il.iris_fp8_quantize(torch.from_numpy(x).to(torch.float32).cuda(), q)
+    return q
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(2432, 2432), (2433, 2437)])
+def test_swiglu_bwd_of_many_tiles(rows, cols, dtype):
+    """More than 341 tiles: one workgroup forms all results of a tile, its second
+    turn in the shared memory of the first. Every choice of the transposed outputs
+    gives the same bits as all of them together."""
+    note(f"swiglu_bwd {rows}x{cols} {dtype}")
+    gk, uk = from_gpu(sample(rows, cols, 1)), from_gpu(sample(rows, cols, 2))
+    g, u = ref.values(*parts(gk)), ref.values(*parts(uk))
+    dh, dv = on_gpu(sample(rows, cols, 3) / 64, dtype, *((cols + 3, 1) if cols % 2 else ()))
+    wg, wu = ref.swiglu_bwd(g, u, dv)
+    wants = {"dgate": wg, "dup": wu, "dgate_t": wg.T, "dup_t": wu.T, "h_t": ref.swiglu(g, u).T}
+    whole = None
+    for turned in (("dgate_t", "dup_t", "h_t"), (), ("dgate_t",), ("dup_t",), ("h_t",), ("dgate_t", "dup_t"),
+                   ("dgate_t", "h_t"), ("dup_t", "h_t")):
+        note(f"  with {turned}")
+        out = {k: fresh(rows, cols) for k in ("dgate", "dup")}
+        out.update({k: fresh(cols, rows) for k in turned})
+        il.iris_fp8_swiglu_bwd(out["dgate"], out["dup"], dh, gk, uk, out.get("dgate_t"), out.get("dup_t"), out.get("h_t"))
+        if whole is None:
+            whole = out
+            for k, q in out.items():
+                check_gradient(q, wants[k], wg_size(g, u, dv, k), k)
+            again = {k: fresh(*q.shape) for k, q in out.items()}
+            il.iris_fp8_swiglu_bwd(again["dgate"], again["dup"], dh, gk, uk, again["dgate_t"], again["dup_t"], again["h_t"])
+            out = again
+        for k, q in out.items():
+            assert torch.equal(q.codes.view(torch.uint8), whole[k].codes.view(torch.uint8)), (turned, k)
+            assert torch.equal(q.scales.view(torch.uint8), whole[k].scales.view(torch.uint8)), (turned, k)
+            assert_untouched(q, k)
+
+
 # --------------------------------------------------------- streams and graphs
 
 @pytest.mark.gpu
