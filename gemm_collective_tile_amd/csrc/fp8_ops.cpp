@@ -5,12 +5,13 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include "fp8.hpp"
 
@@ -113,27 +114,53 @@ int ready() {
 // ------------------------------------------------------------- workspace
 // The split products' sums, one buffer per (device, stream). Every split plan
 // fits kOwnBytes (at most 512 tiles of 128 x 128 fp32 sums), so a buffer never
-// grows and nothing waits for the stream. It needs no clearing.
+// grows and nothing waits for the stream. It needs no clearing. A split product
+// is two launches: whoever enqueues them holds the buffer's lock over both, so
+// that host threads that share a stream do not put one product's sums between
+// the other's sums and their joining. The per-thread default stream is a stream
+// of each thread under one handle: there the thread is part of the key.
 constexpr size_t kOwnBytes = (size_t)512 * 128 * 128 * 4;
-std::mutex g_mu;
-std::map<std::pair<int, void*>, void*> g_own;
+struct OwnWorkspace {
+  std::mutex mu;
+  void* ptr = nullptr;
+};
+struct OwnKey {
+  int dev;
+  void* stream;
+  uint64_t thread;   // 0 but for hipStreamPerThread
+  bool operator<(const OwnKey& o) const { return std::tie(dev, stream, thread) < std::tie(o.dev, o.stream, o.thread); }
+};
+std::mutex g_mu;   // of the map; its entries stay
+std::map<OwnKey, OwnWorkspace> g_own;
 
-int own_workspace(int dev, void* stream, size_t need, void** out) {
+// a number of this thread that no other thread has or will have
+uint64_t thread_number() {
+  static std::atomic<uint64_t> count{0};
+  thread_local const uint64_t mine = ++count;
+  return mine;
+}
+
+// The buffer, locked by `hold` until the caller has enqueued all its launches.
+int own_workspace(int dev, void* stream, size_t need, void** out, std::unique_lock<std::mutex>* hold) {
   try {
-    std::lock_guard<std::mutex> lk(g_mu);
-    void*& p = g_own[{dev, stream}];
-    if (!p) {
+    OwnWorkspace* w;
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      w = &g_own[{dev, stream, stream == (void*)hipStreamPerThread ? thread_number() : 0}];
+    }
+    *hold = std::unique_lock<std::mutex>(w->mu);
+    if (!w->ptr) {
       // allocating is no stream operation: allowed while a stream captures
       hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
       (void)hipThreadExchangeStreamCaptureMode(&mode);
-      const hipError_t e = hipMalloc(&p, std::max(need, kOwnBytes));
+      const hipError_t e = hipMalloc(&w->ptr, std::max(need, kOwnBytes));
       (void)hipThreadExchangeStreamCaptureMode(&mode);
       if (e != hipSuccess) {
-        p = nullptr;
+        w->ptr = nullptr;
         return fail(IRIS_ERR_NO_MEMORY, "hipMalloc of a %zu-byte workspace failed: %s", kOwnBytes, hipGetErrorString(e));
       }
     }
-    *out = p;
+    *out = w->ptr;
     return IRIS_OK;
   } catch (const std::exception& e) {
     return fail(IRIS_ERR_NO_MEMORY, "workspace: %s", e.what());
@@ -157,12 +184,17 @@ int fp8_finalize() {
   std::lock_guard<std::mutex> lk(g_mu);
   int status = IRIS_OK;
   for (auto& kv : g_own) {
-    if (!kv.second) continue;
-    (void)hipSetDevice(kv.first.first);
-    (void)hipStreamSynchronize((hipStream_t)kv.first.second);
-    if (hipFree(kv.second) != hipSuccess) status = IRIS_ERR_HIP;
+    std::lock_guard<std::mutex> hold(kv.second.mu);
+    if (!kv.second.ptr) continue;
+    (void)hipSetDevice(kv.first.dev);
+    // another thread's default stream cannot be named here
+    if (kv.first.thread)
+      (void)hipDeviceSynchronize();
+    else
+      (void)hipStreamSynchronize((hipStream_t)kv.first.stream);
+    if (hipFree(kv.second.ptr) != hipSuccess) status = IRIS_ERR_HIP;
+    kv.second.ptr = nullptr;
   }
-  g_own.clear();
   return status;
 }
 }  // namespace iris
@@ -232,7 +264,8 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   if (workspace && (uintptr_t)workspace % 256 != 0) return fail(IRIS_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
   int dev = 0, cus = 0;
   if ((st = iris::use_device(&dev, &cus))) return st;
-  if (plan.ws_bytes > 0 && !workspace && (st = own_workspace(dev, stream, plan.ws_bytes, &workspace))) return st;
+  std::unique_lock<std::mutex> hold;   // over both launches of a split product
+  if (plan.ws_bytes > 0 && !workspace && (st = own_workspace(dev, stream, plan.ws_bytes, &workspace, &hold))) return st;
   iris::Fp8MmArgs a{};
   a.A = mat(A);
   a.B = mat(B);

@@ -348,9 +348,11 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
  * 256-byte aligned, contents of no account; not the workspace of an op above,
  * which has to stay zeroed. NULL: the library's own, 32 MiB per (device,
  * stream), allocated by the first call that needs it (also during a graph
- * capture, whose replays then use it) and freed by iris_finalize(). One
- * workspace may not serve two calls at the same time: graphs captured on one
- * stream that replay side by side need one each.
+ * capture, whose replays then use it) and freed by iris_finalize(). Host threads
+ * may share a stream; on the per-thread default stream each thread has its own
+ * 32 MiB. One workspace may not serve two calls at the same time: graphs captured
+ * on one stream that replay side by side need one each, and so do host threads
+ * that pass theirs.
  */
 int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B,
                 const void* bias, int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace,

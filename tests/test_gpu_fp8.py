@@ -10,6 +10,8 @@ all. Sums of small integers are exact. Computed activations: the value before it
 8-bit rounding is good to 1e-5 (the hardware's exp2 and reciprocal), its code
 to half an e4m3 step more.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -607,3 +609,31 @@ def test_other_stream_and_graph_replay():
         step()
         for a, b in zip(results(), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_split_products_of_threads_that_share_a_stream():
+    """Split contractions from several host threads, on one stream (one workspace) and on streams of their own."""
+    note("split products from threads")
+    M, N, K = 260, 390, 4100
+    assert il.iris_fp8_mm_workspace_size(M, N, K) > 0
+    ops = [(made(sample(M, K, t)), made(sample(N, K, 10 + t, 0.0) / np.sqrt(K), 128)) for t in range(4)]
+    wants = [torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in ops]
+    for (A, B), C in zip(ops, wants):
+        il.iris_fp8_mm(C, A, B)
+    torch.cuda.synchronize()
+    for streams in ([torch.cuda.current_stream()] * 4, [torch.cuda.Stream() for _ in ops]):
+        outs = [[torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(30)] for _ in ops]
+        torch.cuda.synchronize()
+
+        def calls(t):
+            for C in outs[t]:
+                il.iris_fp8_mm(C, *ops[t], stream=streams[t])
+        threads = [threading.Thread(target=calls, args=(t,)) for t in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for t in range(4):
+            assert all(torch.equal(C, wants[t]) for C in outs[t]), t
