@@ -166,13 +166,16 @@ struct Piece {
     }
   }
 };
+// The values, any signalling NaN quiet: the maxima below drop the neighbour of a
+// signalling one. Conversion from fp16 has that effect, bf16 and fp32 come as they
+// are (one instruction a value; computed values are quiet by themselves).
 template <bool WHOLE, int C, class T>
 __device__ __forceinline__ void load_piece(const T* x, uint32_t row, int col, int cols, bool on, bool more,
                                            float (&v)[C]) {
   Piece<T, C> p;
   p.template load<WHOLE>(x, row, col, cols, on, more);
 #pragma unroll
-  for (int i = 0; i < C; ++i) v[i] = p.value(i);
+  for (int i = 0; i < C; ++i) v[i] = std::is_same_v<T, f16> ? p.value(i) : __builtin_canonicalizef(p.value(i));
 }
 
 // 8 consecutive codes. Rows of codes start at multiples of 16 bytes, which are
@@ -242,8 +245,10 @@ __device__ __forceinline__ void encode_piece(const float (&v)[C], float scale, u
 }
 
 // Largest magnitudes, as bits. v_max3_f32 takes two values at once and their
-// magnitudes for free; an infinity (or a signalling NaN) leaves something that
-// is not finite, and only then are the values looked at one by one.
+// magnitudes for free, and passes over a quiet NaN (values are quiet here, see
+// load_piece: at a signalling NaN it would pass over the other value as well). An
+// infinity, or nothing but NaN, leaves something that is not finite, and only
+// then are the values looked at one by one.
 __device__ __forceinline__ float max_abs(float a, float b) {
   float m;
   asm("v_max_f32 %0, |%1|, |%2|" : "=v"(m) : "v"(a), "v"(b));

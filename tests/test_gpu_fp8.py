@@ -183,6 +183,63 @@ def test_quantize_special_values(dtype):
             check_quantized(q, xv, 1, "rows alone")
 
 
+SIGNALLING = {"fp16": 0x7c01, "bf16": 0x7f81, "fp32": 0x7f800001}
+
+
+def with_nan_beside_the_largest(dtype, rows, cols, places):
+    """Ordinary values with, for every (row, column, other column) of `places`, a signalling NaN and, at the other
+    column, a value that is the largest of all its blocks; on the GPU, and in float64."""
+    v = sample(rows, cols, 11, 0.0)
+    for n, (r, c, o) in enumerate(places):
+        v[r, o] = 3000.0 + n
+    x, _ = on_gpu(v, dtype)
+    bits = x.view(torch.int32 if dtype == "fp32" else torch.int16)
+    sign = 1 << (31 if dtype == "fp32" else 15)
+    for n, (r, c, o) in enumerate(places):
+        bits[r, c] = SIGNALLING[dtype] - (sign if n % 2 else 0)    # both signs
+    values = x.double().cpu().numpy()
+    assert np.isnan(values).sum() == len(places)
+    return x, values
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DT))
+def test_quantize_signalling_nan_leaves_the_scale(dtype):
+    """A signalling NaN at every place of a piece, its neighbours in the hardware's pairs the largest of their blocks."""
+    for cols in (256, 253):
+        note(f"quantize signalling NaN {dtype} {cols}")
+        diagonal = [(p, p, p ^ 1) for p in range(128)] + [(p, 128 + p, 128 + (p + 1) % 125) for p in range(0, 125, 2)]
+        x, xv = with_nan_beside_the_largest(dtype, 128, cols, diagonal)
+        q, qt = fresh(128, cols), fresh(cols, 128)
+        il.iris_fp8_quantize(x, q)
+        check_quantized(q, xv, 1, "rows")
+        q = fresh(128, cols)
+        il.iris_fp8_quantize(x, q, qt)
+        check_quantized(q, xv, 1, "rows of both")
+        check_quantized(qt, np.ascontiguousarray(xv.T), 1, "columns")
+    places = [(128 * i + 3 * i + j, 128 * j + 8 * i + 2 * j + i % 2, 128 * j + (8 * i + 2 * j + i % 2 ^ 1))
+              for i in range(4) for j in range(4)]
+    x, xv = with_nan_beside_the_largest(dtype, 512, 512, places)
+    q, qt = fresh(512, 512, 128), fresh(512, 512, 128)
+    il.iris_fp8_quantize(x, q, qt)
+    check_quantized(q, xv, 128, "blocks")
+    check_quantized(qt, np.ascontiguousarray(xv.T), 128, "blocks of columns")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_swiglu_signalling_nan_leaves_the_scale(dtype):
+    diagonal = [(p, p, p ^ 1) for p in range(128)]
+    note(f"swiglu signalling NaN {dtype}")
+    gate, gv = with_nan_beside_the_largest(dtype, 128, 128, diagonal)
+    up, uv = with_nan_beside_the_largest(dtype, 128, 128, [(p, p ^ 3, p ^ 2) for p in range(128)])
+    h, gk, uk = (fresh(128, 128) for _ in range(3))
+    il.iris_fp8_swiglu(h, gate, up, gk, uk)
+    check_quantized(gk, gv, 1, "gate")
+    check_quantized(uk, uv, 1, "up")
+    assert np.array_equal((parts(h)[0] & 0x7f) == 0x7f, np.isnan(gv) | np.isnan(uv))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,cols", SHAPES)
 def test_quantize_kept(rows, cols):
