@@ -422,12 +422,13 @@ class Fp8:
     `block` 1 (a scale for every 1 x 128 entries) or 128 (128 x 128). An entry's
     value is its code times 2^(scale byte - 127). Rows of codes start at
     multiples of 16 bytes and, in an operand of iris_fp8_mm, rows of scales at
-    multiples of 4 (iris_fp8_empty lays memory out that way).
+    multiples of 4; the last row is followed by memory up to the next such
+    multiple (iris_fp8_empty lays memory out that way).
 
     The object is a handle: it reads the tensors' addresses once and holds the
     tensors, so their memory must not be exchanged (set_, resize_) under it.
     """
-    __slots__ = ("codes", "scales", "block", "shape", "_c", "_p", "_on_gpu")
+    __slots__ = ("codes", "scales", "block", "shape", "_c", "_p", "_on_gpu", "_scale_words")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, block: int = 1):
         rows, cols = _shape2(codes, "codes")
@@ -450,6 +451,9 @@ class Fp8:
             end = codes.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
             if end > codes.untyped_storage().nbytes():
                 raise ValueError("the last row of codes must be followed by memory up to the next multiple of 16 bytes")
+        # whether the scales can be read in words of four, as products do
+        end = scales.storage_offset() + (scales.shape[0] - 1) * lds + -(-scales.shape[1] // 4) * 4
+        self._scale_words = scales.numel() == 0 or end <= scales.untyped_storage().nbytes()
         self.codes, self.scales, self.block, self.shape = codes, scales, block, (rows, cols)
         self._on_gpu = codes.is_cuda
         self._c = _Fp8(codes.data_ptr(), scales.data_ptr(), ld, lds, block)
@@ -538,6 +542,9 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
     N = B.shape[0]
     if B.shape[1] != K:
         raise ValueError(f"B has shape {B.shape}, expected ({N}, {K})")
+    if not (A._scale_words and B._scale_words):
+        raise ValueError(f"the last row of {'B' if A._scale_words else 'A'}'s scales must be followed by memory up to the "
+                         "next multiple of 4 bytes; see iris_fp8_empty")
     if not isinstance(C, torch.Tensor) or C.shape != (M, N):
         _want_shape(C, (M, N), "C")
     flags = IRIS_FLAG_ACCUMULATE if accumulate else 0

@@ -83,6 +83,21 @@ def test_mm_refuses():
     expect(ValueError, "on a GPU", f, C, A, B)
 
 
+def test_mm_refuses_scales_that_end_inside_a_word():
+    """Products read a row's scales four at a time: the last row needs memory up to the next multiple of 4."""
+    codes, C = torch.zeros((1, 304), dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.float16)
+    whole = empty(1, 300)
+    tight = il.Fp8(codes[:, :300], torch.zeros((1, 3), dtype=torch.uint8))
+    pitched = torch.zeros(8 + 5, dtype=torch.uint8).as_strided((2, 5), (8, 1))
+    weight = il.Fp8(torch.zeros((129, 640), dtype=torch.uint8), pitched, 128)
+    late = il.Fp8(codes[:, :300], torch.zeros(8, dtype=torch.uint8)[5:].reshape(1, 3))
+    for A, B, name in ((tight, whole, "A"), (whole, tight, "B"), (late, whole, "A"), (empty(1, 640), weight, "B")):
+        expect(ValueError, f"{name}'s scales", il.iris_fp8_mm, torch.zeros((1, B.shape[0]), dtype=torch.float16), A, B)
+    roomy = il.Fp8(codes[:, :300], torch.zeros((1, 4), dtype=torch.uint8)[:, :3])
+    expect(ValueError, "on a GPU", il.iris_fp8_mm, C, roomy, whole)
+    expect(ValueError, "on a GPU", il.iris_fp8_mm, C, il.Fp8(codes[:, :0], torch.zeros((1, 0), dtype=torch.uint8)), empty(1, 0))
+
+
 def test_swiglu_refuses():
     g, h = torch.zeros((6, 200), dtype=torch.float16), empty(6, 200)
     f = il.iris_fp8_swiglu
