@@ -509,6 +509,17 @@ def _plain(t, name: str, kinds, rows: int, cols: int):
     return t.data_ptr(), kind, (ld if rows > 1 else cols)
 
 
+def _fp8_ws(workspace):
+    """(pointer, bytes) of a caller's workspace, which the kernels write from its first byte on."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if not workspace.is_cuda:
+        raise ValueError("workspace must be on a GPU")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 _FP8_HALVES = {torch.float16: 1, torch.bfloat16: 2}
 
 
@@ -547,6 +558,7 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
                          "next multiple of 4 bytes; see iris_fp8_empty")
     if not isinstance(C, torch.Tensor) or C.shape != (M, N):
         _want_shape(C, (M, N), "C")
+    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace)
     flags = IRIS_FLAG_ACCUMULATE if accumulate else 0
     bias_ptr = None
     if bias is not None:
@@ -562,7 +574,6 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
         if not bias.is_cuda:
             raise ValueError("bias must be on a GPU")
         bias_ptr = bias.data_ptr()
-    ws, wsb = (None, 0) if workspace is None else _ws(workspace)
     st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8(A, A.shape, "A"), _fp8(B, B.shape, "B"), bias_ptr, M, N, K, flags, ws,
                           wsb, _current_stream(_current_device()) if stream is None else _stream(stream))
     if st:

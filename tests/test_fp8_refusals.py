@@ -98,6 +98,14 @@ def test_mm_refuses_scales_that_end_inside_a_word():
     expect(ValueError, "on a GPU", il.iris_fp8_mm, C, il.Fp8(codes[:, :0], torch.zeros((1, 0), dtype=torch.uint8)), empty(1, 0))
 
 
+def test_mm_refuses_workspaces():
+    A, B, C = empty(100, 200), empty(90, 200), torch.zeros((100, 90), dtype=torch.float16)
+    f = il.iris_fp8_mm
+    expect(ValueError, "workspace must be on a GPU", f, C, A, B, workspace=torch.zeros(1 << 20))
+    expect(ValueError, "workspace must be contiguous", f, C, A, B, workspace=torch.zeros(1 << 20)[::2])
+    expect(TypeError, "workspace must be a torch tensor", f, C, A, B, workspace=1 << 20)
+
+
 def test_swiglu_refuses():
     g, h = torch.zeros((6, 200), dtype=torch.float16), empty(6, 200)
     f = il.iris_fp8_swiglu
