@@ -8,6 +8,10 @@
 
 namespace iris {
 
+// A launch's threads are counted in 32 bits (beyond, the count wraps without an error).
+constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 1;     // tiles of 128 x 128, 512 threads each
+constexpr int64_t kMaxMmTiles = ((int64_t)1 << 24) - 256; // of a product, 256 threads each, in rounds of 256
+
 enum Fp8Type : int32_t { T_FP16 = 1, T_BF16 = 2, T_FP32 = 3, T_FP8 = 4 };
 
 struct Fp8MmArgs {

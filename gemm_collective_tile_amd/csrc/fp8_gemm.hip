@@ -543,6 +543,7 @@ Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32) {
   for (const TileTimes& tile : kTileTimes) {
     const int64_t n_tiles = (M + tile.bm - 1) / tile.bm * ((N + tile.bn - 1) / tile.bn);
     const int64_t held = (int64_t)kFp8Cus << (tile.levels - 1);
+    if (n_tiles > kMaxMmTiles) continue;
     // 256 x 256 tiles are for large products and never split
     for (int64_t want = 1; want == 1 || (want <= 16 && tile.levels > 1 && n_tiles * want <= held); ++want) {
       // shares are whole words of scale bytes

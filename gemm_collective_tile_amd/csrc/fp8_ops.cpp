@@ -56,6 +56,13 @@ int check_dims(int64_t rows, int64_t cols) {
   return IRIS_OK;
 }
 
+// of the operators that work on tiles of 128 x 128, one launch for all
+int check_tiles(int64_t rows, int64_t cols) {
+  if (blocks(rows) * blocks(cols) > iris::kMaxTiles)
+    return fail(IRIS_ERR_UNSUPPORTED, "matrix too large (limit: fewer than 2^23 tiles of 128 x 128)");
+  return IRIS_OK;
+}
+
 int check_fp8(const iris_fp8_t* q, int64_t rows, int64_t cols, const char* name) {
   if (!q) return fail(IRIS_ERR_INVALID_ARG, "%s is NULL", name);
   if (q->block != 1 && q->block != kBlk)
@@ -171,8 +178,9 @@ int check_mm_dims(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0)
     return fail(IRIS_ERR_INVALID_ARG, "M, N, K must not be negative (got %lld, %lld, %lld)", (long long)M, (long long)N,
                 (long long)K);
-  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 21) || blocks(M) * blocks(N) > (1 << 30))
-    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N <= 2^30, K <= 2^21, 2^30 output blocks)");
+  // the largest tile, 256 x 256, has to fit one launch
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 21) || (M + 255) / 256 * ((N + 255) / 256) > iris::kMaxMmTiles)
+    return fail(IRIS_ERR_UNSUPPORTED, "shape too large (limits: M, N <= 2^30, K <= 2^21, fewer than 2^24 output tiles of 256 x 256)");
   return IRIS_OK;
 }
 
@@ -213,6 +221,7 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
     return fail(IRIS_ERR_INVALID_ARG, "q and q_t have different blocks (%d, %d)", q->block, q_t->block);
   iris::Fp8QuantArgs a{};
   a.block = q ? q->block : q_t->block;
+  if ((q_t || a.block != 1) && (st = check_tiles(rows, cols))) return st;
   if (x8) {
     if (x) return fail(IRIS_ERR_INVALID_ARG, "x and x8 are both given");
     if (q || a.block != 1)
@@ -321,6 +330,7 @@ int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const ir
   iris::set_error(IRIS_OK, "");
   int st;
   if ((st = check_dims(rows, cols)) || (st = check_dims(cols, rows))) return st;
+  if ((st = check_tiles(rows, cols))) return st;
   const struct {
     const iris_fp8_t* q;
     const char* name;

@@ -13,6 +13,8 @@
 //          instead of 8.2, 1 x 4096 3.6 instead of 3.3); codes of 4 rows of
 //          one column are one 32-bit word of the transposed tile, which turns
 //          around in LDS and leaves in rows of 128 bytes.
+#include <algorithm>
+
 #include "fp8.hpp"
 
 namespace iris {
@@ -415,22 +417,41 @@ __global__ __launch_bounds__(512) void fp8_swiglu_bwd_parts_kernel(Fp8SwigluBwdA
 
 uint32_t blocks_of(int n) { return (uint32_t)((n + kFp8Block - 1) / kFp8Block); }
 
+// Calls launch(first row, rows, grid) for parts of the rows whose blocks, 8 threads
+// each, are 2^31 threads at most.
+template <class F>
+hipError_t by_rows(int rows, uint32_t nkb, F launch) {
+  const int part = (int)(((uint32_t)1 << 28) / nkb);
+  for (int r = 0; r < rows;) {
+    const int n = std::min(part, rows - r);
+    launch(r, n, dim3(((uint32_t)n * nkb * 8 + kThreads - 1) / kThreads));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    r += n;
+  }
+  return hipSuccess;
+}
+Fp8Mat from_row(const Fp8Mat& q, int r) {
+  return Fp8Mat{q.codes + (int64_t)r * q.ld, q.scales + (int64_t)r * q.lds, q.ld, q.lds};
+}
+
 // Values, types and whether all pieces of 16 are whole and aligned choose the kernel.
 template <bool WHOLE>
 hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
   const FastDiv d = FastDiv::make(nkb);
   if (a.block == 1 && !a.qt.codes) {
-    const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads)), block(kThreads);
-#define ROWS(T) \
-  hipLaunchKernelGGL((fp8_rows_kernel<T, WHOLE>), grid, block, 0, s, (const T*)a.x, a.ldx, a.rows, a.cols, a.q, d)
-    switch (a.x_type) {
-      case T_FP16: ROWS(f16); break;
-      case T_BF16: ROWS(bf16); break;
-      default: ROWS(float); break;
-    }
+    return by_rows(a.rows, nkb, [&](int r, int rows, dim3 grid) {
+#define ROWS(T)                                                                                                      \
+  hipLaunchKernelGGL((fp8_rows_kernel<T, WHOLE>), grid, dim3(kThreads), 0, s, (const T*)a.x + (int64_t)r * a.ldx, a.ldx, \
+                     rows, a.cols, from_row(a.q, r), d)
+      switch (a.x_type) {
+        case T_FP16: ROWS(f16); break;
+        case T_BF16: ROWS(bf16); break;
+        default: ROWS(float); break;
+      }
 #undef ROWS
-    return hipGetLastError();
+    });
   }
   const dim3 grid(blocks_of(a.rows) * nkb), block(TilePlace::T);
   switch (a.x_type) {
@@ -445,15 +466,17 @@ hipError_t quantize(const Fp8QuantArgs& a, hipStream_t s) {
 template <class T, bool WHOLE>
 hipError_t swiglu(const Fp8SwigluArgs& a, hipStream_t s) {
   const uint32_t nkb = blocks_of(a.cols);
-  const dim3 grid((uint32_t)(((uint64_t)a.rows * nkb * 8 + kThreads - 1) / kThreads));
   const FastDiv d = FastDiv::make(nkb);
-  if (a.gate8.codes)
-    hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE, Kept>), grid, dim3(kThreads), 0, s, (const T*)a.gate, (const T*)a.up,
-                       a.ld_gate, a.ld_up, a.rows, a.cols, a.h, d, Kept{a.gate8, a.up8});
-  else
-    hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE, NotKept>), grid, dim3(kThreads), 0, s, (const T*)a.gate,
-                       (const T*)a.up, a.ld_gate, a.ld_up, a.rows, a.cols, a.h, d, NotKept{});
-  return hipGetLastError();
+  return by_rows(a.rows, nkb, [&](int r, int rows, dim3 grid) {
+    const T* const gate = (const T*)a.gate + (int64_t)r * a.ld_gate;
+    const T* const up = (const T*)a.up + (int64_t)r * a.ld_up;
+    if (a.gate8.codes)
+      hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE, Kept>), grid, dim3(kThreads), 0, s, gate, up, a.ld_gate, a.ld_up,
+                         rows, a.cols, from_row(a.h, r), d, Kept{from_row(a.gate8, r), from_row(a.up8, r)});
+    else
+      hipLaunchKernelGGL((fp8_swiglu_kernel<T, WHOLE, NotKept>), grid, dim3(kThreads), 0, s, gate, up, a.ld_gate, a.ld_up,
+                         rows, a.cols, from_row(a.h, r), d, NotKept{});
+  });
 }
 
 template <class T, bool WHOLE>
@@ -470,7 +493,7 @@ hipError_t swiglu_bwd(const Fp8SwigluBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// The host has checked that rows * blocks and the tiles fit 31 bits.
+// The host has checked that rows * blocks fit 31 bits and the tiles one launch.
 hipError_t launch_fp8_quantize(const Fp8QuantArgs& a, hipStream_t s) {
   return (a.x_type == T_FP8 || a.vec) && a.cols % 16 == 0 ? quantize<true>(a, s) : quantize<false>(a, s);
 }

@@ -297,9 +297,11 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  * pitch >= their columns and need only the alignment of their type; rows that
  * start at multiples of 16 bytes are a little faster.
  * Limits (IRIS_ERR_UNSUPPORTED beyond): row pitches of codes, scales and plain
- * matrices up to 2^22, rows and columns up to 2^30 with fewer than 2^31 blocks of
- * 128 along either direction, K of a product up to 2^21 and up to 2^30 output
- * blocks of 128 x 128. Matrices may exceed 4 GiB.
+ * matrices up to 2^22, and so columns (N of a product, rows of a matrix that is
+ * turned around); rows up to 2^30, fewer than 2^31 blocks of 128 along the rows;
+ * where a result is turned around or has 128 x 128 blocks, fewer than 2^23 tiles of
+ * 128 x 128. A product: K up to 2^21, fewer than 2^24 output tiles of 256 x 256.
+ * Matrices may exceed 4 GiB.
  * Every result is the same from call to call. A product's last bits may differ
  * with its shape, which chooses the order of its sums; up to 64 rows of A a
  * column's result does not depend on N.

@@ -157,6 +157,18 @@ def test_library_quantize_refuses():
     assert quant(m8(), rows=0) == "IRIS_OK" and quant(m8(), cols=0) == "IRIS_OK"
 
 
+def test_library_refuses_more_tiles_than_a_launch_holds():
+    """2^23 tiles of 128 x 128, 512 threads each, are 2^32 threads."""
+    wide = dict(ldx=1 << 22, rows=(1 << 15) + 1, cols=1 << 22)
+    assert quant(m8(ld=1 << 22, lds=1 << 15, block=128), **wide) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(None, m8(ld=1 << 16, lds=1 << 9), **wide) == "IRIS_ERR_UNSUPPORTED"
+    assert quant(m8(block=128, ld=128), ldx=128, rows=1 << 30, cols=128) == "IRIS_ERR_UNSUPPORTED"
+    big = ctypes.pointer(_Fp8(P, P, 1 << 22, 1 << 15, 1))
+    assert st(_lib.iris_fp8_swiglu_bwd(big, big, None, None, None, P, 1, 1 << 22, big, big, (1 << 15) + 1, 1 << 22,
+                                       None)) == "IRIS_ERR_UNSUPPORTED"
+    assert mm(M=1 << 30, N=1 << 14, ldc=1 << 14) == "IRIS_ERR_UNSUPPORTED"
+
+
 def mm(C=P, kind=1, ldc=512, A=None, B=None, bias=None, M=512, N=512, K=1000, flags=0, ws=None, wsb=0):
     return st(_lib.iris_fp8_mm(C, kind, ldc, A or m8(), B or m8(block=128), bias, M, N, K, flags, ws, wsb, None))
 

@@ -694,3 +694,42 @@ def test_split_products_of_threads_that_share_a_stream():
         torch.cuda.synchronize()
         for t in range(4):
             assert all(torch.equal(C, wants[t]) for C in outs[t]), t
+
+
+@pytest.mark.gpu
+def test_more_blocks_than_a_launch_holds():
+    """2^29 blocks and more, at 8 threads a block, are more threads than one launch can have."""
+    rows = (1 << 29) + 1000
+    x = (torch.arange(rows, device="cuda", dtype=torch.int32) % 2039).to(torch.float16).reshape(rows, 1)
+    q = il.Fp8(torch.zeros((rows, 16), dtype=torch.uint8, device="cuda")[:, :1],
+               torch.zeros((rows, 1), dtype=torch.uint8, device="cuda"))
+
+    def same_as_alone(call):
+        for start in (0, (1 << 28) - 500, (1 << 29) - 500, rows - 1000):
+            p = il.iris_fp8_empty(1000, 1)
+            call(p, x[start:start + 1000])
+            for big, small in ((q.codes, p.codes), (q.scales, p.scales.view(torch.uint8))):
+                assert torch.equal(big[start:start + 1000], small.view(torch.uint8))
+    note("quantize 2^29 blocks")
+    il.iris_fp8_quantize(x, q)
+    same_as_alone(lambda p, v: il.iris_fp8_quantize(v, p))
+    note("swiglu 2^29 blocks")
+    il.iris_fp8_swiglu(q, x, x)
+    same_as_alone(lambda p, v: il.iris_fp8_swiglu(p, v, v))
+
+
+@pytest.mark.gpu
+def test_mm_of_more_small_tiles_than_a_launch_holds():
+    """2^30 rows of A and one of B: 2^24 tiles of 64 x 64."""
+    M, K = 1 << 30, 16
+    note("mm 2^30 rows")
+    codes = torch.full((M, K), 0x38, dtype=torch.uint8, device="cuda")            # ones
+    codes[:, 3] = torch.arange(M, device="cuda", dtype=torch.int32).remainder_(7).to(torch.uint8).mul_(8)   # 0, 2^-6 .. 2^-1
+    scales = torch.full((M, 4), 127, dtype=torch.uint8, device="cuda")
+    B = put(np.full((1, K), 0x38, np.uint8), np.full((1, 1), 127, np.uint8))
+    C = torch.zeros((M, 1), dtype=torch.float16, device="cuda")
+    il.iris_fp8_mm(C, il.Fp8(codes, scales[:, :1]), B)
+    want = 15.0 + torch.tensor([0.0] + [2.0 ** -i for i in range(6, 0, -1)], dtype=torch.float16, device="cuda")
+    for start in range(0, M, 1 << 28):
+        at = torch.arange(start, start + (1 << 28), device="cuda", dtype=torch.int32).remainder_(7)
+        assert torch.equal(C[start:start + (1 << 28), 0], want[at])
