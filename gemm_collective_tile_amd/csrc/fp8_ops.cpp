@@ -103,6 +103,28 @@ int check_plain(const void* x, int32_t type, bool fp32_too, int64_t ld, int64_t 
   return IRIS_OK;
 }
 
+// What a call reads and writes, by address. An output that is also another operand
+// would be read before or after it is written as the kernel for its size happens to.
+struct Memory {
+  const void* at[2];   // codes and scales, or a plain matrix
+  const char* name;
+  bool output;
+  Memory(const iris_fp8_t* q, const char* name, bool output)
+      : at{q ? q->codes : nullptr, q ? q->scales : nullptr}, name(name), output(output) {}
+  Memory(const void* x, const char* name, bool output) : at{x, nullptr}, name(name), output(output) {}
+};
+template <size_t N>
+int check_distinct(const Memory (&m)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = 0; j < i; ++j) {
+      if (!m[i].output && !m[j].output) continue;
+      for (const void* p : m[i].at)
+        if (p && (p == m[j].at[0] || p == m[j].at[1]))
+          return fail(IRIS_ERR_INVALID_ARG, "%s and %s share memory", m[j].name, m[i].name);
+    }
+  return IRIS_OK;
+}
+
 // every row of a plain matrix starts at a multiple of 16 bytes
 bool rows16(const void* x, int64_t ld, int32_t type) {
   return (uintptr_t)x % 16 == 0 && ld * type_bytes(type) % 16 == 0;
@@ -237,6 +259,7 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
     a.vec = rows16(x, ldx, x_type);
   }
   if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = check_distinct({{q, "q", true}, {q_t, "q_t", true}, {x, "x", false}, {x8, "x8", false}}))) return st;
   if ((st = ready())) return st;
   a.q = mat(q);
   a.qt = mat(q_t);
@@ -271,6 +294,9 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   if (workspace && workspace_bytes < plan.ws_bytes)
     return fail(IRIS_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, plan.ws_bytes);
   if (workspace && (uintptr_t)workspace % 256 != 0) return fail(IRIS_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  if ((st = check_distinct({{C, "C", true}, {A, "A", false}, {B, "B", false}, {bias, "bias", false},
+                            {workspace, "workspace", true}})))
+    return st;
   int dev = 0, cus = 0;
   if ((st = iris::use_device(&dev, &cus))) return st;
   std::unique_lock<std::mutex> hold;   // over both launches of a split product
@@ -307,6 +333,9 @@ int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris
       (st = check_plain(up, type, false, ld_up, rows, cols, "up")))
     return st;
   if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = check_distinct({{h, "h", true}, {gate_kept, "gate_kept", true}, {up_kept, "up_kept", true},
+                            {gate, "gate", false}, {up, "up", false}})))
+    return st;
   if ((st = ready())) return st;
   iris::Fp8SwigluArgs a{};
   a.gate = gate;
@@ -345,6 +374,10 @@ int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const ir
       return st;
   if ((st = check_plain(dh, type, false, ld_dh, rows, cols, "dh"))) return st;
   if (rows == 0 || cols == 0) return IRIS_OK;
+  if ((st = check_distinct({{dgate, "dgate", true}, {dup, "dup", true}, {dgate_t, "dgate_t", true}, {dup_t, "dup_t", true},
+                            {h_t, "h_t", true}, {gate_kept, "gate_kept", false}, {up_kept, "up_kept", false},
+                            {dh, "dh", false}})))
+    return st;
   if ((st = ready())) return st;
   iris::Fp8SwigluBwdArgs a{};
   a.dh = dh;

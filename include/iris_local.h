@@ -293,7 +293,8 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  *              of iris_fp8_mm: 4-byte aligned, ld_scales a multiple of 4 (the
  *              bytes up to it allocated; ignored).
  * The structs are read before the call returns; the buffers belong to the
- * caller. Unlike above, plain matrices (x, C, gate, up, dh) may have any row
+ * caller. No output may overlap another operand (equal addresses are refused with
+ * IRIS_ERR_INVALID_ARG): no operator works in place. Unlike above, plain matrices (x, C, gate, up, dh) may have any row
  * pitch >= their columns and need only the alignment of their type; rows that
  * start at multiples of 16 bytes are a little faster.
  * Limits (IRIS_ERR_UNSUPPORTED beyond): row pitches of codes, scales and plain
@@ -341,7 +342,7 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
  * C: (M, N) of c_type, row pitch ldc elements. bias: NULL, or N values of
  * c_type (M with IRIS_FLAG_BIAS_ALONG_M). Sums run in 32 bits; each output is
  * rounded once, after the bias and, with IRIS_FLAG_ACCUMULATE, C's old value.
- * K = 0 gives the bias (and old value) alone. C must not overlap an input.
+ * K = 0 gives the bias (and old value) alone.
  * The product of a layer is A = activations, B = weights (out, in); the
  * input's gradient A = output gradients, B = transposed weights; the weight's
  * gradient A = transposed output gradients, B = transposed activations.

@@ -225,3 +225,33 @@ def test_library_activation_refuses():
     assert bwd(ht=m8(block=128, ld=512)) == "IRIS_ERR_UNSUPPORTED"
     assert bwd(gk=m8(codes=ODD)) == "IRIS_ERR_ALIGNMENT"
     assert bwd(cols=0) == "IRIS_OK"
+
+
+def test_library_refuses_outputs_that_are_another_operand():
+    """Whether an operator in place would read before it writes depends on its kernel, so none is allowed."""
+    at = lambda n, ld=1024, lds=8: m8(0x1000000 * n, 0x1000000 * n + 0x800000, ld, lds)  # noqa: E731
+    x, stop = 0x1000000 * 30, 7                      # operand number 7 takes the place of another below
+    share = at(stop)
+
+    def fwd(h=at(1), gk=at(2), uk=at(3), gate=x, up=x + (1 << 20)):
+        return st(_lib.iris_fp8_swiglu(h, gk, uk, gate, up, 1, 1024, 1024, 512, 1000, None))
+    assert fwd(gk=share, uk=share) == fwd(h=share, gk=share) == fwd(h=m8(x, P)) == "IRIS_ERR_INVALID_ARG"
+    assert fwd(uk=m8(0x1000000 * 9, 0x1000000 * 2 + 0x800000)) == "IRIS_ERR_INVALID_ARG"      # scales alone
+
+    names = ["dg", "du", "dgt", "dut", "ht", "gk", "uk"]
+
+    def bwd(dh=x, **other):
+        m = {n: at(i + 10, 512 if n.endswith("t") else 1024) for i, n in enumerate(names)}
+        m.update(other)
+        return st(_lib.iris_fp8_swiglu_bwd(m["dg"], m["du"], m["dgt"], m["dut"], m["ht"], dh, 1, 1024, m["gk"], m["uk"],
+                                           512, 1000, None))
+    for a in names[:5]:
+        for b in names:
+            if a != b:
+                same = {n: at(stop, 512 if n.endswith("t") else 1024) for n in (a, b)}
+                assert bwd(**same) == "IRIS_ERR_INVALID_ARG", (a, b)
+    assert bwd(dg=m8(x, P)) == "IRIS_ERR_INVALID_ARG"
+    assert quant(at(1), at(1, 512)) == quant(m8(x, P), x=x) == "IRIS_ERR_INVALID_ARG"
+    assert quant(None, at(1, 512), x=None, x8=at(1)) == "IRIS_ERR_INVALID_ARG"
+    assert mm(C=x, A=m8(x, P)) == mm(C=x, B=m8(x, P)) == mm(C=x, bias=x) == "IRIS_ERR_INVALID_ARG"
+    assert mm(C=x, ws=x, wsb=1 << 25) == "IRIS_ERR_INVALID_ARG"
