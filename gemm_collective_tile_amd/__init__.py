@@ -428,7 +428,7 @@ class Fp8:
     The object is a handle: it reads the tensors' addresses once and holds the
     tensors, so their memory must not be exchanged (set_, resize_) under it.
     """
-    __slots__ = ("codes", "scales", "block", "shape", "_c", "_p", "_on_gpu", "_scale_words")
+    __slots__ = ("codes", "scales", "block", "shape", "_c", "_p", "_device", "_scale_words")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, block: int = 1):
         rows, cols = _shape2(codes, "codes")
@@ -455,7 +455,7 @@ class Fp8:
         end = scales.storage_offset() + (scales.shape[0] - 1) * lds + -(-scales.shape[1] // 4) * 4
         self._scale_words = scales.numel() == 0 or end <= scales.untyped_storage().nbytes()
         self.codes, self.scales, self.block, self.shape = codes, scales, block, (rows, cols)
-        self._on_gpu = codes.is_cuda
+        self._device = codes.get_device()   # -1: not on a GPU
         self._c = _Fp8(codes.data_ptr(), scales.data_ptr(), ld, lds, block)
         self._p = ctypes.pointer(self._c)
 
@@ -483,20 +483,27 @@ def iris_fp8_empty(rows: int, cols: int, block: int = 1, device=None) -> Fp8:
 
 
 # These run once per call in front of a 2 us launch, so they do little more than
-# the comparisons themselves.
+# the comparisons themselves. `dev` is the device that all operands have to be on:
+# the current one, where the kernels run.
 
-def _fp8(q, shape, name: str):
-    """q's C struct, after the check of its kind, shape and (last) device."""
+def _elsewhere(name: str, device: int, dev: int):
+    if device < 0 or dev < 0:
+        return ValueError(f"{name if device < 0 else 'every operand'} must be on a GPU")
+    return ValueError(f"{name} is on GPU {device}, not on GPU {dev}")
+
+
+def _fp8(q, shape, name: str, dev: int):
+    """q's C struct, after the check of its kind, shape and device."""
     if q.__class__ is not Fp8:
         raise TypeError(f"{name} must be an Fp8 matrix") if q is not None else ValueError(f"{name} is required")
     if q.shape != shape:
         raise ValueError(f"{name} has shape {q.shape}, expected {shape}")
-    if not q._on_gpu:
-        raise ValueError(f"{name} must be on a GPU")
+    if q._device != dev or dev < 0:
+        raise _elsewhere(name, q._device, dev)
     return q._p
 
 
-def _plain(t, name: str, kinds, rows: int, cols: int):
+def _plain(t, name: str, kinds, rows: int, cols: int, dev: int):
     """(pointer, type, row pitch) of a row-major matrix with any row pitch."""
     kind = kinds.get(t.dtype)
     if kind is None:
@@ -504,19 +511,33 @@ def _plain(t, name: str, kinds, rows: int, cols: int):
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU")
+    device = t.get_device()
+    if device != dev or dev < 0:
+        raise _elsewhere(name, device, dev)
     return t.data_ptr(), kind, (ld if rows > 1 else cols)
 
 
-def _fp8_ws(workspace):
+def _fp8_stream(stream, dev: int):
+    """The stream's handle (the current one, a torch stream or a handle), after the check of the current device."""
+    current = _current_device()
+    if current != dev:
+        raise ValueError(f"the operands are on GPU {dev}, the current device is {current}")
+    if stream is None:
+        return _current_stream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise _elsewhere("stream", stream.device_index, dev)
+    return _stream(stream)
+
+
+def _fp8_ws(workspace, dev: int):
     """(pointer, bytes) of a caller's workspace, which the kernels write from its first byte on."""
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch tensor")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    if not workspace.is_cuda:
-        raise ValueError("workspace must be on a GPU")
+    device = workspace.get_device()
+    if device != dev or dev < 0:
+        raise _elsewhere("workspace", device, dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -531,15 +552,16 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
     if not from8 and (not isinstance(x, torch.Tensor) or x.dim() != 2):
         _shape2(x, "x")
     shape = rows, cols = x.shape
-    qp = None if q is None else _fp8(q, (rows, cols), "q")
-    qtp = None if q_t is None else _fp8(q_t, (cols, rows), "q_t")
+    dev = x._device if from8 else x.get_device()
+    qp = None if q is None else _fp8(q, (rows, cols), "q", dev)
+    qtp = None if q_t is None else _fp8(q_t, (cols, rows), "q_t", dev)
     if from8:
-        ptr, kind, ld, x8 = None, 0, 0, _fp8(x, shape, "x")
+        ptr, kind, ld, x8 = None, 0, 0, _fp8(x, shape, "x", dev)
     else:
-        ptr, kind, ld = _plain(x, "x", _FP8_TYPES, rows, cols)
+        ptr, kind, ld = _plain(x, "x", _FP8_TYPES, rows, cols, dev)
         x8 = None
     st = _lib.iris_fp8_quantize(qp, qtp, ptr, kind, ld, x8, rows, cols,
-                                _current_stream(_current_device()) if stream is None else _stream(stream))
+                                _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -558,7 +580,8 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
                          "next multiple of 4 bytes; see iris_fp8_empty")
     if not isinstance(C, torch.Tensor) or C.shape != (M, N):
         _want_shape(C, (M, N), "C")
-    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace)
+    dev = A._device
+    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
     flags = IRIS_FLAG_ACCUMULATE if accumulate else 0
     bias_ptr = None
     if bias is not None:
@@ -569,13 +592,14 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
             raise ValueError("bias must be contiguous")
         if _bias_along_m(config):
             flags |= IRIS_FLAG_BIAS_ALONG_M
-    ptr, kind, ld = _plain(C, "C", _FP8_TYPES, M, N)
+    ptr, kind, ld = _plain(C, "C", _FP8_TYPES, M, N, dev)
     if bias is not None:
-        if not bias.is_cuda:
-            raise ValueError("bias must be on a GPU")
+        if bias.get_device() != dev:
+            raise _elsewhere("bias", bias.get_device(), dev)
         bias_ptr = bias.data_ptr()
-    st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8(A, A.shape, "A"), _fp8(B, B.shape, "B"), bias_ptr, M, N, K, flags, ws,
-                          wsb, _current_stream(_current_device()) if stream is None else _stream(stream))
+    st = _lib.iris_fp8_mm(ptr, kind, ld, _fp8(A, A.shape, "A", dev), _fp8(B, B.shape, "B", dev), bias_ptr, M, N, K, flags,
+                          ws, wsb,
+                          _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -591,14 +615,15 @@ def iris_fp8_swiglu(h: Fp8, gate, up, gate_kept: Optional[Fp8] = None, up_kept: 
         _want_shape(up, shape, "up")
     if up.dtype != gate.dtype:
         raise TypeError("gate and up must have one dtype")
-    hp = _fp8(h, shape, "h")
+    dev = gate.get_device()
+    hp = _fp8(h, shape, "h", dev)
     kept = gate_kept is not None or up_kept is not None
-    gkp = _fp8(gate_kept, shape, "gate_kept") if kept else None
-    ukp = _fp8(up_kept, shape, "up_kept") if kept else None
-    gp, kind, gld = _plain(gate, "gate", _FP8_HALVES, rows, cols)
-    up_ptr, _, uld = _plain(up, "up", _FP8_HALVES, rows, cols)
+    gkp = _fp8(gate_kept, shape, "gate_kept", dev) if kept else None
+    ukp = _fp8(up_kept, shape, "up_kept", dev) if kept else None
+    gp, kind, gld = _plain(gate, "gate", _FP8_HALVES, rows, cols, dev)
+    up_ptr, _, uld = _plain(up, "up", _FP8_HALVES, rows, cols, dev)
     st = _lib.iris_fp8_swiglu(hp, gkp, ukp, gp, up_ptr, kind, gld, uld, rows, cols,
-                              _current_stream(_current_device()) if stream is None else _stream(stream))
+                              _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -612,12 +637,15 @@ def iris_fp8_swiglu_bwd(dgate: Fp8, dup: Fp8, dh, gate_kept: Fp8, up_kept: Fp8, 
         _shape2(dh, "dh")
     shape = rows, cols = dh.shape
     turned = (cols, rows)
+    dev = dh.get_device()
     st = _lib.iris_fp8_swiglu_bwd(
-        _fp8(dgate, shape, "dgate"), _fp8(dup, shape, "dup"),
-        None if dgate_t is None else _fp8(dgate_t, turned, "dgate_t"),
-        None if dup_t is None else _fp8(dup_t, turned, "dup_t"), None if h_t is None else _fp8(h_t, turned, "h_t"),
-        *_plain(dh, "dh", _FP8_HALVES, rows, cols), _fp8(gate_kept, shape, "gate_kept"),
-        _fp8(up_kept, shape, "up_kept"), rows, cols, _stream(stream))
+        _fp8(dgate, shape, "dgate", dev), _fp8(dup, shape, "dup", dev),
+        None if dgate_t is None else _fp8(dgate_t, turned, "dgate_t", dev),
+        None if dup_t is None else _fp8(dup_t, turned, "dup_t", dev),
+        None if h_t is None else _fp8(h_t, turned, "h_t", dev),
+        *_plain(dh, "dh", _FP8_HALVES, rows, cols, dev), _fp8(gate_kept, shape, "gate_kept", dev),
+        _fp8(up_kept, shape, "up_kept", dev), rows, cols,
+        _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 

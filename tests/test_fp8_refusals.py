@@ -119,6 +119,45 @@ def test_swiglu_refuses():
     expect(ValueError, "is required", b, None, h, g, h, h)
 
 
+class OnGpu1:
+    """A matrix on the second GPU, as far as the binding looks before it takes its address."""
+    def __init__(self, t):
+        self.dtype, self.stride = t.dtype, t.stride
+
+    def get_device(self):
+        return 1
+
+    def data_ptr(self):
+        raise AssertionError("its address was taken")
+
+
+def test_operands_on_another_device_are_refused(monkeypatch):
+    """The kernels run on the current device, on its stream: operands of another one would be reached over the
+    link, or not at all, and ordered by no stream."""
+    here, there = empty(6, 200), empty(6, 200)
+    here._device, there._device = 0, 1
+    assert il._fp8(here, (6, 200), "q", 0) is here._p
+    expect(ValueError, "q is on GPU 1, not on GPU 0", il._fp8, there, (6, 200), "q", 0)
+    expect(ValueError, "q must be on a GPU", il._fp8, empty(6, 200), (6, 200), "q", 0)
+    expect(ValueError, "q must be on a GPU", il._fp8, empty(6, 200), (6, 200), "q", -1)
+    expect(ValueError, "every operand must be on a GPU", il._fp8, here, (6, 200), "q", -1)
+    x = torch.zeros((6, 200), dtype=torch.float16)
+    expect(ValueError, "x is on GPU 1, not on GPU 0", il._plain, OnGpu1(x), "x", il._FP8_TYPES, 6, 200, 0)
+    expect(ValueError, "x must be on a GPU", il._plain, x, "x", il._FP8_TYPES, 6, 200, 0)
+    expect(ValueError, "q_t is on GPU 1, not on GPU 0", il.iris_fp8_quantize, here, None, turned(1))
+    monkeypatch.setattr(il, "_current_device", lambda: 1)
+    expect(ValueError, "operands are on GPU 0, the current device is 1", il.iris_fp8_quantize, here, None, turned(0))
+    monkeypatch.setattr(il, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "Stream", type("Stream", (), {"device_index": 1, "cuda_stream": 0}))
+    expect(ValueError, "stream is on GPU 1, not on GPU 0", il._fp8_stream, torch.cuda.Stream(), 0)
+
+
+def turned(device):
+    q = empty(200, 6)
+    q._device = device
+    return q
+
+
 # ------------------------------------------------------------------- library
 
 def st(status):
