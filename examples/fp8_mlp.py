@@ -24,11 +24,13 @@ class Weight8:
     """A weight (out, in) in 8 bits: `fwd` for x W^T, `bwd` (in, out) for dy W."""
 
     def __init__(self, out_features, in_features):
+        self.version = 0
         self.fwd = il.iris_fp8_empty(out_features, in_features, block=128)
         self.bwd = il.iris_fp8_empty(in_features, out_features, block=128)
 
     def set(self, w):
         il.iris_fp8_quantize(w, self.fwd, self.bwd)
+        self.version += 1
 
 
 class FeedForward(torch.autograd.Function):
@@ -51,11 +53,14 @@ class FeedForward(torch.autograd.Function):
         y = torch.empty((n, wd.shape[0]), dtype=x.dtype, device=x.device)
         il.iris_fp8_mm(y, h8, d8.fwd)
         ctx.kept, ctx.weights = (x8, gate8, up8), (g8, u8, d8)
+        ctx.versions = [w.version for w in ctx.weights]
         return y
 
     @staticmethod
     def backward(ctx, dy):
         (x8, gate8, up8), (g8, u8, d8) = ctx.kept, ctx.weights
+        if [w.version for w in ctx.weights] != ctx.versions:
+            raise RuntimeError("the 8-bit weights have been set anew since the forward pass")
         n, width = x8.shape
         hidden = gate8.shape[1]
         dy = dy.contiguous()

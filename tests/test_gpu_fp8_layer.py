@@ -72,3 +72,21 @@ def test_training_goes_as_in_32_bits_and_a_token_decodes(monkeypatch):
     _, want = ex.train(256, 256, 344, 15)
     assert want[0] > want[-1]
     assert losses[0] - losses[-1] >= 0.9 * (want[0] - want[-1]), (losses, want)
+
+
+@pytest.mark.gpu
+def test_backward_refuses_weights_set_anew():
+    """The backward pass reads the 8-bit weights of the forward pass: other ones would change the gradient unseen."""
+    ex = example()
+    note("8-bit layer: weights set anew")
+    layer = ex.Layer(256, 344)
+    x = torch.randn(20, 256, device="cuda").to(torch.bfloat16).requires_grad_()
+    y = layer(x)
+    with torch.no_grad():
+        layer.wg.mul_(2.0)
+    layer.refresh()
+    with pytest.raises(RuntimeError, match="set anew"):
+        y.backward(torch.ones_like(y))
+    y = layer(x)
+    y.backward(torch.ones_like(y))
+    assert x.grad is not None
