@@ -61,27 +61,36 @@ class FeedForward(torch.autograd.Function):
         (x8, gate8, up8), (g8, u8, d8) = ctx.kept, ctx.weights
         if [w.version for w in ctx.weights] != ctx.versions:
             raise RuntimeError("the 8-bit weights have been set anew since the forward pass")
+        for_x, for_wg, for_wu, for_wd = ctx.needs_input_grad[:4]
         n, width = x8.shape
         hidden = gate8.shape[1]
         dy = dy.contiguous()
-        dy8, dy8_t = il.iris_fp8_empty(n, width), il.iris_fp8_empty(width, n)
+        dy8, dy8_t = il.iris_fp8_empty(n, width), il.iris_fp8_empty(width, n) if for_wd else None
         il.iris_fp8_quantize(dy, dy8, dy8_t)
         dh = torch.empty((n, hidden), dtype=dy.dtype, device=dy.device)
         il.iris_fp8_mm(dh, dy8, d8.bwd)
         dg, du = il.iris_fp8_empty(n, hidden), il.iris_fp8_empty(n, hidden)
-        dg_t, du_t, h_t = (il.iris_fp8_empty(hidden, n) for _ in range(3))
+        dg_t, du_t, h_t = (il.iris_fp8_empty(hidden, n) if wanted else None for wanted in (for_wg, for_wu, for_wd))
         il.iris_fp8_swiglu_bwd(dg, du, dh, gate8, up8, dg_t, du_t, h_t)
-        dx = torch.empty((n, width), dtype=torch.float32, device=dy.device)
-        il.iris_fp8_mm(dx, dg, g8.bwd)
-        il.iris_fp8_mm(dx, du, u8.bwd, accumulate=True)
-        x8_t = il.iris_fp8_empty(width, n)
-        il.iris_fp8_quantize(x8, None, x8_t)
-        dwg, dwu = (torch.empty((hidden, width), dtype=torch.float32, device=dy.device) for _ in range(2))
-        dwd = torch.empty((width, hidden), dtype=torch.float32, device=dy.device)
-        il.iris_fp8_mm(dwg, dg_t, x8_t)
-        il.iris_fp8_mm(dwu, du_t, x8_t)
-        il.iris_fp8_mm(dwd, dy8_t, h_t)
-        return dx.to(dy.dtype), dwg, dwu, dwd, None, None, None
+        dx = dwg = dwu = dwd = None
+        if for_x:
+            dx = torch.empty((n, width), dtype=torch.float32, device=dy.device)
+            il.iris_fp8_mm(dx, dg, g8.bwd)
+            il.iris_fp8_mm(dx, du, u8.bwd, accumulate=True)
+            dx = dx.to(dy.dtype)
+        if for_wg or for_wu:
+            x8_t = il.iris_fp8_empty(width, n)
+            il.iris_fp8_quantize(x8, None, x8_t)
+        if for_wg:
+            dwg = torch.empty((hidden, width), dtype=torch.float32, device=dy.device)
+            il.iris_fp8_mm(dwg, dg_t, x8_t)
+        if for_wu:
+            dwu = torch.empty((hidden, width), dtype=torch.float32, device=dy.device)
+            il.iris_fp8_mm(dwu, du_t, x8_t)
+        if for_wd:
+            dwd = torch.empty((width, hidden), dtype=torch.float32, device=dy.device)
+            il.iris_fp8_mm(dwd, dy8_t, h_t)
+        return dx, dwg, dwu, dwd, None, None, None
 
 
 class Layer(torch.nn.Module):

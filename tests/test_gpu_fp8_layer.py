@@ -90,3 +90,41 @@ def test_backward_refuses_weights_set_anew():
     y = layer(x)
     y.backward(torch.ones_like(y))
     assert x.grad is not None
+
+
+@pytest.mark.gpu
+def test_gradients_that_are_not_wanted_are_not_formed():
+    ex = example()
+    note("8-bit layer: some gradients")
+    layer = ex.Layer(256, 344)
+    x = torch.randn(20, 256, device="cuda").to(torch.bfloat16)
+    calls = []
+    mm = ex.il.iris_fp8_mm
+
+    def counted(*a, **kw):
+        calls.append(a[0].dtype)
+        return mm(*a, **kw)
+
+    def gradients(names, for_x):
+        for n in ("wg", "wu", "wd"):
+            w = getattr(layer, n)
+            w.requires_grad_(n in names)
+            w.grad = None
+        xi = x.clone().requires_grad_(for_x)
+        y = layer(xi)
+        calls.clear()
+        ex.il.iris_fp8_mm = counted
+        try:
+            y.backward(torch.ones_like(y))
+        finally:
+            ex.il.iris_fp8_mm = mm
+        return [xi.grad] + [getattr(layer, n).grad for n in ("wg", "wu", "wd")], len(calls)
+
+    whole, n = gradients(("wg", "wu", "wd"), True)
+    assert n == 6 and all(g is not None for g in whole)
+    for names, for_x, products in ((("wg",), False, 2), (("wu",), True, 4), (("wd",), False, 2), ((), True, 3),
+                                   (("wg", "wd"), False, 3)):
+        got, n = gradients(names, for_x)
+        assert n == products, (names, for_x, n)
+        for g, want, wanted in zip(got, whole, [for_x] + [w in names for w in ("wg", "wu", "wd")]):
+            assert torch.equal(g, want) if wanted else g is None
