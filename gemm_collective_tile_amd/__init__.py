@@ -568,7 +568,9 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
 
 def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, workspace=None, stream=None) -> None:
     """C = A @ B^T + bias (+ C with accumulate): A (M, K) Fp8 with blocks of
-    1 x 128, B (N, K) Fp8, C (M, N) float16, bfloat16 or float32, bias of C's type."""
+    1 x 128, B (N, K) Fp8, C (M, N) float16, bfloat16 or float32, bias of C's type.
+    A float32 C has exact products and 32-bit sums; a 16-bit one drops, of every 8
+    products, what lies under 2^-13 of the largest."""
     if A.__class__ is not Fp8 or B.__class__ is not Fp8:
         raise TypeError("A and B must be Fp8 matrices")
     M, K = A.shape

@@ -10,7 +10,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 8 codes times a scale, exactly (the scale's bits: byte << 23)
+// 8 codes times a scale (its bits: byte << 23). Exact under bytes 3 to 246: the last
+// bit of a code is 2^-9, bf16's last subnormal bit 2^-133 (which the matrix
+// instructions take), and 448 * 2^119 is below 2^128.
 __device__ __forceinline__ bf16x8 to_bf16x8(uint32_t lo, uint32_t hi, float scale) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);

@@ -340,8 +340,19 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
 /*
  * C = A @ B^T + bias,  A (M, K) with block 1, B (N, K) with block 1 or 128.
  * C: (M, N) of c_type, row pitch ldc elements. bias: NULL, or N values of
- * c_type (M with IRIS_FLAG_BIAS_ALONG_M). Sums run in 32 bits; each output is
- * rounded once, after the bias and, with IRIS_FLAG_ACCUMULATE, C's old value.
+ * c_type (M with IRIS_FLAG_BIAS_ALONG_M). Each output is rounded once, after the
+ * bias and, with IRIS_FLAG_ACCUMULATE, C's old value.
+ * Precision, by C's type:
+ *   fp32        every product is exact and sums run in 32 bits. Entries of A and B
+ *               are taken as bf16 values, which hold them exactly under scale bytes
+ *               3 to 246: below, parts under 2^-133 are lost, above, entries of
+ *               2^128 and more are infinite.
+ *   fp16, bf16  every scale byte from 1 to 254. The 8-bit matrix instructions line
+ *               up the products of 8 neighbouring k with the largest of them and
+ *               drop what lies under 2^-13 of it (8 * 2^-13 of the sum of all |a b|
+ *               at most; 1.4e-5 of the result, measured on normally distributed
+ *               operands); the sums of such eights run in 32 bits. Who needs full
+ *               32-bit sums asks for an fp32 C.
  * K = 0 gives the bias (and old value) alone.
  * The product of a layer is A = activations, B = weights (out, in); the
  * input's gradient A = output gradients, B = transposed weights; the weight's

@@ -429,6 +429,28 @@ def test_mm_block_scales_act_per_block(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M", [5, 40, 90, 200])
+def test_mm_scale_bytes_of_the_whole_range(M):
+    """Scale bytes of one operand from the smallest to the largest against the other's opposite: every one from 1 to
+    254 into 16 bits, 3 to 246 (entries that bf16 holds) into 32."""
+    N, K = 70, 300
+    rng = np.random.default_rng(M)
+    a, b = (rng.integers(0, 256, (n, K)).astype(np.uint8) for n in (M, N))
+    for codes in (a, b):
+        codes[(codes & 0x7f) == 0x7f] = 1
+        codes[1], codes[2], codes[3] = 1, rng.integers(1, 8, K), 0x7e    # the smallest, subnormal ones, the largest
+    for dtype, lo, hi in (("bf16", 1, 254), ("fp32", 3, 246)):
+        for s in sorted({lo, lo + 1, 3, 9, 10, 60, 127, 200, 246, hi}):
+            t = max(lo, min(hi, 254 - s))
+            note(f"mm scale bytes M {M} {dtype} {s} {t}")
+            for sa, sb in ((s, t), (t, s)):
+                A, B = put(a, np.full((M, 3), sa, np.uint8)), put(b, np.full((N, 3), sb, np.uint8))
+                C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+                il.iris_fp8_mm(C, A, B)
+                check_product(C, ref.values(*parts(A)), ref.values(*parts(B)), None, None, dtype, (M, dtype, sa, sb))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N", [(1, 200), (40, 200), (300, 200)])
 def test_mm_nan_stays_in_its_row_and_column(M, N):
     K = 520
