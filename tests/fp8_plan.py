@@ -17,3 +17,14 @@ def plan(M, N, K, dtype="fp16"):
     """(tile rows, tile columns, splits of the contraction); (0, 0, 1): the kernel for few rows."""
     p = _plan(M, N, K, dtype == "fp32")
     return (p.bm, p.bn, p.splits) if p.bm else (0, 0, 1)
+
+
+# a product for each way to run one beyond the few rows, ragged in all lengths and more than eight steps of k deep
+OF_EACH_PLAN = [
+    ("fp16", 97, 101, 1100, (64, 64, 1)), ("bf16", 301, 397, 4111, (64, 64, 9)), ("bf16", 1501, 2051, 1101, (128, 64, 1)),
+    ("fp16", 2637, 208, 8305, (128, 64, 6)), ("fp16", 2051, 2053, 1111, (128, 128, 1)),
+    ("bf16", 517, 2053, 8305, (128, 128, 3)), ("fp16", 3005, 4103, 1105, (256, 256, 1)),
+    ("fp32", 301, 391, 1101, (64, 64, 1)), ("fp32", 301, 397, 4111, (64, 64, 9)), ("fp32", 1503, 1505, 1101, (128, 64, 1)),
+    ("fp32", 1803, 515, 3001, (128, 64, 3)), ("fp32", 2051, 2053, 1111, (128, 128, 1)),
+    ("fp32", 517, 2053, 6001, (128, 128, 3)), ("fp32", 3005, 5003, 1105, (256, 256, 1)),
+]

@@ -1,7 +1,7 @@
 """The plan of an 8-bit product, on the host."""
 import pytest
 
-from fp8_plan import plan
+from fp8_plan import OF_EACH_PLAN, plan
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "fp32"])
@@ -16,3 +16,8 @@ def test_every_plan_can_be_launched(dtype):
                 if bm:
                     tiles = -(-M // bm) * -(-N // bn) * splits
                     assert -(-tiles // 256) * 256 * 256 < 1 << 32, (M, N, K, bm, bn)
+
+
+@pytest.mark.parametrize("dtype,M,N,K,want", OF_EACH_PLAN)
+def test_shapes_of_the_gpu_tests_get_the_plans_they_stand_for(dtype, M, N, K, want):
+    assert plan(M, N, K, dtype) == want

@@ -18,6 +18,7 @@ import torch
 
 import fp8_ref as ref
 import gemm_collective_tile_amd as il
+from fp8_plan import OF_EACH_PLAN, plan
 from gpu_util import note
 
 DT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
@@ -302,6 +303,44 @@ def test_mm_of_each_tile(M, N, K, dtype, block):
     C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
     il.iris_fp8_mm(C, A, B)
     check_product(C, a, b, None, None, dtype, (M, N, K, dtype))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,M,N,K,want", OF_EACH_PLAN)
+def test_mm_of_each_plan(dtype, M, N, K, want):
+    """Every tile, whole and with a split contraction: with a bias along N into whole rows, then along M and added to
+    what an unaligned C of odd pitch holds; both twice, with the same bits."""
+    assert plan(M, N, K, dtype) == want
+    note(f"mm plan {M}x{N}x{K} {dtype} {want}")
+    block = 128 if K % 2 else 1
+    A, B = from_gpu(sample(M, K, 1)), il.iris_fp8_empty(N, K, block)
+    il.iris_fp8_quantize(torch.from_numpy(sample(N, K, 2, 0.0) / np.sqrt(K)).to(torch.float32).cuda(), B)
+    a, b = ref.values(*parts(A)), ref.values(*parts(B), block)
+    exact, size = a @ b.T, np.abs(a) @ np.abs(b).T
+
+    def check(C, more, old, what):
+        e, s = exact + more + old, size + np.abs(more) + np.abs(old)
+        bound = (K + 2) * 2.0 ** -23 * s + ULP[dtype] * np.abs(e) + (0.0 if dtype == "fp32" else 2.0 ** -10) * s
+        off = ~(np.abs(C.double().cpu().numpy() - e) <= bound + (2.0 ** -25 if dtype == "fp16" else 0.0))
+        assert not off.any(), (what, int(off.sum()), np.argwhere(off)[0].tolist())
+    along_n, nv = on_gpu(np.random.default_rng(3).normal(size=(1, N)), dtype)
+    C, D = (torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda") for _ in range(2))
+    for out in (C, D):
+        il.iris_fp8_mm(out, A, B, along_n.reshape(-1))
+    check(C, nv, 0.0, "bias along N")
+    assert torch.equal(C, D)
+    along_m, mv = on_gpu(np.random.default_rng(4).normal(size=(M, 1)), dtype)
+    first = None
+    for _ in range(2):
+        old, ov = on_gpu(sample(M, N, 5), dtype, N + 5, 3)
+        il.iris_fp8_mm(old, A, B, along_m.reshape(-1), accumulate=True, config=il.Config(flags=il.IRIS_FLAG_BIAS_ALONG_M))
+        if first is None:
+            first = old
+            check(old, mv, ov, "accumulated, bias along M")
+    assert torch.equal(first, old)
+    outside = torch.empty(0, dtype=DT[dtype], device="cuda").set_(old.untyped_storage()).clone()
+    torch.as_strided(outside, (M, N), (N + 5, 1), 3).fill_(float("nan"))
+    assert bool(outside.isnan().all()), "C's padding was written"
 
 
 @pytest.mark.gpu
@@ -755,3 +794,45 @@ def test_mm_of_more_small_tiles_than_a_launch_holds():
     for start in range(0, M, 1 << 28):
         at = torch.arange(start, start + (1 << 28), device="cuda", dtype=torch.int32).remainder_(7)
         assert torch.equal(C[start:start + (1 << 28), 0], want[at])
+
+
+@pytest.mark.gpu
+def test_split_products_in_graphs_on_streams_and_in_a_callers_workspace():
+    """The library's workspace, its first use within a capture, on a stream of its own and on the current one; a
+    caller's of just the size asked for, holding NaN."""
+    M, N, K = 301, 397, 4111
+    note("split products: workspaces")
+    need = il.iris_fp8_mm_workspace_size(M, N, K)
+    assert need > 0 and plan(M, N, K, "bf16")[2] > 1
+    A, B = from_gpu(sample(M, K, 1)), made(sample(N, K, 2, 0.0) / np.sqrt(K), 128)
+    C = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    il.iris_finalize()                                  # no workspace is there
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        il.iris_fp8_mm(C, A, B)
+    want = torch.empty_like(C)
+    il.iris_fp8_mm(want, A, B)
+    check_product(want, ref.values(*parts(A)), ref.values(*parts(B), 128), None, None, "bf16", "eager")
+    for _ in range(3):
+        C.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C, want)
+        il.iris_fp8_mm(C, A, B)                         # eager work between the replays
+        torch.cuda.synchronize()
+        assert torch.equal(C, want)
+    other = torch.cuda.Stream()
+    C.fill_(7.0)
+    torch.cuda.synchronize()
+    il.iris_fp8_mm(C, A, B, stream=other)
+    other.synchronize()
+    assert torch.equal(C, want)
+    ws = torch.full((need // 4 + 64,), float("nan"), dtype=torch.float32, device="cuda")
+    for _ in range(2):
+        C.fill_(7.0)
+        il.iris_fp8_mm(C, A, B, workspace=ws[:need // 4])
+        assert torch.equal(C, want) and bool(ws[need // 4:].isnan().all())
+    with pytest.raises(il.IrisError, match="WORKSPACE"):
+        il.iris_fp8_mm(C, A, B, workspace=ws[:need // 4 - 1])
