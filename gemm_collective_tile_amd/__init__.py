@@ -256,11 +256,14 @@ def _want_count(ts, n: int, name: str) -> None:
         raise ValueError(f"{name} holds {len(ts)} tensors, expected {n}")
 
 
-def _bias_along_m(config) -> bool:
+def _flags(config) -> int:
     if config is None:
-        return False
-    flags = config.get("flags", 0) if isinstance(config, dict) else config.flags
-    return bool(int(flags) & IRIS_FLAG_BIAS_ALONG_M)
+        return 0
+    return int(config.get("flags", 0) if isinstance(config, dict) else config.flags)
+
+
+def _bias_along_m(config) -> bool:
+    return bool(_flags(config) & IRIS_FLAG_BIAS_ALONG_M)
 
 
 def _want_bias(bias, M: int, N: int, config) -> None:
@@ -567,7 +570,7 @@ def iris_fp8_quantize(x, q: Optional[Fp8] = None, q_t: Optional[Fp8] = None, str
 
 
 def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, workspace=None, stream=None) -> None:
-    """C = A @ B^T + bias (+ C with accumulate): A (M, K) Fp8 with blocks of
+    """C = A @ B^T + bias (+ C with accumulate, or the flag in config): A (M, K) Fp8 with blocks of
     1 x 128, B (N, K) Fp8, C (M, N) float16, bfloat16 or float32, bias of C's type.
     A float32 C has exact products and 32-bit sums; a 16-bit one drops, of every 8
     products, what lies under 2^-13 of the largest."""
@@ -584,7 +587,7 @@ def iris_fp8_mm(C, A: Fp8, B: Fp8, bias=None, accumulate=False, config=None, wor
         _want_shape(C, (M, N), "C")
     dev = A._device
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
-    flags = IRIS_FLAG_ACCUMULATE if accumulate else 0
+    flags = IRIS_FLAG_ACCUMULATE if accumulate else _flags(config) & IRIS_FLAG_ACCUMULATE
     bias_ptr = None
     if bias is not None:
         _want_bias(bias, M, N, config)

@@ -433,6 +433,22 @@ def test_mm_accumulate_bias_along_m_and_pitch(M, N, K):
 
 
 @pytest.mark.gpu
+def test_mm_accumulates_by_argument_and_by_flag():
+    note("mm accumulate by flag")
+    A, B = made(sample(70, 260, 1)), made(sample(90, 260, 2))
+    outs = []
+    for kw in (dict(accumulate=True), dict(config=il.Config(flags=il.IRIS_FLAG_ACCUMULATE)),
+               dict(config={"flags": il.IRIS_FLAG_ACCUMULATE})):
+        C = torch.full((70, 90), 3.0, dtype=torch.float32, device="cuda")
+        il.iris_fp8_mm(C, A, B, **kw)
+        outs.append(C)
+    plain = torch.empty_like(outs[0])
+    il.iris_fp8_mm(plain, A, B)
+    assert torch.equal(outs[0], plain + 3.0)
+    assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 384, 4096), (5, 200, 11008), (48, 256, 2000), (130, 140, 1500), (520, 300, 4000)])
 def test_mm_integers_are_exact(M, N, K):
     """Small integers times powers of two: every partial sum fits 24 bits, so fp32 results are exact."""
