@@ -135,6 +135,10 @@ Fp8Mat mat(const iris_fp8_t* q) {
   return Fp8Mat{(uint8_t*)q->codes, (uint8_t*)q->scales, (int32_t)q->ld, (int32_t)q->ld_scales};
 }
 
+// No exception leaves a C entry: what can throw here is memory for a message or
+// for a device's record, or a lock.
+int caught(const std::exception& e) { return iris::set_error(IRIS_ERR_NO_MEMORY, e.what()); }
+
 int ready() {
   int dev = 0, cus = 0;
   return iris::use_device(&dev, &cus);
@@ -232,7 +236,7 @@ int fp8_finalize() {
 extern "C" {
 
 int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x, int32_t x_type, int64_t ldx,
-                      const iris_fp8_t* x8, int64_t rows, int64_t cols, void* stream) {
+                      const iris_fp8_t* x8, int64_t rows, int64_t cols, void* stream) try {
   iris::set_error(IRIS_OK, "");
   int st;
   if ((st = check_dims(rows, cols)) || (st = check_dims(cols, rows))) return st;
@@ -266,16 +270,20 @@ int iris_fp8_quantize(const iris_fp8_t* q, const iris_fp8_t* q_t, const void* x,
   a.rows = (int)rows;
   a.cols = (int)cols;
   return launched(iris::launch_fp8_quantize(a, (hipStream_t)stream), "iris_fp8_quantize");
+} catch (const std::exception& e) {
+  return caught(e);
 }
 
-size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K) {
+size_t iris_fp8_mm_workspace_size(int64_t M, int64_t N, int64_t K) try {
   if (check_mm_dims(M, N, K) || M == 0 || N == 0) return 0;
   return std::max(iris::fp8_mm_plan(M, N, K, false).ws_bytes, iris::fp8_mm_plan(M, N, K, true).ws_bytes);
+} catch (const std::exception&) {
+  return 0;
 }
 
 int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B, const void* bias,
                 int64_t M, int64_t N, int64_t K, int32_t flags, void* workspace, size_t workspace_bytes,
-                void* stream) {
+                void* stream) try {
   iris::set_error(IRIS_OK, "");
   int st = check_mm_dims(M, N, K);
   if (st) return st;
@@ -317,11 +325,13 @@ int iris_fp8_mm(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const
   const hipError_t e = plan.bm == 0 ? iris::launch_fp8_mm_few(a, (hipStream_t)stream)
                                               : iris::launch_fp8_mm(a, plan, workspace, (hipStream_t)stream);
   return launched(e, "iris_fp8_mm");
+} catch (const std::exception& e) {
+  return caught(e);
 }
 
 int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept, const void* gate,
                     const void* up, int32_t type, int64_t ld_gate, int64_t ld_up, int64_t rows, int64_t cols,
-                    void* stream) {
+                    void* stream) try {
   iris::set_error(IRIS_OK, "");
   int st;
   if ((st = check_dims(rows, cols)) || (st = check_blocks1(h, rows, cols, "h"))) return st;
@@ -350,12 +360,14 @@ int iris_fp8_swiglu(const iris_fp8_t* h, const iris_fp8_t* gate_kept, const iris
   a.rows = (int)rows;
   a.cols = (int)cols;
   return launched(iris::launch_fp8_swiglu(a, (hipStream_t)stream), "iris_fp8_swiglu");
+} catch (const std::exception& e) {
+  return caught(e);
 }
 
 int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const iris_fp8_t* dgate_t,
                         const iris_fp8_t* dup_t, const iris_fp8_t* h_t, const void* dh, int32_t type, int64_t ld_dh,
                         const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept, int64_t rows, int64_t cols,
-                        void* stream) {
+                        void* stream) try {
   iris::set_error(IRIS_OK, "");
   int st;
   if ((st = check_dims(rows, cols)) || (st = check_dims(cols, rows))) return st;
@@ -394,6 +406,8 @@ int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const ir
   a.rows = (int)rows;
   a.cols = (int)cols;
   return launched(iris::launch_fp8_swiglu_bwd(a, (hipStream_t)stream), "iris_fp8_swiglu_bwd");
+} catch (const std::exception& e) {
+  return caught(e);
 }
 
 }  // extern "C"

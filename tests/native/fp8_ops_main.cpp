@@ -11,6 +11,7 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
+#include <new>
 #include <set>
 #include <string>
 #include <thread>
@@ -24,6 +25,7 @@ std::set<void*> busy;                              // workspaces between a produ
 std::map<std::thread::id, std::set<void*>> used;   // by thread
 int overlaps = 0;
 std::atomic<int> mallocs{0}, frees{0};
+bool no_memory = false;
 }  // namespace
 
 extern "C" {
@@ -47,6 +49,7 @@ const char* hipGetErrorString(hipError_t) { return ""; }
 namespace iris {
 int set_error(int status, const char*) { return status; }
 int use_device(int* dev, int* cus) {
+  if (no_memory) throw std::bad_alloc();
   *dev = 0;
   *cus = 256;
   return 0;
@@ -120,6 +123,16 @@ int main() {
   bad += check(overlaps == 0, "products of different streams met in one workspace");
   bad += check(iris::fp8_finalize() == IRIS_OK && mallocs == frees, "everything is freed");
   bad += check(product(nullptr) == IRIS_OK && iris::fp8_finalize() == IRIS_OK && mallocs == frees, "use after finalize");
+  no_memory = true;   // no exception leaves an entry
+  const iris_fp8_t a{(void*)0x100000, (void*)0x200000, 4096, 32, 1}, b{(void*)0x300000, (void*)0x400000, 4096, 32, 1},
+      c{(void*)0x600000, (void*)0x700000, 4096, 32, 1}, d{(void*)0x800000, (void*)0x900000, 4096, 32, 1};
+  bad += check(product(nullptr) == IRIS_ERR_NO_MEMORY, "iris_fp8_mm without memory");
+  bad += check(iris_fp8_quantize(&a, nullptr, (void*)0x500000, IRIS_TYPE_FP16, 4096, nullptr, 8, 4096, nullptr) ==
+                   IRIS_ERR_NO_MEMORY, "iris_fp8_quantize without memory");
+  bad += check(iris_fp8_swiglu(&a, nullptr, nullptr, (void*)0x500000, (void*)0x510000, IRIS_TYPE_FP16, 4096, 4096, 8, 4096,
+                               nullptr) == IRIS_ERR_NO_MEMORY, "iris_fp8_swiglu without memory");
+  bad += check(iris_fp8_swiglu_bwd(&a, &b, nullptr, nullptr, nullptr, (void*)0x500000, IRIS_TYPE_FP16, 4096, &c, &d, 8, 4096,
+                                   nullptr) == IRIS_ERR_NO_MEMORY, "iris_fp8_swiglu_bwd without memory");
   if (!bad) printf("ok\n");
   return bad ? 1 : 0;
 }

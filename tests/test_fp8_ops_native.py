@@ -1,6 +1,6 @@
 """The 8-bit operators' entry points on the host alone: csrc/fp8_ops.cpp linked with
 stand-ins of the HIP runtime and of the kernels' launches (tests/native/fp8_ops_main.cpp),
-called from several threads."""
+called from several threads and with no memory left."""
 import os
 import shutil
 import subprocess
