@@ -68,15 +68,20 @@ int current_device(int* dev, DevInfo* info) {
   int d = 0;
   hipError_t e = hipGetDevice(&d);
   if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  bool known = false;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_dev.find(d);
-    if (it != g_dev.end()) {
+    known = it != g_dev.end();
+    if (known) {
       *dev = d;
       *info = it->second;
-      return IRIS_OK;
     }
   }
+  const auto unserved = [&] {
+    return fail(IRIS_ERR_NO_DEVICE, "device %d is %s; this library is built for gfx950", d, info->arch.c_str());
+  };
+  if (known) return info->ok ? IRIS_OK : unserved();
   hipDeviceProp_t prop;
   e = hipGetDeviceProperties(&prop, d);
   if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
@@ -97,8 +102,7 @@ int current_device(int* dev, DevInfo* info) {
   }
   *dev = d;
   *info = di;
-  if (!di.ok) return fail(IRIS_ERR_NO_DEVICE, "device %d is %s; this library is built for gfx950", d, di.arch.c_str());
-  return IRIS_OK;
+  return di.ok ? IRIS_OK : unserved();
 }
 
 // ------------------------------------------------------------ tuning cache
