@@ -693,6 +693,34 @@ def test_swiglu_bwd_of_many_tiles(rows, cols, dtype):
             assert_untouched(q, k)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1, 200), (200, 300), (2432, 2433)])
+def test_swiglu_bwd_nan_and_infinities_stay_where_they_are(rows, cols):
+    """NaN and infinities in dh and NaN codes in the kept gate give NaN codes there, and all else is as if zeros stood there."""
+    note(f"swiglu_bwd special values {rows}x{cols}")
+    rng = np.random.default_rng(rows)
+    at = np.zeros((rows, cols), bool)
+    at[rng.integers(0, rows, 60), rng.integers(0, cols, 60)] = True
+    kept = np.zeros((rows, cols), bool)
+    kept[rng.integers(0, rows, 20), rng.integers(0, cols, 20)] = True
+    base = sample(rows, cols, 3)
+    specials = np.array([np.nan, np.inf, -np.inf])[rng.integers(0, 3, (rows, cols))]
+    results = []
+    for filled in (False, True):
+        dh, _ = on_gpu(np.where(at, specials if filled else 0.0, np.where(kept, 0.0, base)), "bf16")
+        gk, uk = from_gpu(np.where(at | kept, 0.0, sample(rows, cols, 1))), from_gpu(np.where(at | kept, 0.0, sample(rows, cols, 2)))
+        if filled:
+            gk.codes.view(torch.uint8)[torch.from_numpy(kept).cuda()] = 0x7f
+        out = [fresh(rows, cols), fresh(rows, cols)] + [fresh(cols, rows) for _ in range(3)]
+        il.iris_fp8_swiglu_bwd(out[0], out[1], dh, gk, uk, *out[2:])
+        results.append([(c if i < 2 else c.T, s) for i, (c, s) in enumerate(parts(q) for q in out)])
+    for i, ((want, ws), (got, gs)) in enumerate(zip(*results)):
+        nan = kept if i == 4 else at | kept                 # h does not depend on dh
+        assert np.array_equal(ws, gs), i
+        assert np.array_equal((got & 0x7f) == 0x7f, nan), i
+        assert np.array_equal(got[~nan], want[~nan]), i
+
+
 # --------------------------------------------------------- streams and graphs
 
 @pytest.mark.gpu
