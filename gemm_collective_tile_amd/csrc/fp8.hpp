@@ -38,6 +38,7 @@ constexpr int kFp8Cus = 256;   // compute units of the chip
 // Few rows of A (at most kFp8FewRows): blocks of 16 rows of B for a workgroup. From
 // 17 rows of A on its time goes with what a CU loads, B's rows and A's once
 // for every workgroup, so the least of (workgroups a CU gets) * (blocks of both).
+// Up to kFp8AlwaysFew rows this kernel always runs: one order of sums for any N.
 constexpr int kFp8AlwaysFew = 64, kFp8FewRows = 96;
 inline int64_t fp8_few_loads(int64_t M, int64_t N, int nb) {
   return ((N + 16 * nb - 1) / (16 * nb) + kFp8Cus - 1) / kFp8Cus * (16 * nb + M);

@@ -45,9 +45,10 @@
 //     start at different ones: each fetches a quarter first and finds the
 //     others' quarters in L2. 8192^3: 505 -> 438 us on MI355X; with eight steps
 //     449, with sixteen 506 (the patch's rows no longer stay in L2).
-//   * Measured: 8192^3 into fp16 438 us, 2.5 PFLOP/s (its matrix instructions alone,
-//     at the power limit, 335; without loads 366); 11008 x 4096 x 4095 into fp32 316 us,
-//     1.17 PFLOP/s (8192^3: 812 us, 1.35), 2.69 rounds of tiles in the time of three.
+//   * Measured, by the card and its clocks: 8192^3 into fp16 421-444 us, 2.5-2.6 PFLOP/s
+//     (where it took 438, its matrix instructions alone, at the power limit, 335;
+//     without loads 366); 11008 x 4096 x 4095 into fp32 312-334 us, 1.1-1.2 PFLOP/s
+//     (8192^3: 787-812, 1.35-1.40), 2.69 rounds of tiles in the time of three.
 //   * The loads into LDS are written as assembly, because the compiler would
 //     wait for all of them at the next LDS read.
 #include <algorithm>
@@ -496,13 +497,20 @@ hipError_t run(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t 
 //   784 x 389 x 5242            23.9   18.6   14.5
 //   182 x 4704 x 9980           37.3   29.5   28.9
 //   2048 x 1024 x 4096          21.2   26.5   33.5
-// Over 42 such sizes its choice is 3 % slower than the best tile (geometric mean).
-// More LDS stages (five of each operand) leave all of these as they are.
+// Over 42 sizes drawn at random (97 to 4096 rows, 97 to 8192 columns, 256 to 8192
+// deep) its choice is 1.2 % slower than the best tile and split (geometric mean; the
+// worst, 948 x 207 x 3204 in 7 splits where 4 are best, 15 %). Its predicted times are
+// looser than its choice: 1360 x 3015 x 5344 is predicted at 40.6 and took 38.9 and 50.2
+// on two cards. More LDS stages (five of each operand) leave all of these as they are.
 // Up to 96 rows of A the kernel for few rows competes, by what a CU loads at 66 GB/s:
 //   65 x 4096 x 4096     few 8.6, tiles 12.5      96 x 11008 x 4096 (fp32)   16.2, 26.8
 //   65 x 800 x 11008         14.0       11.9      96 x 2048 x 8192           14.5, 13.4
 // From 97 rows on its gain is gone (128 x 8192 x 8192: 23.8, 24.2; 128 x 4096 x 11008:
-// 24.9, 22.5), and up to 64 rows it loses by 4 % at most but where B has few rows.
+// 24.9, 22.5). Up to 64 rows of A it runs without a comparison, so that a column's bits
+// do not depend on N (a token's logits not on the vocabulary's shard). Where B has few
+// rows and K is long that costs time: 64 x 512 x 11008 takes 13.7 us on 32 workgroups,
+// split tiles of 65 rows 10.3; 64 x 1024 x 11008 14.3 and 12.1; at 2048 rows of B they
+// are even (14.4, 15.4).
 namespace {
 struct TileTimes {
   int bm, bn, levels;       // levels: 1, 2, 4 tiles on a CU

@@ -19,8 +19,9 @@
 // workgroup reads all of A again. NB = 2 or 3 share that reading among more rows of
 // B, if the CUs stay occupied (fp8_few_blocks). 11008 x 4096 in bf16: 33 rows 10.7
 // us against 17.2 with NB = 1, 64 rows 12.7 against 23.3, 17 rows 9.7 against 13.0.
-// At one row it is memory: 8.3 us (11008 x 4096, 5.4 TB/s with the launch; 6.6 TB/s
-// between 16 and 45 MB). Two steps under way per wave gained nothing there and
+// At one row it is B's bytes: 11008 x 4096 in 8.4 us out of the last-level cache (5.3
+// TB/s with the launch; 6.6 TB/s between 16 and 45 MB), 10.0 out of HBM (ten such
+// matrices in turn, 4.5 TB/s). Two steps under way per wave gained nothing there and
 // cost a tenth at 33 rows. NB = 4 gained 8 % at 64 rows of 32000 x 4096 and took
 // more than the register file with 32-bit sums kept in two parts.
 #include <algorithm>

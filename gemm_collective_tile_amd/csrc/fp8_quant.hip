@@ -50,9 +50,9 @@ __device__ __forceinline__ void put_row_block(const Fp8Mat& q, const RowPlace& p
   if ((threadIdx.x & 7) == 0) q.scales[(int64_t)p.row * q.lds + p.kb] = (uint8_t)s;
 }
 
-// Bound by memory where the matrix is large: 8192 x 16384 in bf16 69.7 us, 5.8 TB/s
+// Bound by memory where the matrix is large: 8192 x 16384 in bf16 69.9 us, 5.8 TB/s
 // read and written (a 1 GiB copy runs at 5.1); 2048 x 4096 5.4 us; one row of
-// 4096 1.6 us, of which the launch is all. Eight lanes a block and no loop, so that
+// 4096 1.75 us, of which the launch is all. Eight lanes a block and no loop, so that
 // every load of a round of workgroups is under way at once.
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(const T* x, int ldx, int rows, int cols, Fp8Mat q, FastDiv nkb) {
@@ -230,9 +230,9 @@ __device__ __forceinline__ void put_row(const Fp8Mat& q, const TilePlace& p, int
 }
 
 // x -> rows and / or columns, or 128 x 128 blocks. Both directions of 8192 x 16384
-// in bf16 112 us, 4.8 TB/s (a 1 GiB copy: 5.1); 4096 x 11008 40 us; 128 x 128 blocks
-// of 11008 x 4096 in fp32, both directions, 53 us, 5.1 TB/s; 8 bits turned around,
-// 4096 x 4096, 8.2 us. The small ones are one round of workgroups, which load, turn
+// in bf16 111 us, 4.8 TB/s (a 1 GiB copy: 5.1); 4096 x 11008 39 us; 128 x 128 blocks
+// of 11008 x 4096 in fp32, both directions, 54 us, 5.0 TB/s; 8 bits turned around,
+// 4095 x 4096, 8.5 us. The small ones are one round of workgroups, which load, turn
 // and store in step: what one waits for is not hidden by another. 128 x 128 is the
 // least tile that holds whole blocks of both directions.
 template <class T, bool WHOLE>
@@ -311,7 +311,7 @@ struct BwdInputs {
 // registers are free: 113 a thread, so 4 waves fit a SIMD. All three at once
 // spill at that width (4096 x 11008: 143 us against 100), and with 2 waves a SIMD,
 // the next tile's loads under way, take 123; 6 waves a SIMD, the results formed one
-// at a time, 164. 4096 x 11008 in bf16: 100 us, 4.1 TB/s; its loads and stores with
+// at a time, 164. 4096 x 11008 in bf16: 101 us, 4.0 TB/s; its loads and stores with
 // nothing formed between them take 88, the vector units are busy two thirds of the
 // time (40 instructions a value, two of them exp and two rcp).
 template <class T, bool WHOLE>
