@@ -880,3 +880,36 @@ def test_split_products_in_graphs_on_streams_and_in_a_callers_workspace():
         assert torch.equal(C, want) and bool(ws[need // 4:].isnan().all())
     with pytest.raises(il.IrisError, match="WORKSPACE"):
         il.iris_fp8_mm(C, A, B, workspace=ws[:need // 4 - 1])
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(3, 40), (70, 90), (90, 300), (200, 130), (700, 1100), (2300, 2100)])
+def test_mm_of_nothing_in_every_kernel(M, N):
+    """K = 0: the bias and the old value alone, from the kernel for few rows and from tiles."""
+    note(f"mm {M}x{N}x0")
+    A, B = il.iris_fp8_empty(M, 0), il.iris_fp8_empty(N, 0, 128)
+    bias = torch.arange(M, dtype=torch.float32, device="cuda")
+    C = torch.full((M, N), float("nan"), dtype=torch.float32, device="cuda")
+    il.iris_fp8_mm(C, A, B)
+    assert torch.equal(C, torch.zeros_like(C))
+    along_m = dict(config=il.Config(flags=il.IRIS_FLAG_BIAS_ALONG_M))
+    il.iris_fp8_mm(C, A, B, bias, **along_m)
+    assert torch.equal(C, bias[:, None].expand(M, N))
+    il.iris_fp8_mm(C, A, B, bias, accumulate=True, **along_m)
+    assert torch.equal(C, 2 * bias[:, None].expand(M, N))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(1, 1 << 21), (40, (1 << 21) - 77), (90, 1 << 21), (200, (1 << 21) - 77), (200, 1 << 21)])
+def test_mm_of_the_longest_contraction(M, K):
+    """2^21 products of -1, 0 and 1: every sum is exact, whatever its order."""
+    N = 70
+    note(f"mm {M}x{N}x{K}")
+    rng = np.random.default_rng(M)
+    a, b = (rng.integers(-1, 2, (n, K)).astype(np.int8) for n in (M, N))
+    one = np.array([0xb8, 0x00, 0x38], np.uint8)
+    A, B = put(one[a + 1], np.full((M, -(-K // 128)), 127, np.uint8)), put(one[b + 1], np.full((N, -(-K // 128)), 127, np.uint8))
+    want = a.astype(np.float32) @ b.T.astype(np.float32)     # below 2^24
+    for dtype in ("fp32", "fp16"):
+        C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+        il.iris_fp8_mm(C, A, B)
+        assert torch.equal(C.cpu(), torch.from_numpy(want).to(DT[dtype]))
