@@ -14,9 +14,9 @@
 //
 // fp32 C (weight gradients to be summed up) asks for more: the codes become
 // bf16 values with their scales applied (v_cvt_scalef32_pk_bf16_fp8, exact
-// within bf16's range) and v_mfma_f32_32x32x16_bf16, at half the rate, multiplies them exactly and
-// sums in 32 bits (4e-8 of the result, measured). The conversions run in the
-// shadow of the matrix instructions.
+// within bf16's range) and v_mfma_f32_32x32x16_bf16, at half the rate,
+// multiplies them exactly and sums in 32 bits (4e-8 of the result, measured).
+// The conversions run in the shadow of the matrix instructions.
 //
 // Any order of k inside an instruction's slice gives the same sum as long as
 // both operands use it, and a block's scale is the same for all its slices, so

@@ -294,9 +294,10 @@ int iris_concurrent(void* C, const void* A, const void* B, const void* bias,
  *              bytes up to it allocated; ignored).
  * The structs are read before the call returns; the buffers belong to the
  * caller. No output may overlap another operand (equal addresses are refused with
- * IRIS_ERR_INVALID_ARG): no operator works in place. Unlike above, plain matrices (x, C, gate, up, dh) may have any row
- * pitch >= their columns and need only the alignment of their type; rows that
- * start at multiples of 16 bytes are a little faster.
+ * IRIS_ERR_INVALID_ARG): no operator works in place. Unlike above, plain matrices
+ * (x, C, gate, up, dh) may have any row pitch >= their columns and need only the
+ * alignment of their type; rows that start at multiples of 16 bytes are a little
+ * faster.
  * Limits (IRIS_ERR_UNSUPPORTED beyond): row pitches of codes, scales and plain
  * matrices up to 2^22, and so columns (N of a product, rows of a matrix that is
  * turned around); rows up to 2^30, fewer than 2^31 blocks of 128 along the rows;
