@@ -203,11 +203,15 @@ def prepare(case, seed):
             s["C"] = torch.empty((M, N), dtype=dt, device="cuda")
             s["dbias"] = torch.empty((N,), dtype=dt, device="cuda")
         fp8 = {"A": 1, "B": BLK, "q": 1}
-    if own:  # the handles that a program keeps: of its block-scaled buffers, of the generator's place
+    if own:  # the handles that a program keeps: of its block-scaled buffers, of the generator's place, of a norm's parameters
         import gemm_collective_tile_amd as il
         s["il"] = il
         s["m"] = {k: None if s.get(k) is None else il.Fp8(*s[k], block=b) for k, b in fp8.items()}
         s["drop"] = il.Dropout(case["p"], *s["key"]) if case["p"] > 0 else None
+        if op in ("norm", "norm_bwd"):
+            s["norm"] = il.BlockNorm(kind=case["kind"], eps=EPS, pre_w=s["pre_w"], pre_b=s["pre_b"], post=case["post"],
+                                     post_w=s["post_w"], post_b=s["post_b"], gate=s["gate"],
+                                     rows_per_gate=case["gate"], alpha=s["alpha"], dropout=s["drop"])
     return s
 
 
@@ -389,14 +393,10 @@ def run(state):
         il.iris_dropout(s["out"], s["x"], s["drop"], residual=s["residual"], alpha=s["alpha"])
         return s["out"]
     if case["op"] == "norm":
-        il.iris_block_norm(s["x"], kind=case["kind"], eps=EPS, pre_w=s["pre_w"], pre_b=s["pre_b"], n=s["n"], q=s["m"]["q"],
-                           y=s["y"], r=s["r"], post=case["post"], post_w=s["post_w"], post_b=s["post_b"], gate=s["gate"],
-                           rows_per_gate=case["gate"], alpha=s["alpha"], dropout=s["drop"], stats=s["stats"])
+        il.iris_block_norm(s["x"], s["norm"], y=s["y"], r=s["r"], n=s["n"], q=s["m"]["q"], stats=s["stats"])
         return {k: s[k] for k in ("r", "n", "q", "stats")}
     if case["op"] == "norm_bwd":
-        il.iris_block_norm_bwd(s["dx"], s["r"], s["stats"], kind=case["kind"], dn=s["dn"], dr=s["dr"], pre_w=s["pre_w"],
-                               y=s["y"], dy=s["dy"], post=case["post"], post_w=s["post_w"], post_b=s["post_b"],
-                               gate=s["gate"], rows_per_gate=case["gate"], alpha=s["alpha"], dropout=s["drop"],
+        il.iris_block_norm_bwd(s["dx"], s["r"], s["stats"], s["norm"], dn=s["dn"], dr=s["dr"], y=s["y"], dy=s["dy"],
                                dpre_w=s["dpre_w"], dpre_b=s["dpre_b"], dpost_w=s["dpost_w"], dpost_b=s["dpost_b"],
                                dgate=s["dgate"])
         return {k: s[k] for k in ("dx", "dy", "dpre_w", "dpre_b", "dpost_w", "dpost_b", "dgate")}
@@ -527,7 +527,8 @@ def exact(case, seed):
         return r, (r - sr[0][:, None]) * sr[1][:, None] * pre_w + pre_b, torch.stack([*sy, *sr], 1)
 
     which = torch.arange(case["rows"], device="cuda") // max(1, case["gate"])
-    wide = {k: (v if d[k] is None else d[k].reshape(1, -1)) for k, v in (("pre_w", one), ("pre_b", zero), ("post_w", one), ("post_b", zero))}
+    wide = {k: v if d[k] is None else d[k].reshape(1, -1)
+            for k, v in (("pre_w", one), ("pre_b", zero), ("post_w", one), ("post_b", zero))}
     gate = one if d["gate"] is None else d["gate"][which]
     if op == "norm":
         r, n, stats = forward(d["x"], d["y"], wide["pre_w"], wide["pre_b"], wide["post_w"], wide["post_b"], gate)
