@@ -33,6 +33,12 @@ struct Fp8MmPlan {
   size_t ws_bytes = 0;
 };
 Fp8MmPlan fp8_mm_plan(int64_t M, int64_t N, int64_t K, bool fp32);
+// the same with whole (unsplit) tiles of at least so many columns
+Fp8MmPlan fp8_mm_plan_wide(int64_t M, int64_t N, int64_t K, bool fp32, int least_bn);
+// floats from one row of a split's sums to the next
+inline int64_t fp8_sums_pitch(int64_t N) { return (N + 3) / 4 * 4; }
+// a split product's sums alone: plan.splits matrices of M rows, in 32 bits
+hipError_t launch_fp8_mm_splits(const Fp8MmArgs& a, const Fp8MmPlan& plan, bool exact, void* ws, hipStream_t s);
 hipError_t launch_fp8_mm(const Fp8MmArgs& a, const Fp8MmPlan& plan, void* ws, hipStream_t s);
 constexpr int kFp8Cus = 256;   // compute units of the chip
 // Few rows of A (at most kFp8FewRows): blocks of 16 rows of B for a workgroup. From
