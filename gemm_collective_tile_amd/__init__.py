@@ -19,6 +19,15 @@ and, in block-scaled 8-bit floating point (Fp8: codes, scales):
   iris_fp8_swiglu      h = silu(gate) * up, gate and up kept in 8 bits if wanted
   iris_fp8_swiglu_bwd  its backward pass from the kept gate and up
 
+and, between a block's products and its residual stream (BlockNorm: the parameters of
+its norms; Dropout: the place of a mask that is computed and never stored):
+
+  iris_dropout         out = residual + alpha m x
+  iris_block_norm      r = x + alpha gate m norm(y), n = norm(r), in 16 bits and / or 8
+  iris_block_norm_bwd  its backward pass
+  iris_fp8_mm_act      C = residual + alpha m act(A @ B^T + bias), in 16 or 32 bits and / or 8
+  iris_fp8_mm_act_bwd  C = alpha m (A @ B^T) act'(z), and the bias's gradient
+
 There is no fallback: if the library is missing or fails to load, importing
 this package raises.
 """
@@ -52,6 +61,13 @@ IRIS_COLL_ALL_GATHER = 2
 IRIS_COLL_REDUCE_SCATTER = 3
 IRIS_COLL_ALL_TO_ALL = 4
 IRIS_COLL_BROADCAST = 5
+IRIS_NORM_RMS = 1
+IRIS_NORM_LAYER = 2
+IRIS_ACT_NONE = 0
+IRIS_ACT_RELU = 1
+IRIS_ACT_GELU = 2
+IRIS_ACT_GELU_TANH = 3
+IRIS_ACT_SILU = 4
 
 STATUS = {
     0: "IRIS_OK", 1: "IRIS_ERR_INVALID_ARG", 2: "IRIS_ERR_UNSUPPORTED", 3: "IRIS_ERR_CONFIG",
@@ -105,6 +121,26 @@ class _Fp8(ctypes.Structure):
                 ("ld_scales", ctypes.c_int64), ("block", ctypes.c_int32)]
 
 
+class _Drop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_at", ctypes.c_void_p)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("type", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("param_type", ctypes.c_int32), ("gate_type", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("pre_w", ctypes.c_void_p), ("pre_b", ctypes.c_void_p), ("post_w", ctypes.c_void_p),
+                ("post_b", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("rows_per_gate", ctypes.c_int64), ("drop", ctypes.POINTER(_Drop))]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("alpha", ctypes.c_float), ("bias", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("ld_z", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("q", ctypes.POINTER(_Fp8)), ("drop", ctypes.POINTER(_Drop))]
+
+
 class _PredictParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in (
         "gemm_tflops_per_cu", "tile_overhead_us", "comm_gbps_per_cu", "comm_gbps_chip", "unit_overhead_us",
@@ -128,6 +164,7 @@ def _load() -> ctypes.CDLL:
     vpp = ctypes.POINTER(ctypes.c_void_p)
     cfgp = ctypes.POINTER(_Config)
     f8 = ctypes.POINTER(_Fp8)
+    drop, norm, f32 = ctypes.POINTER(_Drop), ctypes.POINTER(_Norm), ctypes.c_float
     sig = {
         "iris_ag_mm": [vp, vp, vpp, i32, vp, vp, i64, i64, i64, cfgp, vp, sz, vp],
         "iris_ag_mm_noalloc": [vp, vp, vpp, i32, vp, vp, i64, i64, i64, cfgp, vp],
@@ -139,6 +176,12 @@ def _load() -> ctypes.CDLL:
         "iris_fp8_mm": [vp, i32, i64, f8, f8, vp, i64, i64, i64, i32, vp, sz, vp],
         "iris_fp8_swiglu": [f8, f8, f8, vp, vp, i32, i64, i64, i64, i64, vp],
         "iris_fp8_swiglu_bwd": [f8, f8, f8, f8, f8, vp, i32, i64, f8, f8, i64, i64, vp],
+        "iris_dropout": [vp, i64, vp, i64, vp, i64, i32, f32, drop, i64, i64, vp],
+        "iris_block_norm": [vp, i64, vp, i64, f8, vp, vp, i64, vp, i64, norm, i64, i64, vp],
+        "iris_block_norm_bwd": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, norm, i64, i64,
+                                vp, sz, vp],
+        "iris_fp8_mm_act": [vp, i32, i64, f8, f8, ctypes.POINTER(_Epilogue), i64, i64, i64, vp, sz, vp],
+        "iris_fp8_mm_act_bwd": [vp, i32, i64, vp, f8, f8, vp, i64, i32, f32, drop, i64, i64, i64, vp, sz, vp],
         "iris_grid_size": [ctypes.c_int32, cfgp],
         "iris_tune_gemm_wgs": [ctypes.POINTER(_OpArgs), ctypes.POINTER(i32), i32, i32, i32,
                                ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_float), vp],
@@ -162,6 +205,10 @@ def _load() -> ctypes.CDLL:
     lib.iris_workspace_size.restype = sz
     lib.iris_fp8_mm_workspace_size.argtypes = [i64, i64, i64]
     lib.iris_fp8_mm_workspace_size.restype = sz
+    lib.iris_block_norm_bwd_workspace_size.argtypes = [i64, i64]
+    lib.iris_block_norm_bwd_workspace_size.restype = sz
+    lib.iris_fp8_mm_act_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+    lib.iris_fp8_mm_act_workspace_size.restype = sz
     lib.iris_status_str.restype = ctypes.c_char_p
     lib.iris_last_error_message.restype = ctypes.c_char_p
     return lib
@@ -657,6 +704,344 @@ def iris_fp8_swiglu_bwd(dgate: Fp8, dup: Fp8, dh, gate_kept: Fp8, up_kept: Fp8, 
 
 def iris_fp8_mm_workspace_size(M, N, K) -> int:
     return int(_lib.iris_fp8_mm_workspace_size(M, N, K))
+
+
+# ---------------------------------------------------------- block operators
+
+class Dropout:
+    """The place of a mask: probability p, 64-bit seed and offset, and optionally
+    `counter`, an int64 tensor of one element on the GPU that the kernels add to the
+    offset (a graph that is replayed takes new masks by it). The mask goes by these and
+    a value's row and column alone; operators on matrices of one size that are given
+    the same Dropout drop the same values. `offset` may be set anew between calls."""
+    __slots__ = ("p", "seed", "counter", "_c", "_p", "_device")
+
+    def __init__(self, p: float, seed: int, offset: int = 0, counter: Optional[torch.Tensor] = None):
+        if not 0.0 <= p < 1.0:
+            raise ValueError(f"p must be in [0, 1) (got {p})")
+        at, self._device = None, None
+        if counter is not None:
+            if not isinstance(counter, torch.Tensor) or counter.dtype != torch.int64:
+                raise TypeError("counter must be an int64 torch tensor")
+            _want_numel(counter, 1, "counter")
+            at, self._device = counter.data_ptr(), counter.get_device()
+        self.p, self.seed, self.counter = float(p), int(seed) % 2 ** 64, counter
+        self._c = _Drop(self.p, self.seed, int(offset) % 2 ** 64, at)
+        self._p = ctypes.pointer(self._c)
+
+    @property
+    def offset(self) -> int:
+        return self._c.offset
+
+    @offset.setter
+    def offset(self, value: int) -> None:
+        self._c.offset = int(value) % 2 ** 64
+
+
+def _drop(dropout, dev: int):
+    if dropout is None:
+        return None
+    if dropout.__class__ is not Dropout:
+        raise TypeError("dropout must be a Dropout")
+    if dropout._device is not None and dropout._device != dev:
+        raise _elsewhere("dropout's counter", dropout._device, dev)
+    return dropout._p
+
+
+def _any_plain(t, name: str, shape, kind, dev: int):
+    """(pointer, row pitch) of a matrix of one type; (None, 0) if it is not given."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        _want_shape(t, shape, name)
+    if t.dtype is not kind:
+        raise TypeError(f"{name} must be {str(kind)[6:]}")
+    ptr, _, ld = _plain(t, name, _FP8_TYPES, shape[0], shape[1], dev)
+    return ptr, ld
+
+
+def _call_stream(stream, dev: int):
+    return _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev)
+
+
+def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float = 1.0, stream=None) -> None:
+    """out = residual + alpha m x, (rows, cols) float16, bfloat16 or float32 of any row
+    pitch; m is dropout's mask. On out's gradient it is its own backward pass."""
+    shape = rows, cols = _shape2(x, "x")
+    dev = x.get_device()
+    ptr, kind, ld = _plain(x, "x", _FP8_TYPES, rows, cols, dev)
+    if out is None:
+        raise ValueError("out is required")
+    op, old = _any_plain(out, "out", shape, x.dtype, dev)
+    rp, rld = _any_plain(residual, "residual", shape, x.dtype, dev)
+    st = _lib.iris_dropout(op, old, ptr, ld, rp, rld, kind, alpha, _drop(dropout, dev), rows, cols, _call_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+_NORM_KINDS = {"rms": IRIS_NORM_RMS, "layer": IRIS_NORM_LAYER, IRIS_NORM_RMS: IRIS_NORM_RMS, IRIS_NORM_LAYER: IRIS_NORM_LAYER}
+
+
+class BlockNorm:
+    """The parameters of the norms around a block (iris_norm_t): of the norm after it,
+    if there is one (`post`), and of the norm before the next. Weights and biases are
+    vectors of one dtype (float32, or that of the activations), `gate` a vector or a
+    matrix whose row i / rows_per_gate goes with row i. A handle: it reads the
+    tensors' addresses once and holds the tensors, so their memory must not be
+    exchanged under it; their values may change between calls."""
+    __slots__ = ("cols", "post", "gate", "rows_per_gate", "dropout", "_fields", "_held", "_param", "_gate", "_structs", "_device")
+
+    def __init__(self, kind="rms", eps: float = 1e-6, pre_w=None, pre_b=None, post: bool = False, post_w=None, post_b=None,
+                 gate=None, rows_per_gate: Optional[int] = None, alpha: float = 1.0, dropout: Optional[Dropout] = None,
+                 w_offset: float = 0.0):
+        if kind not in _NORM_KINDS:
+            raise ValueError(f"kind must be 'rms' or 'layer' (got {kind!r})")
+        if dropout is not None and dropout.__class__ is not Dropout:
+            raise TypeError("dropout must be a Dropout")
+        if not post and (post_w is not None or post_b is not None):
+            raise ValueError("post_w and post_b need post")
+        given = {k: v for k, v in (("pre_w", pre_w), ("pre_b", pre_b), ("post_w", post_w), ("post_b", post_b)) if v is not None}
+        self.cols = self._param = self._device = None
+        for name, t in given.items():
+            if not isinstance(t, torch.Tensor) or t.dtype not in _FP8_TYPES:
+                raise TypeError(f"{name} must be a float16, bfloat16 or float32 torch tensor")
+            if t.dim() != 1 or (self.cols is not None and t.numel() != self.cols):
+                raise ValueError(f"{name} must be a vector" + ("" if self.cols is None else f" of {self.cols} values"))
+            if t.numel() > 1 and t.stride(0) != 1:
+                raise ValueError(f"{name} must be contiguous")
+            if self._param is not None and t.dtype != self._param:
+                raise TypeError("weights and biases must have one dtype")
+            self._at(t, name)
+            self.cols, self._param = t.numel(), t.dtype
+        self._gate, ld = None, 0
+        if gate is not None:
+            if not isinstance(gate, torch.Tensor) or gate.dtype not in _FP8_TYPES:
+                raise TypeError("gate must be a float16, bfloat16 or float32 torch tensor")
+            if gate.dim() not in (1, 2) or (self.cols is not None and gate.shape[-1] != self.cols):
+                raise ValueError("gate must be a vector or a matrix" + ("" if self.cols is None else f" of {self.cols} columns"))
+            if gate.shape[-1] > 1 and gate.stride(-1) != 1:
+                raise ValueError("gate must be contiguous along its rows")
+            if gate.dim() == 2 and rows_per_gate is None and gate.shape[0] != 1:
+                raise ValueError("rows_per_gate is required with a gate of several rows")
+            if rows_per_gate is not None and rows_per_gate < 1:
+                raise ValueError(f"rows_per_gate must be positive (got {rows_per_gate})")
+            self._at(gate, "gate")
+            self.cols, self._gate = gate.shape[-1], gate.dtype
+            ld = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else gate.shape[-1]
+        self.post, self.gate, self.dropout = bool(post), gate, dropout
+        self.rows_per_gate = (1 << 62) if gate is None or rows_per_gate is None else int(rows_per_gate)
+        self._held = given
+        at = [given[k].data_ptr() if k in given else None for k in ("pre_w", "pre_b", "post_w", "post_b")]
+        self._fields = (_NORM_KINDS[kind], int(self.post), eps, w_offset, alpha, at, None if gate is None else gate.data_ptr(), ld,
+                        self.rows_per_gate, None if dropout is None else dropout._p)
+        self._structs = {}
+
+    def _at(self, t, name: str) -> None:
+        if self._device is not None and t.get_device() != self._device:
+            raise ValueError(f"{name} is on another device than the other parameters")
+        self._device = t.get_device()
+
+    def _struct(self, kind, stream_kind):
+        """iris_norm_t for activations and a stream of these dtypes; never changed once made."""
+        p = self._structs.get((kind, stream_kind))
+        if p is None:
+            types = []
+            for dtype, name in ((stream_kind, "the stream (x, r)"), (self._param, "weights and biases"), (self._gate, "the gate")):
+                if dtype is not None and dtype not in (kind, torch.float32):
+                    raise TypeError(f"{name} must be {str(kind)[6:]} as y and n are, or float32")
+                types.append(_FP8_TYPES[dtype or kind])
+            norm, post, eps, w_offset, alpha, at, gate, ld, every, drop = self._fields
+            p = ctypes.pointer(_Norm(norm, _FP8_TYPES[kind], *types, post, eps, w_offset, alpha, *at, gate, ld, every, drop))
+            self._structs[kind, stream_kind] = p
+        return p
+
+    def _for(self, rows: int, cols: int, dev: int) -> None:
+        if self.cols is not None and self.cols != cols:
+            raise ValueError(f"the norm's parameters have {self.cols} columns, the activations {cols}")
+        if self._device is not None and self._device != dev:
+            raise _elsewhere("the norm's parameters", self._device, dev)
+        if self.gate is not None and self.gate.dim() == 2 and rows > 0 and self.gate.shape[0] != -(-rows // self.rows_per_gate):
+            raise ValueError(f"gate has {self.gate.shape[0]} rows, expected {-(-rows // self.rows_per_gate)}")
+        if self.gate is not None and self.gate.dim() == 1 and self.rows_per_gate < rows:
+            raise ValueError("a gate for every rows_per_gate rows must be a matrix")
+        if self.dropout is not None:
+            _drop(self.dropout, dev)
+
+
+def _norm_kind(norm, stream_kind, *tensors):
+    """dtype of the activations: of the first tensor that is given, else of the stream or the parameters."""
+    if norm.__class__ is not BlockNorm:
+        raise TypeError("norm must be a BlockNorm")
+    for t in tensors:
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dtype not in _FP8_HALVES:
+                raise TypeError("y, n, dn and dy must be float16 or bfloat16 torch tensors")
+            return t.dtype
+    for dtype in (stream_kind, norm._param, norm._gate):
+        if dtype in _FP8_HALVES:
+            return dtype
+    return torch.bfloat16
+
+
+def _stats_ptr(stats, rows: int, dev: int):
+    if stats is None:
+        return None
+    _want_shape(stats, (rows, 4), "stats")
+    if stats.dtype != torch.float32 or not stats.is_contiguous():
+        raise TypeError("stats must be a contiguous float32 tensor")
+    if stats.get_device() != dev:
+        raise _elsewhere("stats", stats.get_device(), dev)
+    return stats.data_ptr()
+
+
+def iris_block_norm(x, norm: BlockNorm, y=None, r=None, n=None, q: Optional[Fp8] = None, stats=None, stream=None) -> None:
+    """r = x + alpha gate m p with p = norm(y) (norm.post) or y, and n = norm(r), in 16
+    bits (n), in 8 (q) or both; without y, n = norm(x). x, r: float32 or the dtype of y
+    and n (float16, bfloat16); stats (rows, 4) float32 receives what the backward pass
+    needs. Outputs that are not wanted are None."""
+    shape = rows, cols = _shape2(x, "x")
+    dev = x.get_device()
+    kind = _norm_kind(norm, x.dtype, y, n)
+    norm._for(rows, cols, dev)
+    p = norm._struct(kind, x.dtype)
+    xp, _, xld = _plain(x, "x", _FP8_TYPES, rows, cols, dev)
+    st = _lib.iris_block_norm(*_any_plain(r, "r", shape, x.dtype, dev), *_any_plain(n, "n", shape, kind, dev),
+                              None if q is None else _fp8(q, shape, "q", dev), _stats_ptr(stats, rows, dev), xp, xld,
+                              *_any_plain(y, "y", shape, kind, dev), p, rows, cols, _call_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def _sums(t, name: str, shape, dev: int):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        _want_shape(t, shape, name)
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise _elsewhere(name, t.get_device(), dev)
+    return t.data_ptr()
+
+
+def iris_block_norm_bwd(dx, r, stats, norm: BlockNorm, dn=None, dr=None, y=None, dy=None, dpre_w=None, dpre_b=None, dpost_w=None,
+                        dpost_b=None, dgate=None, workspace=None, stream=None) -> None:
+    """Backward pass of iris_block_norm at its r, y and stats: dn is n's gradient, dr
+    what reaches r from elsewhere. dx (dtype of r), dy (of y); the parameters' gradients
+    in float32, dgate of the gate's shape. What is not wanted is None."""
+    shape = rows, cols = _shape2(r, "r")
+    dev = r.get_device()
+    kind = _norm_kind(norm, r.dtype, y, dn, dy)
+    norm._for(rows, cols, dev)
+    p = norm._struct(kind, r.dtype)
+    if dgate is not None and norm.gate is None:
+        raise ValueError("dgate needs a gate")
+    rp, _, rld = _plain(r, "r", _FP8_TYPES, rows, cols, dev)
+    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
+    st = _lib.iris_block_norm_bwd(
+        *_any_plain(dx, "dx", shape, r.dtype, dev), *_any_plain(dy, "dy", shape, kind, dev),
+        _sums(dpre_w, "dpre_w", (cols,), dev), _sums(dpre_b, "dpre_b", (cols,), dev), _sums(dpost_w, "dpost_w", (cols,), dev),
+        _sums(dpost_b, "dpost_b", (cols,), dev), None if dgate is None else _sums(dgate, "dgate", norm.gate.shape, dev),
+        *_any_plain(dn, "dn", shape, kind, dev), *_any_plain(dr, "dr", shape, r.dtype, dev), rp, rld,
+        *_any_plain(y, "y", shape, kind, dev), _stats_ptr(stats, rows, dev), p, rows, cols, ws, wsb, _call_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def iris_block_norm_bwd_workspace_size(rows: int, cols: int) -> int:
+    return int(_lib.iris_block_norm_bwd_workspace_size(rows, cols))
+
+
+_ACTS = {"none": IRIS_ACT_NONE, "relu": IRIS_ACT_RELU, "gelu": IRIS_ACT_GELU, "gelu_tanh": IRIS_ACT_GELU_TANH,
+         "silu": IRIS_ACT_SILU}
+_ACTS.update({v: v for v in tuple(_ACTS.values())})
+
+
+def _mm_operands(A, B, act):
+    """(M, N, K, dev, activation) of a product of Fp8 matrices."""
+    if A.__class__ is not Fp8 or B.__class__ is not Fp8:
+        raise TypeError("A and B must be Fp8 matrices")
+    M, K = A.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError(f"B has shape {B.shape}, expected ({N}, {K})")
+    if not (A._scale_words and B._scale_words):
+        raise ValueError(f"the last row of {'B' if A._scale_words else 'A'}'s scales must be followed by memory up to the "
+                         "next multiple of 4 bytes; see iris_fp8_empty")
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(k for k in _ACTS if isinstance(k, str))} (got {act!r})")
+    return M, N, K, A._device, code
+
+
+def _mm_vector(t, name: str, N: int, kind, dev: int):
+    if t is None:
+        return None
+    _want_shape(t, (N,), name)
+    if t.dtype != kind:
+        raise TypeError(f"{name} must be {kind} as C is")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise _elsewhere(name, t.get_device(), dev)
+    return t.data_ptr()
+
+
+def iris_fp8_mm_act(C, A: Fp8, B: Fp8, act="none", bias=None, z=None, residual=None, alpha: float = 1.0,
+                    dropout: Optional[Dropout] = None, q: Optional[Fp8] = None, dtype=None, workspace=None, stream=None) -> None:
+    """C = residual + alpha m act(A @ B^T + bias), C (M, N) float16, bfloat16 or float32;
+    q receives it in 8 bits, too or instead (C None: `dtype` then names the type of
+    bias, z and residual, float16 if they do not). z receives the value before the
+    activation. act: "none", "relu", "gelu", "gelu_tanh", "silu". Precision: as iris_fp8_mm."""
+    M, N, K, dev, code = _mm_operands(A, B, act)
+    shape = (M, N)
+    kind = dtype
+    for t in (C, z, residual, bias):
+        if t is not None and (kind is None or t is C):
+            kind = getattr(t, "dtype", None)
+    kind = torch.float16 if kind is None else kind
+    c_type = _FP8_TYPES.get(kind)
+    if c_type is None:
+        raise TypeError("C must be one of float16, bfloat16, float32")
+    ap, bp = _fp8(A, A.shape, "A", dev), _fp8(B, B.shape, "B", dev)
+    cp, ldc = _any_plain(C, "C", shape, kind, dev)
+    zp, ldz = _any_plain(z, "z", shape, kind, dev)
+    rp, ldr = _any_plain(residual, "residual", shape, kind, dev)
+    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
+    e = _Epilogue(code, alpha, _mm_vector(bias, "bias", N, kind, dev), zp, ldz, rp, ldr,
+                  None if q is None else _fp8(q, shape, "q", dev), _drop(dropout, dev))
+    st = _lib.iris_fp8_mm_act(cp, c_type, ldc, ap, bp, e, M, N, K, ws, wsb, _call_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def iris_fp8_mm_act_bwd(C, A: Fp8, B: Fp8, z, act, alpha: float = 1.0, dropout: Optional[Dropout] = None, dbias=None,
+                        workspace=None, stream=None) -> None:
+    """C = alpha m (A @ B^T) act'(z): the output's gradient A through the next product's
+    transposed weight B and back through the activation whose input was z (C's dtype);
+    dbias (N values of C's dtype) receives the column sums."""
+    M, N, K, dev, code = _mm_operands(A, B, act)
+    shape = (M, N)
+    if C is None or z is None:
+        raise ValueError(f"{'C' if C is None else 'z'} is required")
+    kind = getattr(C, "dtype", None)
+    c_type = _FP8_TYPES.get(kind)
+    if c_type is None:
+        raise TypeError("C must be one of float16, bfloat16, float32")
+    ap, bp = _fp8(A, A.shape, "A", dev), _fp8(B, B.shape, "B", dev)
+    cp, ldc = _any_plain(C, "C", shape, kind, dev)
+    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
+    st = _lib.iris_fp8_mm_act_bwd(cp, c_type, ldc,
+                                  _mm_vector(dbias, "dbias", N, kind, dev), ap, bp, *_any_plain(z, "z", shape, kind, dev), code,
+                                  alpha, _drop(dropout, dev), M, N, K, ws, wsb, _call_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def iris_fp8_mm_act_workspace_size(M: int, N: int, K: int, dtype=torch.float16, to8: bool = False, dbias: bool = False) -> int:
+    return int(_lib.iris_fp8_mm_act_workspace_size(M, N, K, _FP8_TYPES[dtype], int(to8), int(dbias)))
 
 
 # ------------------------------------------------------------------- helpers

@@ -1,0 +1,60 @@
+// Host-side view of the block norms: what their launches take.
+#pragma once
+
+#include "dropout.hpp"
+#include "fp8.hpp"
+
+namespace iris {
+
+constexpr int kNormMaxCols = 16384;
+constexpr int kNormWgs = kFp8Cus;   // workgroups of a backward pass at most: one a compute unit
+
+// Parameters of the norms: weights and biases are of y's type or (param32) fp32, the gate too (gate32).
+struct NormParams {
+  const void *pre_w, *pre_b, *post_w, *post_b, *gate;
+  int32_t ld_gate;
+  int32_t rows_per_gate;      // > 0
+  float eps, w_offset;
+  uint8_t layer, post, param32, gate32;
+  DropArgs drop;              // scale: alpha / (1 - p)
+};
+
+struct NormArgs {
+  const void *x, *y;          // y: NULL: none
+  void *r, *n;                // NULL: not wanted
+  Fp8Mat q;                   // codes NULL: not wanted
+  float* stats;               // rows x 4, or NULL
+  int32_t ldx, ldy, ldr, ldn;
+  int32_t rows, cols;
+  uint32_t first_row;         // of this launch's rows
+  NormParams p;
+};
+
+struct NormBwdArgs {
+  const void *dn, *dr, *r, *y;  // dn, dr, y: NULL: none
+  const float* stats;
+  void *dx, *dy;
+  float *dpre_w, *dpre_b, *dpost_w, *dpost_b, *dgate;  // NULL: not wanted
+  int32_t ld_dn, ld_dr, ld_r, ld_y, ld_dx, ld_dy;
+  int32_t rows, cols;
+  int32_t wg_rows, wgs;         // rows of a workgroup, workgroups
+  float* part;                  // their sums of columns
+  NormParams p;
+};
+
+// Workgroups share the rows in equal, contiguous shares, in steps of the rows that a
+// workgroup works on at a time.
+struct NormBwdPlan {
+  int wgs, wg_rows;
+  size_t ws_bytes;
+};
+NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols);
+
+// by the type of y (T), the stream's (x, r: fp32 or T) and whether all rows are whole and aligned
+template <class T>
+hipError_t launch_norm(const NormArgs& a, bool stream32, bool whole, hipStream_t s);
+template <class T>
+hipError_t launch_norm_bwd(const NormBwdArgs& a, bool stream32, bool whole, hipStream_t s);
+hipError_t launch_norm_join(const NormBwdArgs& a, hipStream_t s);
+
+}  // namespace iris

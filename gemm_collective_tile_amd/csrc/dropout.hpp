@@ -1,0 +1,125 @@
+// Dropout with a mask that is computed and never stored.
+//
+// Value (i, j) of a matrix is dropped by a 16-bit number u(i, j) of its own: half
+// j % 8 (the low half of a word first) of Philox4x32-10 (Salmon, Moraes, Dror, Shaw:
+// Parallel random numbers: as easy as 1, 2, 3; SC 2011) at counter
+// (j / 8, i, offset low, offset high) and key (seed low, seed high). It is kept if
+// u >= t, t = 65536 p rounded, and then divided by 1 - t / 65536. The mask goes by
+// the value's place alone: any kernel, split or pitch gives the same one, so what one
+// operator dropped in a forward pass another drops in the backward pass.
+//
+// 16 bits a value, so that a thread's 8 values of a row take one call: p is held to
+// 2^-17, and a kept value's factor is exact for the p that is held. A call is 20
+// multiplications of 32 x 32 into 64 bits.
+#pragma once
+
+#include "fp8_common.hpp"
+
+namespace iris {
+
+struct DropArgs {
+  uint64_t seed, offset;
+  const uint64_t* offset_at;   // device: added to offset, or NULL
+  uint32_t threshold;          // 0: nothing is dropped
+  float scale;                 // of what is kept
+};
+
+// The words of one launch's generator, read once a thread.
+struct Drop {
+  uint32_t k0, k1, c2, c3, threshold;
+  float scale;
+  __device__ __forceinline__ explicit Drop(const DropArgs& a) {
+    uint64_t offset = a.offset;
+    if (a.threshold != 0 && a.offset_at) offset += *a.offset_at;
+    k0 = (uint32_t)a.seed;
+    k1 = (uint32_t)(a.seed >> 32);
+    c2 = (uint32_t)offset;
+    c3 = (uint32_t)(offset >> 32);
+    threshold = a.threshold;
+    scale = a.scale;
+  }
+  // the 128 bits of columns 8 piece .. + 7 of a row
+  __device__ __forceinline__ u32x4 bits(uint32_t row, uint32_t piece) const {
+    uint32_t a = piece, b = row, c = c2, d = c3, x = k0, y = k1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const uint64_t m0 = (uint64_t)a * 0xD2511F53u, m1 = (uint64_t)c * 0xCD9E8D57u;
+      a = (uint32_t)(m1 >> 32) ^ b ^ x;
+      b = (uint32_t)m1;
+      c = (uint32_t)(m0 >> 32) ^ d ^ y;
+      d = (uint32_t)m0;
+      x += 0x9E3779B9u;
+      y += 0xBB67AE85u;
+    }
+    return u32x4{a, b, c, d};
+  }
+  // v: columns 8 piece .. + 7 of a row. What is dropped becomes 0, whatever it was.
+  __device__ __forceinline__ void apply(uint32_t row, uint32_t piece, float (&v)[8]) const {
+    if (threshold == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      return;
+    }
+    const u32x4 w = bits(row, piece);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
+      v[i] = u >= threshold ? v[i] * scale : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float apply(uint32_t row, uint32_t col, float v) const {
+    if (threshold == 0) return v * scale;
+    const u32x4 w = bits(row, col >> 3);
+    const uint32_t word = col & 4 ? (col & 2 ? w[3] : w[2]) : (col & 2 ? w[1] : w[0]);
+    return ((word >> (col & 1 ? 16 : 0)) & 0xffffu) >= threshold ? v * scale : 0.0f;
+  }
+};
+
+// 8 values of a row from column `col` on, at any alignment; those past the last column are 0.
+template <class T>
+__device__ __forceinline__ void load8(const T* row, int col, int cols, float (&v)[8]) {
+  T t[8];
+  if (col + 8 <= cols) {
+    __builtin_memcpy(t, row + col, sizeof t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = widen(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? widen(row[col + i]) : 0.0f;
+  }
+}
+// 8 values to a row, each rounded once, none past the last column. WHOLE: 16-byte
+// aligned, and all or none of the 8 are inside.
+template <bool WHOLE, class T>
+__device__ __forceinline__ void store8(T* row, int col, int cols, const float (&v)[8]) {
+  if (WHOLE ? col < cols : col + 8 <= cols) {
+    T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) narrow(v[i], t[i]);
+    if constexpr (WHOLE) {
+      u32x4 w[sizeof t / 16];
+      __builtin_memcpy(w, t, sizeof t);
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof t / 16); ++i) ((u32x4*)(row + col))[i] = w[i];
+    } else {
+      __builtin_memcpy(row + col, t, sizeof t);
+    }
+  } else if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < cols) narrow(v[i], row[col + i]);
+  }
+}
+
+struct DropoutArgs {
+  const void *x, *residual;   // residual: NULL: none
+  void* out;
+  int32_t ldx, ldr, ldo;
+  int32_t rows, cols;
+  int32_t type, vec;          // vec: rows start at multiples of 16 bytes
+  uint32_t first_row;         // of this launch's rows (set by the launch)
+  DropArgs drop;
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
+
+}  // namespace iris

@@ -399,6 +399,149 @@ int iris_fp8_swiglu_bwd(const iris_fp8_t* dgate, const iris_fp8_t* dup, const ir
                         int64_t ld_dh, const iris_fp8_t* gate_kept, const iris_fp8_t* up_kept,
                         int64_t rows, int64_t cols, void* stream);
 
+/*
+ * What lies between a block's products and its residual stream: dropout, the norms
+ * before and after the block, and the 8-bit product with an activation in its epilogue.
+ * They have no counterpart on the pages. Conventions are those of the 8-bit operators
+ * above: any number of rows and columns >= 0, any row pitch >= the columns (up to 2^22),
+ * pointers aligned to their type (rows that start at multiples of 16 bytes are faster),
+ * no output may be another operand, everything is on the current device, every result
+ * is the same from call to call. Rows up to 2^30. All arithmetic is in 32 bits, each
+ * output is rounded once.
+ */
+
+/*
+ * Dropout with a mask that is not stored: it is computed from the place of a value in
+ * its matrix. Value (i, j) is dropped (becomes 0, whatever it holds) if u(i, j) < t, with
+ * t = 65536 p rounded to nearest even and u(i, j) a 16-bit number: half j % 8 (the low
+ * half of a word first) of Philox4x32-10 at counter (j / 8, i, offset low, offset high)
+ * and key (seed low, seed high); what is kept is multiplied by 1 / (1 - t / 65536).
+ * The operators below share this definition: the mask of one is the mask of another of
+ * the same size, seed and offset, and a backward pass passes the same struct.
+ *   p          in [0, 1), and 65536 p below 65535.5
+ *   offset_at  device, 8-byte aligned, or NULL: read by the kernel and added to offset
+ *              (modulo 2^64). A graph that is replayed takes new masks by way of it.
+ * A NULL iris_drop_t drops nothing. The struct is read before the call returns.
+ */
+typedef struct iris_drop {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_at;
+} iris_drop_t;
+
+/*
+ * out = residual + alpha m x, m the mask above (alpha times the kept value's factor is
+ * rounded to 32 bits once). residual may be NULL. All (rows, cols) of `type` (fp16, bf16
+ * or fp32). Its own backward pass with respect to x: the same call on out's gradient.
+ */
+int iris_dropout(void* out, int64_t ld_out, const void* x, int64_t ldx, const void* residual, int64_t ld_residual,
+                 int32_t type, float alpha, const iris_drop_t* drop, int64_t rows, int64_t cols, void* stream);
+
+#define IRIS_NORM_RMS 1   /* v / sqrt(mean(v^2) + eps) */
+#define IRIS_NORM_LAYER 2 /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */
+
+/*
+ * The norms around a block, row by row over the columns (at most 16384, beyond
+ * IRIS_ERR_UNSUPPORTED):
+ *   p = post ? norm(y) (post_w + w_offset) + post_b : y      the block's output y
+ *   r = x + alpha gate m p                                   the residual stream
+ *   n = norm(r) (pre_w + w_offset) + pre_b                   the next block's input
+ * A NULL weight counts as 1 (w_offset is not added to it), a NULL bias as 0, a NULL gate
+ * as 1. n is formed from r before r is rounded.
+ *   type         of y and n: fp16 or bf16
+ *   stream_type  of x and r: type or fp32
+ *   param_type   of weights and biases (cols values each), type or fp32
+ *   gate_type    of the gate, type or fp32: rows of cols values, ld_gate apart; row i of
+ *                the matrices takes gate row i / rows_per_gate (one gate for all:
+ *                rows_per_gate >= rows)
+ *   eps > 0; w_offset: 1 for weights that are stored as what they add to 1
+ */
+typedef struct iris_norm {
+  int32_t kind;
+  int32_t type, stream_type, param_type, gate_type;
+  int32_t post;
+  float eps, w_offset, alpha;
+  const void *pre_w, *pre_b, *post_w, *post_b;
+  const void* gate;
+  int64_t ld_gate, rows_per_gate;
+  const iris_drop_t* drop;
+} iris_norm_t;
+
+/*
+ * x required; y may be NULL (then n = norm(x): no r, post, gate or drop). Outputs, each
+ * NULL if not wanted, one at least: r; n; q, n in 8 bits (block 1); stats, rows x 4 fp32,
+ * 16-byte aligned: mean and 1 / sqrt(...) of y (zeros without post) and of r, for the
+ * backward pass (a mean is 0 for IRIS_NORM_RMS).
+ */
+int iris_block_norm(void* r, int64_t ld_r, void* n, int64_t ld_n, const iris_fp8_t* q, float* stats, const void* x,
+                    int64_t ld_x, const void* y, int64_t ld_y, const iris_norm_t* norm, int64_t rows, int64_t cols,
+                    void* stream);
+
+/*
+ * Its backward pass, at the given r, y and stats: dn is n's gradient, dr what reaches r
+ * from elsewhere; either may be NULL (0). Gradients, each NULL if not wanted: dx (which
+ * is all of r's), dy, and in 32 bits dpre_w, dpre_b, dpost_w, dpost_b (cols) and dgate
+ * (contiguous rows of cols, one for each gate row that the rows use). r is needed with dn,
+ * y with dy, dgate, dpost_w or dpost_b. dx, dr, r of stream_type; dy, dn, y of type.
+ * Sums over the rows run in 32 bits in an order that the sizes alone decide.
+ * workspace: at least iris_block_norm_bwd_workspace_size() bytes (at most 101 MB), 256-byte
+ * aligned, contents of no account, for one call at a time; NULL: the library's own, as
+ * with iris_fp8_mm (32 MiB, or a second one of 128 MiB for what needs more).
+ */
+int iris_block_norm_bwd(void* dx, int64_t ld_dx, void* dy, int64_t ld_dy, float* dpre_w, float* dpre_b, float* dpost_w,
+                        float* dpost_b, float* dgate, const void* dn, int64_t ld_dn, const void* dr, int64_t ld_dr,
+                        const void* r, int64_t ld_r, const void* y, int64_t ld_y, const float* stats,
+                        const iris_norm_t* norm, int64_t rows, int64_t cols, void* workspace, size_t workspace_bytes,
+                        void* stream);
+size_t iris_block_norm_bwd_workspace_size(int64_t rows, int64_t cols);
+
+#define IRIS_ACT_NONE 0
+#define IRIS_ACT_RELU 1
+#define IRIS_ACT_GELU 2      /* z Phi(z), Phi the normal distribution */
+#define IRIS_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define IRIS_ACT_SILU 4      /* z / (1 + exp(-z)) */
+
+/*
+ * The 8-bit product with an epilogue:
+ *   z = A @ B^T + bias,  C = residual + alpha m act(z)
+ * A (M, K) with block 1, B (N, K) with block 1 or 128, as for iris_fp8_mm, whose statement
+ * of precision by C's type holds here too. C, z and residual are (M, N) of c_type with row
+ * pitches of their own, bias N values of c_type; z, residual, bias may be NULL. z receives
+ * the value before the activation, for the backward pass. q: C in 8 bits too (block 1,
+ * from 32 bits), or instead of C (C NULL; c_type then is that of the others).
+ */
+typedef struct iris_epilogue {
+  int32_t act;
+  float alpha;
+  const void* bias;
+  void* z;
+  int64_t ld_z;
+  const void* residual;
+  int64_t ld_residual;
+  const iris_fp8_t* q;
+  const iris_drop_t* drop;
+} iris_epilogue_t;
+
+int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B,
+                    const iris_epilogue_t* epilogue, int64_t M, int64_t N, int64_t K, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * The product whose result goes back through an activation (not IRIS_ACT_NONE):
+ *   C = alpha m (A @ B^T) act'(z),  dbias[j] = sum over the rows i of C[i][j]
+ * A: the output's gradient, B: the transposed weight of the next product, z: what the
+ * forward pass kept (M, N; relu's slope is 0 at 0). dbias: N values of c_type, or NULL;
+ * summed in 32 bits before C's rounding.
+ */
+int iris_fp8_mm_act_bwd(void* C, int32_t c_type, int64_t ldc, void* dbias, const iris_fp8_t* A, const iris_fp8_t* B,
+                        const void* z, int64_t ld_z, int32_t act, float alpha, const iris_drop_t* drop, int64_t M,
+                        int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+/* Of either, with an 8-bit output (to8) or a bias gradient (dbias). A NULL workspace is the
+ * library's own (32 MiB, or a second one of 128 MiB), as with iris_fp8_mm; what needs more
+ * than that gives IRIS_ERR_WORKSPACE without a caller's. */
+size_t iris_fp8_mm_act_workspace_size(int64_t M, int64_t N, int64_t K, int32_t c_type, int32_t to8, int32_t dbias);
+
 /* Bytes of device workspace an op needs (0 on invalid arguments). The
  * workspace holds per-workgroup timestamps, then the queue counters (one
  * GEMM queue per XCD and the comm queue), the finished-workgroup and
