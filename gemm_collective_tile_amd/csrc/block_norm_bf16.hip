@@ -10,24 +10,30 @@ namespace {
 
 constexpr int kJoinGates = 16;
 
-// Adds the workgroups' sums, 16 of every 64 columns at a time. blockIdx.y: 0 to 3 the
-// parameters' gradients; from 4 on the gates' whose rows several workgroups share, each
-// by the workgroup that has its first row.
-__global__ __launch_bounds__(1024) void block_norm_join_kernel(NormBwdArgs a) {
+// Adds the workgroups' sums, 64 columns at a time, 16 waves a sixteenth of the workgroups
+// each with up to 16 loads under way. blockIdx.y: 0 to 3 the parameters' gradients; from
+// 4 on the gates' whose rows several workgroups share, each by the workgroup that has
+// its first row.
+__global__ __launch_bounds__(1024) void block_norm_join_kernel(NormBwdArgs a, FastDiv gate_rows) {
   __shared__ float sums[16][64];
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
   const int64_t pitch = (a.cols + 7) & ~7;
-  // rows [from, to) of `first` on, every step-th
-  const auto join = [&](const float* first, int n, int64_t step, float* out) {
+  // out = own + rows 0 .. n - 1 of `first` on, each step floats after the one before
+  const auto join = [&](const float* own, const float* first, int n, int64_t step, float* out) {
     float v = 0.0f;
     if (c < a.cols) {
-#pragma unroll 4
-      for (int i = part; i < n; i += 16) v += first[i * step + c];
+      for (int i = part; i < n; i += 256) {
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = i + 16 * k < n ? first[(i + 16 * k) * step + c] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v += x[k];
+      }
     }
     sums[part][threadIdx.x & 63] = v;
     __syncthreads();
     if (part == 0 && c < a.cols) {
-      v = 0.0f;
+      v = own ? own[c] : 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) v += sums[i][threadIdx.x & 63];
       out[c] = v;
@@ -40,30 +46,21 @@ __global__ __launch_bounds__(1024) void block_norm_join_kernel(NormBwdArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (k == (int)blockIdx.y) out = outs[k];
-    if (out && a.wgs > 1) join(a.part + (int64_t)blockIdx.y * a.wgs * pitch, a.wgs, pitch, out);
+    if (out) join(nullptr, a.part + (int64_t)blockIdx.y * a.wgs * pitch, a.wgs, pitch, out);
     return;
   }
-  const int64_t every = a.p.rows_per_gate;
+  const float* const gates = a.part + (int64_t)4 * a.wgs * pitch;
   for (int w = blockIdx.y - 4; w < a.wgs - 1; w += kJoinGates) {
-    const int64_t next = (int64_t)(w + 1) * a.wg_rows;       // the first row of the next workgroup
-    const int64_t g = (next - 1) / every, g0 = g * every, g1 = min(g0 + every, (int64_t)a.rows);
-    if (g1 <= next || g0 < next - a.wg_rows) continue;       // ends here, or began before
-    const int n = (int)((g1 - 1) / a.wg_rows) - w;           // further workgroups: their first share each
-    const float* const own = a.part + ((int64_t)4 * a.wgs + 2 * w + (g0 == next - a.wg_rows ? 0 : 1)) * pitch;
-    float v = 0.0f;
-    if (c < a.cols) {
-#pragma unroll 4
-      for (int i = part; i < n; i += 16) v += a.part[((int64_t)4 * a.wgs + 2 * (w + 1 + i)) * pitch + c];
+    const int next = (w + 1) * a.wg_rows;                    // the first row of the next workgroup
+    const uint32_t g = gate_rows.div(next - 1);
+    const int64_t g0 = (int64_t)g * a.p.rows_per_gate;
+    const int g1 = (int)min(g0 + a.p.rows_per_gate, (int64_t)a.rows);
+    if (g1 > next && g0 >= next - a.wg_rows) {               // goes on there, and begins here
+      const int n = (g1 - 1) / a.wg_rows - w;                // further workgroups: their first share each
+      join(gates + (2 * w + (g0 == next - a.wg_rows ? 0 : 1)) * pitch, gates + 2 * (w + 1) * pitch, n, 2 * pitch,
+           a.dgate + (int64_t)g * a.cols);
     }
-    sums[part][threadIdx.x & 63] = v;
-    __syncthreads();
-    if (part == 0 && c < a.cols) {
-      v = own[c];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v += sums[i][threadIdx.x & 63];
-      a.dgate[g * a.cols + c] = v;
-    }
-    __syncthreads();
+    if (a.p.rows_per_gate >= a.rows) break;                  // one gate: the first workgroup's
   }
 }
 
@@ -84,8 +81,9 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
 
 hipError_t launch_norm_join(const NormBwdArgs& a, hipStream_t s) {
   if (a.wgs <= 1) return hipSuccess;
-  const dim3 grid((a.cols + 63) / 64, a.dgate ? 4 + kJoinGates : 4);
-  hipLaunchKernelGGL(block_norm_join_kernel, grid, dim3(1024), 0, s, a);
+  const int gates = !a.dgate ? 0 : a.p.rows_per_gate >= a.rows ? 1 : kJoinGates;
+  hipLaunchKernelGGL(block_norm_join_kernel, dim3((a.cols + 63) / 64, 4 + gates), dim3(1024), 0, s, a,
+                     FastDiv::make((uint32_t)a.p.rows_per_gate));
   return hipGetLastError();
 }
 

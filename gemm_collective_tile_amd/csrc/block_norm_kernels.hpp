@@ -211,7 +211,7 @@ template <class T, class X, int W, int P, bool WHOLE>
 __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols, FastDiv gate_rows) {
   constexpr int RG = 16 / W, WIDE = W * 512 * P;
   __shared__ float slots[2][2][RG][2 * W];   // by turns, so that a row's sums are read before the next row's but one are written
-  __shared__ __align__(16) float comb[RG > 1 ? RG * WIDE : 4];
+  __shared__ __align__(16) float comb[RG > 1 ? 4 * RG * WIDE : 4];   // 128 KB: a workgroup has the CU to itself by its registers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = wave / W, w = wave % W;
   const int first = blockIdx.x * a.wg_rows, last = min(first + a.wg_rows, a.rows);
@@ -220,25 +220,42 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
 #pragma unroll
   for (int j = 0; j < P; ++j) col[j] = 8 * ((j * W + w) * 64 + lane);
 
-  // sums of the row groups' columns, to one row of floats
-  const auto put_sums = [&](const float (&s)[P][8], float* to) {
+  // sums of the row groups' columns, each to one row of floats (or nowhere: NULL), N at a time
+  const auto put_sums = [&](auto n_of, const float (*const (&s)[4])[8], float* const (&to)[4]) {
+    constexpr int N = decltype(n_of)::value;
     if constexpr (RG == 1) {
 #pragma unroll
-      for (int j = 0; j < P; ++j) store8<false>(to, col[j], a.cols, s[j]);
+      for (int k = 0; k < N; ++k) {
+        if (!to[k]) continue;
+#pragma unroll
+        for (int j = 0; j < P; ++j) store8<false>(to[k], col[j], a.cols, s[k][j]);
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < P; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *(f32x4*)(comb + sub * WIDE + col[j] + 4 * h) = f32x4{s[j][4 * h], s[j][4 * h + 1], s[j][4 * h + 2], s[j][4 * h + 3]};
       __syncthreads();
-      for (int c = threadIdx.x; c < a.cols; c += 1024) {
-        float v = 0.0f;
 #pragma unroll
-        for (int g = 0; g < RG; ++g) v += comb[g * WIDE + c];
-        to[c] = v;
+      for (int k = 0; k < N; ++k) {
+        if (!to[k]) continue;
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *(f32x4*)(comb + (k * RG + sub) * WIDE + col[j] + 4 * h) =
+                f32x4{s[k][j][4 * h], s[k][j][4 * h + 1], s[k][j][4 * h + 2], s[k][j][4 * h + 3]};
       }
       __syncthreads();
+      for (int c = 4 * threadIdx.x; c < a.cols; c += 4096) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (!to[k]) continue;
+          f32x4 v = *(const f32x4*)(comb + k * RG * WIDE + c);
+#pragma unroll
+          for (int g = 1; g < RG; ++g) v += *(const f32x4*)(comb + (k * RG + g) * WIDE + c);
+          if (c + 4 <= a.cols)
+            __builtin_memcpy(to[k] + c, &v, 16);
+          else
+            for (int e = 0; c + e < a.cols; ++e) to[k][c + e] = v[e];
+        }
+      }
     }
   };
 
@@ -349,8 +366,9 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
     }
     if (a.dgate) {
       const bool here = g0 >= first && (g1 <= last || last == a.rows);
-      put_sums(s_gate, here ? a.dgate + (int64_t)group * a.cols
-                            : a.part + ((int64_t)4 * a.wgs + 2 * blockIdx.x + (row0 == first ? 0 : 1)) * pitch);
+      float* const to = here ? a.dgate + (int64_t)group * a.cols
+                             : a.part + ((int64_t)4 * a.wgs + 2 * blockIdx.x + (row0 == first ? 0 : 1)) * pitch;
+      put_sums(std::integral_constant<int, 1>{}, {s_gate, nullptr, nullptr, nullptr}, {to, nullptr, nullptr, nullptr});
 #pragma unroll
       for (int j = 0; j < P; ++j)
 #pragma unroll
@@ -358,11 +376,12 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
     }
     row0 = end;
   }
-  float* const part = a.part + (int64_t)blockIdx.x * pitch;
-  if (a.dpre_w) put_sums(s_pre_w, a.wgs == 1 ? a.dpre_w : part);
-  if (a.dpre_b) put_sums(s_pre_b, a.wgs == 1 ? a.dpre_b : part + a.wgs * pitch);
-  if (a.dpost_w) put_sums(s_post_w, a.wgs == 1 ? a.dpost_w : part + 2 * a.wgs * pitch);
-  if (a.dpost_b) put_sums(s_post_b, a.wgs == 1 ? a.dpost_b : part + 3 * a.wgs * pitch);
+  float* const outs[4] = {a.dpre_w, a.dpre_b, a.dpost_w, a.dpost_b};
+  float* to[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    to[k] = !outs[k] || a.wgs == 1 ? outs[k] : a.part + ((int64_t)k * a.wgs + blockIdx.x) * pitch;
+  put_sums(std::integral_constant<int, 4>{}, {s_pre_w, s_pre_b, s_post_w, s_post_b}, {to[0], to[1], to[2], to[3]});
 }
 
 // launch(waves of a row, pieces of a lane)

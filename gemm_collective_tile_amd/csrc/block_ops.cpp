@@ -345,6 +345,8 @@ int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, c
   a.ldr = (int32_t)e->ld_residual;
   a.q = mat(e->q);
   a.drop = drop;
+  a.whole = N % 8 == 0 && rows16_or_none(C, ldc, c_type, M) && rows16_or_none(e->z, e->ld_z, c_type, M) &&
+            rows16_or_none(e->residual, e->ld_residual, c_type, M);
   return run_mm(a, plan, nullptr, workspace, stream, "iris_fp8_mm_act");
 } catch (const std::exception& error) {
   return caught(error);
@@ -372,6 +374,7 @@ int iris_fp8_mm_act_bwd(void* C, int32_t c_type, int64_t ldc, void* dbias, const
   a.z = const_cast<void*>(z);
   a.ldz = (int32_t)ld_z;
   a.drop = d;
+  a.whole = N % 8 == 0 && rows16_or_none(C, ldc, c_type, M) && rows16_or_none(z, ld_z, c_type, M);
   return run_mm(a, plan, dbias, workspace, stream, "iris_fp8_mm_act_bwd");
 } catch (const std::exception& e) {
   return caught(e);

@@ -38,15 +38,18 @@ struct Drop {
     threshold = a.threshold;
     scale = a.scale;
   }
+  static __device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+    return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);   // a ^ b ^ c, by its truth table
+  }
   // the 128 bits of columns 8 piece .. + 7 of a row
   __device__ __forceinline__ u32x4 bits(uint32_t row, uint32_t piece) const {
     uint32_t a = piece, b = row, c = c2, d = c3, x = k0, y = k1;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
       const uint64_t m0 = (uint64_t)a * 0xD2511F53u, m1 = (uint64_t)c * 0xCD9E8D57u;
-      a = (uint32_t)(m1 >> 32) ^ b ^ x;
+      a = xor3((uint32_t)(m1 >> 32), b, x);
       b = (uint32_t)m1;
-      c = (uint32_t)(m0 >> 32) ^ d ^ y;
+      c = xor3((uint32_t)(m0 >> 32), d, y);
       d = (uint32_t)m0;
       x += 0x9E3779B9u;
       y += 0xBB67AE85u;
@@ -56,6 +59,7 @@ struct Drop {
   // v: columns 8 piece .. + 7 of a row. What is dropped becomes 0, whatever it was.
   __device__ __forceinline__ void apply(uint32_t row, uint32_t piece, float (&v)[8]) const {
     if (threshold == 0) {
+      if (scale == 1.0f) return;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= scale;
       return;

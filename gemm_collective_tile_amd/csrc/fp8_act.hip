@@ -27,45 +27,117 @@ __device__ __forceinline__ float same_columns_sum(float v) {
   return __builtin_bit_cast(float, (uint32_t)y[0]) + __builtin_bit_cast(float, (uint32_t)y[1]);
 }
 
-// 8 sums of row m, columns n .. n + 7, through the epilogue; on: they lie inside C. All
-// 16 lanes of a block of 128 columns call it together where q is wanted.
-template <class OUT>
-__device__ __forceinline__ void finish8(const Fp8ActArgs& a, const Drop& drop, int m, int n, bool on, const float (&bias)[8],
-                                        float (&v)[8], float (&sums)[8]) {
-  const int N = a.g.N;
-  if (on) {
-    if (a.backward) {
-      float z[8];
-      load8((const OUT*)a.z + (int64_t)m * a.ldz, n, N, z);
-      times_slope(a.act, z, v);
-      drop.apply((uint32_t)m, (uint32_t)n >> 3, v);
-      if (a.dbias_part) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sums[i] += v[i];
-      }
+// 8 values as they lie in memory
+template <class T>
+struct Raw8 {
+  static constexpr int WORDS = 2 * (int)sizeof(T);
+  uint32_t w[WORDS];
+  // of a row from column `col` on, at any alignment; those past the last column are 0
+  __device__ __forceinline__ void load(const T* row, int col, int cols) {
+    if (col + 8 <= cols) {
+      __builtin_memcpy(w, row + col, sizeof w);
     } else {
+      T t[8] = {};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += bias[i];
-      if (a.z) store8<false>((OUT*)a.z + (int64_t)m * a.ldz, n, N, v);
-      activate(a.act, v);
-      drop.apply((uint32_t)m, (uint32_t)n >> 3, v);
-      if (a.residual) {
-        float r[8];
-        load8((const OUT*)a.residual + (int64_t)m * a.ldr, n, N, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-      }
+      for (int i = 0; i < 8; ++i)
+        if (col + i < cols) t[i] = row[col + i];
+      __builtin_memcpy(w, t, sizeof w);
     }
-    if (a.g.C) store8<false>((OUT*)a.g.C + (int64_t)m * a.g.ldc, n, N, v);
   }
-  if (a.q.codes) {
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    T t[8];
+    __builtin_memcpy(t, w, sizeof w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = on && n + i < N ? __builtin_canonicalizef(v[i]) : 0.0f;
-    const uint32_t s = scale_byte(group_max<16>(piece_amax(v)));
+    for (int i = 0; i < 8; ++i) v[i] = widen(t[i]);
+  }
+};
+// the matrix that an epilogue reads beside the sums: z, the residual or none
+template <bool BACKWARD, class OUT>
+struct Beside {
+  const OUT* at;
+  int ld;
+  __device__ __forceinline__ explicit Beside(const Fp8ActArgs& a)
+      : at((const OUT*)(BACKWARD ? a.z : a.residual)), ld(BACKWARD ? a.ldz : a.ldr) {}
+  __device__ __forceinline__ void load(int m, int n, int N, bool on, Raw8<OUT>& r) const {
+    if (at && on) r.load(at + (int64_t)m * ld, n, N);
+  }
+};
+
+// C and z written at any pitch and alignment, by those lanes whose piece lies inside
+template <class OUT>
+struct PutRagged {
+  static constexpr bool WHOLE = false;
+  const Fp8ActArgs& a;
+  int m, n;
+  bool on;
+  __device__ __forceinline__ void z(const float (&v)[8]) const {
+    if (on) store8<false>((OUT*)a.z + (int64_t)m * a.ldz, n, a.g.N, v);
+  }
+  __device__ __forceinline__ void c(const float (&v)[8]) const {
+    if (on) store8<false>((OUT*)a.g.C + (int64_t)m * a.g.ldc, n, a.g.N, v);
+  }
+};
+// whole, aligned pieces through buffers, which drop a lane's that is off: no branch
+// between them, so that the number of stores under way is known
+template <class OUT>
+struct PutWhole {
+  static constexpr bool WHOLE = true;
+  __amdgpu_buffer_rsrc_t c_rows, z_rows;
+  uint32_t c_at, z_at;   // bytes, or kOob
+  static __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t at, const float (&v)[8]) {
+    OUT t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) narrow(v[i], t[i]);
+    u32x4 w[sizeof t / 16];
+    __builtin_memcpy(w, t, sizeof t);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof t / 16); ++i) __builtin_amdgcn_raw_buffer_store_b128(w[i], r, at + 16 * i, 0, 0);
+  }
+  __device__ __forceinline__ void z(const float (&v)[8]) const { put(z_rows, z_at, v); }
+  __device__ __forceinline__ void c(const float (&v)[8]) const { put(c_rows, c_at, v); }
+};
+
+// 8 sums of row m, columns n .. n + 7, through the epilogue; on: they lie inside C. All
+// 16 lanes of a block of 128 columns call it together where q is wanted. `beside`: their
+// values of z (backward) or of the residual, in memory's form.
+template <bool BACKWARD, class OUT, class PUT>
+__device__ __forceinline__ void finish8(const Fp8ActArgs& a, const Drop& drop, int m, int n, bool on, const float (&bias)[8],
+                                        const Raw8<OUT>& beside, const PUT& put, float (&v)[8], float (&sums)[8]) {
+  const int N = a.g.N;
+  if constexpr (BACKWARD) {
+    float z[8];
+    beside.values(z);
+    times_slope(a.act, z, v);
+    drop.apply((uint32_t)m, (uint32_t)n >> 3, v);
+    if (a.dbias_part) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sums[i] += on ? v[i] : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += bias[i];
+    if (a.z) put.z(v);
+    activate(a.act, v);
+    drop.apply((uint32_t)m, (uint32_t)n >> 3, v);
+    if (a.residual) {
+      float r[8];
+      beside.values(r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+  }
+  if (BACKWARD || a.g.C) put.c(v);
+  if (!BACKWARD && a.q.codes) {
+    // what lies outside has no say in the scale, and its codes go nowhere
+    if constexpr (!PUT::WHOLE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = n + i < N ? v[i] : 0.0f;
+    }
+    const uint32_t s = scale_byte(group_max<16>(piece_amax(v) & on_mask(on)));
     uint32_t w[2];
     encode_piece(v, scale_value(s), w);
     if (on) {
-      store_codes<false, 8>(a.q.codes + (int64_t)m * a.q.ld, 0, n, N, w);
+      store_codes<PUT::WHOLE, 8>(a.q.codes + (int64_t)m * a.q.ld, 0, n, N, w);
       if (n % kFp8Block == 0) a.q.scales[(int64_t)m * a.q.lds + n / kFp8Block] = (uint8_t)s;
     }
   }
@@ -78,7 +150,42 @@ __device__ __forceinline__ void load_bias8(const Fp8ActArgs& a, int n, float (&b
   if (a.g.bias && n < a.g.N) load8((const OUT*)a.g.bias, n, a.g.N, b);
 }
 
-template <class OUT, int BM, int BN>
+// between the writes and the reads of a strip: of the workgroup's waves where they share
+// it, else of the wave's lanes
+template <bool SHARED>
+__device__ __forceinline__ void strip_barrier() {
+  if constexpr (SHARED) {
+    __syncthreads();
+  } else {
+    __builtin_amdgcn_wave_barrier();
+    wait_lds();
+  }
+}
+
+// until at most n of this wave's vector memory operations are under way
+__device__ __forceinline__ void wait_vmem(int n) {
+  switch (n) {
+    case 0: wait_loads<0>(); break;
+    case 2: wait_loads<2>(); break;
+    case 4: wait_loads<4>(); break;
+    case 6: wait_loads<6>(); break;
+    case 8: wait_loads<8>(); break;
+    case 12: wait_loads<12>(); break;
+    case 16: wait_loads<16>(); break;
+    default: wait_loads<0>(); break;
+  }
+}
+
+// WHOLE: N is a multiple of 8 and all rows of C, z and the residual start at multiples of
+// 16 bytes.
+//
+// What is read beside the sums (z or the residual) is fetched strips ahead of its use.
+// Vector memory operations are counted in their order, loads and stores alike: a load
+// that is waited for without knowing the number of stores behind it waits for these too,
+// a few us under load, for every strip. So with WHOLE the loads go into LDS unseen by
+// the compiler, and the wait counts the stores of C that are surely behind them. Else
+// they wait in registers, and are waited for as the compiler does it.
+template <class OUT, int BM, int BN, bool WHOLE, bool BACKWARD>
 __global__ __launch_bounds__(256) void fp8_mm_act_kernel(Fp8ActArgs a) {
   using T = Tile<BM, BN>;
   constexpr bool EXACT = sizeof(OUT) == 4;
@@ -87,41 +194,131 @@ __global__ __launch_bounds__(256) void fp8_mm_act_kernel(Fp8ActArgs a) {
   int pm, pn;
   if (!pick_tile<OUT, T>(a.g, pm, pn)) return;
   const int m0 = pm * BM, n0 = pn * BN, r32 = lane & 31;
-  f32x16 acc[T::FM][T::FN];
-  tile_sums<EXACT, T>(a.g, lds, pm, pn, acc, [] {});
 
   // A strip of 32 rows is as wide as a block of 128 (64 where the tile is): a wave's own
   // at 256 columns, else what two waves side by side hold, who then take 16 of its rows each.
   constexpr bool SHARED = BN <= 128;
   constexpr int SW = BN < 128 ? BN : 128, PITCH = SW + 4, LPR = SW / 8, RPI = 64 / LPR;
-  constexpr int STRIP = 32 * PITCH, STRIPS = SHARED ? 2 : 4, ROWS = SHARED ? 16 : 32;
-  static_assert(STRIPS * STRIP * 4 <= T::LDS && 4 * SW * 4 <= T::LDS, "the turn does not fit");
+  constexpr int STRIP = 32 * PITCH, STRIPS = SHARED ? 2 : 4, ROWS = SHARED ? 16 : 32, PASSES = ROWS / RPI;
+  constexpr int PIECES = sizeof(Raw8<OUT>) / 16, RAW_AT = STRIPS * STRIP * 4, RAW = 4 * PASSES * PIECES * 1024;
+  constexpr int AHEAD = T::FM > 1 && WHOLE && RAW_AT + 2 * RAW <= T::LDS ? 2 : 1;   // strips that are fetched
+  static_assert(RAW_AT + AHEAD * RAW <= T::LDS && 4 * SW * 4 <= T::LDS, "the turn does not fit");
   const int right = wave & 1, half = wave >> 1;
+  const int c = 8 * (lane % LPR), nw = n0 + (SHARED ? 0 : right * T::WN), n = nw + c;
+  f32x16 acc[T::FM][T::FN];
+  Raw8<OUT> bias_raw = {};
+  tile_sums<EXACT, T>(a.g, lds, pm, pn, acc, [&] {
+    if (!BACKWARD && a.g.bias && n < a.g.N) bias_raw.load((const OUT*)a.g.bias, n, a.g.N);
+  });
+
   float* const strip = (float*)lds + (SHARED ? half : wave) * STRIP;
-  const int c = 8 * (lane % LPR), n = n0 + (SHARED ? 0 : right * T::WN) + c;
+  // 16-byte pieces, a lane's side by side with the other lanes'
+  const int raw_wave = RAW_AT + wave * PASSES * PIECES * 1024;
+  const int lane_row = (SHARED ? right * 16 : 0) + lane / LPR;   // of a strip, in the first pass
   const Drop drop(a.drop);
+  const Beside<BACKWARD, OUT> beside(a);
   float bias[8], sums[8] = {};
-  load_bias8<OUT>(a, n, bias);
+  bias_raw.values(bias);
+  const auto first_row = [&](int i) { return m0 + half * T::WM + 32 * i; };   // of strip i
+
+  Raw8<OUT> raw[WHOLE ? 1 : PASSES];
+  const uint32_t lds_raw = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + raw_wave);
+  const auto fetch = [&](int i) {
+    if constexpr (WHOLE) {
+      // rows and columns past the end read inside again: their outputs are dropped
+      const int top = min(first_row(i), a.g.M - 1);
+      const i32x4 rsrc = buffer_words(beside.at + (int64_t)top * beside.ld + min(nw, a.g.N - 8));
+      const uint32_t col = nw < a.g.N - 8 ? (uint32_t)min(c, a.g.N - 8 - nw) : 0;
 #pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const uint32_t row = (uint32_t)min(lane_row + RPI * p, a.g.M - 1 - top);
+#pragma unroll
+        for (int h = 0; h < PIECES; ++h)
+          buffer_to_lds(rsrc, (row * (uint32_t)beside.ld + col) * (uint32_t)sizeof(OUT) + 16 * h, 0,
+                        lds_raw + (i % AHEAD) * RAW + (p * PIECES + h) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int m = first_row(i) + lane_row + RPI * p;
+        beside.load(m, n, a.g.N, m < a.g.M && n < a.g.N, raw[p]);
+      }
+    }
+  };
+  // stores that every strip surely has, whatever else is stored
+  const int stores = WHOLE && a.g.C ? PASSES * PIECES : 0;
+  if (beside.at) {
+    fetch(0);
+    if constexpr (AHEAD == 2) fetch(1);
+  }
+  // The passes over a strip stand in the code once: four times they exceed the instruction
+  // cache (76 KB; 8192 x 11008 x 4096 through relu backwards 417 us, so 393).
+#pragma unroll 1
   for (int i = 0; i < T::FM; ++i) {
     float* const to = strip + r32 * PITCH + (SHARED ? right * T::WN : 0) + 4 * (lane >> 5);
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j)
+    for (int k = 0; k < T::FM; ++k) {
+      if (k != i) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(f32x4*)(to + 32 * j + 8 * q) = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    __syncthreads();
-#pragma unroll 1
-    for (int r = 0; r < ROWS; r += RPI) {
-      const int row = (SHARED ? right * 16 : 0) + r + lane / LPR, m = m0 + half * T::WM + 32 * i + row;
-      float v[8];
-      __builtin_memcpy(v, strip + row * PITCH + c, sizeof v);
-      finish8<OUT>(a, drop, m, n, m < a.g.M && n < a.g.N, bias, v, sums);
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(f32x4*)(to + 32 * j + 8 * q) = f32x4{acc[k][j][4 * q], acc[k][j][4 * q + 1], acc[k][j][4 * q + 2], acc[k][j][4 * q + 3]};
     }
-    __syncthreads();
+    char* const raw_at = lds + raw_wave + (i % AHEAD) * RAW + 16 * lane;
+    if (beside.at) {
+      if constexpr (WHOLE) {
+        // behind strip i's loads: the stores of strip i - 1 if they went out ahead of it, and the next strip's loads
+        wait_vmem((i >= AHEAD - 1 && i > 0 && AHEAD == 2 ? stores : 0) + (AHEAD == 2 && i + 1 < T::FM ? PASSES * PIECES : 0));
+      } else {
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+          for (int h = 0; h < PIECES; ++h) __builtin_memcpy(raw_at + (p * PIECES + h) * 1024, raw[p].w + 4 * h, 16);
+        if (i + 1 < T::FM) fetch(i + 1);
+      }
+    }
+    strip_barrier<SHARED>();
+    const int top = first_row(i);
+    PutWhole<OUT> whole;
+    if constexpr (WHOLE) {
+      whole.c_rows = make_rsrc((const OUT*)a.g.C + (int64_t)top * a.g.ldc + nw, 0x7fffffffu);
+      whole.z_rows = make_rsrc((const OUT*)a.z + (int64_t)top * a.ldz + nw, 0x7fffffffu);
+    }
+    // the next pass's values are on their way while this one's go through the epilogue
+    float next[8];
+    Raw8<OUT> next_raw;
+    const auto read = [&](int p) {
+      __builtin_memcpy(next, strip + (lane_row + RPI * p) * PITCH + c, sizeof next);
+      if (beside.at) {
+#pragma unroll
+        for (int h = 0; h < PIECES; ++h) __builtin_memcpy(next_raw.w + 4 * h, raw_at + (p * PIECES + h) * 1024, 16);
+      }
+    };
+    read(0);
+#pragma unroll 4
+    for (int p = 0; p < PASSES; ++p) {
+      const int row = lane_row + RPI * p, m = top + row;
+      const bool on = m < a.g.M && n < a.g.N;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = next[e];
+      const Raw8<OUT> here = next_raw;
+      read(min(p + 1, PASSES - 1));
+      if constexpr (WHOLE) {
+        whole.c_at = on ? ((uint32_t)row * (uint32_t)a.g.ldc + c) * (uint32_t)sizeof(OUT) : kOob;
+        whole.z_at = on ? ((uint32_t)row * (uint32_t)a.ldz + c) * (uint32_t)sizeof(OUT) : kOob;
+        finish8<BACKWARD, OUT>(a, drop, m, n, on, bias, here, whole, v, sums);
+      } else {
+        finish8<BACKWARD, OUT>(a, drop, m, n, on, bias, here, PutRagged<OUT>{a, m, n, on}, v, sums);
+      }
+    }
+    strip_barrier<SHARED>();
+    if (WHOLE && beside.at && i + AHEAD < T::FM) fetch(i + AHEAD);
   }
   if (!a.dbias_part) return;
   // the tile's column sums: over the lanes, then over the waves, in order
+  __syncthreads();
   float* const red = (float*)lds;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sums[e] = same_columns_sum<LPR>(sums[e]);
@@ -168,12 +365,13 @@ struct PutSum {
 
 // Sums in the workspace (those of a.g.splits splits, added in order) through the epilogue.
 // A workgroup takes a block of 128 columns, `rows` rows of it, 16 at a time.
-template <class OUT>
+template <class OUT, bool BACKWARD>
 __global__ __launch_bounds__(256) void fp8_mm_act_join_kernel(Fp8ActArgs a, const float* part, int64_t ldp, int rows) {
   __shared__ float red[4][128];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = blockIdx.x * 128 + 8 * (lane & 15), from = blockIdx.y * rows, to = min(from + rows, a.g.M);
   const Drop drop(a.drop);
+  const Beside<BACKWARD, OUT> beside(a);
   float bias[8], sums[8] = {};
   load_bias8<OUT>(a, n, bias);
   for (int base = from; base < to; base += 16) {
@@ -192,7 +390,9 @@ __global__ __launch_bounds__(256) void fp8_mm_act_join_kernel(Fp8ActArgs a, cons
         }
       }
     }
-    finish8<OUT>(a, drop, m, n, on, bias, v, sums);
+    Raw8<OUT> here;
+    beside.load(m, n, a.g.N, on, here);
+    finish8<BACKWARD, OUT>(a, drop, m, n, on, bias, here, PutRagged<OUT>{a, m, n, on}, v, sums);
   }
   if (!a.dbias_part) return;
 #pragma unroll
@@ -206,24 +406,24 @@ __global__ __launch_bounds__(256) void fp8_mm_act_join_kernel(Fp8ActArgs a, cons
   }
 }
 
-// dbias = the partial sums, 16 of every 64 columns at a time
+// dbias = the partial sums, added in order: a wave a quarter of them, 16 loads under way
 template <class OUT>
-__global__ __launch_bounds__(1024) void fp8_dbias_kernel(const float* part, int parts, int64_t ldp, int N, OUT* dbias) {
-  __shared__ float red[16][64];
+__global__ __launch_bounds__(256) void fp8_dbias_kernel(const float* part, int parts, int64_t ldp, int N, OUT* dbias) {
+  __shared__ float red[4][64];
   const int l = threadIdx.x & 63, c = blockIdx.x * 64 + l, g = threadIdx.x >> 6;
   float v = 0.0f;
   if (c < N) {
-#pragma unroll 4
-    for (int i = g; i < parts; i += 16) v += part[i * ldp + c];
+    for (int i = g; i < parts; i += 64) {
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = i + 4 * k < parts ? part[(i + 4 * k) * ldp + c] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += x[k];
+    }
   }
   red[g][l] = v;
   __syncthreads();
-  if (g == 0 && c < N) {
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v += red[i][l];
-    narrow(v, dbias[c]);
-  }
+  if (g == 0 && c < N) narrow((red[0][l] + red[1][l]) + (red[2][l] + red[3][l]), dbias[c]);
 }
 
 constexpr int kJoinRows = 16, kJoinRowsSummed = 64;   // without and with column sums
@@ -232,13 +432,22 @@ template <class OUT, int BM, int BN>
 hipError_t launch_tiles(const Fp8ActArgs& a, hipStream_t s) {
   const int64_t tiles = ((int64_t)a.g.M + BM - 1) / BM * (((int64_t)a.g.N + BN - 1) / BN);
   const int64_t round = kPatch * kXcds;
-  hipLaunchKernelGGL((fp8_mm_act_kernel<OUT, BM, BN>), dim3((uint32_t)((tiles + round - 1) / round * round)), dim3(256), 0, s, a);
+  const dim3 grid((uint32_t)((tiles + round - 1) / round * round));
+  const auto launch = [&](auto whole, auto backward) {
+    hipLaunchKernelGGL((fp8_mm_act_kernel<OUT, BM, BN, decltype(whole)::value, decltype(backward)::value>), grid, dim3(256), 0,
+                       s, a);
+  };
+  using std::false_type, std::true_type;
+  if (a.backward)
+    a.whole ? launch(true_type{}, true_type{}) : launch(false_type{}, true_type{});
+  else
+    a.whole ? launch(true_type{}, false_type{}) : launch(false_type{}, false_type{});
   return hipGetLastError();
 }
 
 template <class OUT>
 hipError_t join_dbias(const float* part, int parts, int64_t ldp, int N, OUT* dbias, hipStream_t s) {
-  hipLaunchKernelGGL((fp8_dbias_kernel<OUT>), dim3((N + 63) / 64), dim3(1024), 0, s, part, parts, ldp, N, dbias);
+  hipLaunchKernelGGL((fp8_dbias_kernel<OUT>), dim3((N + 63) / 64), dim3(256), 0, s, part, parts, ldp, N, dbias);
   return hipGetLastError();
 }
 
@@ -257,8 +466,11 @@ hipError_t run(const Fp8ActArgs& args, const Fp8ActPlan& plan, OUT* dbias, void*
     if (e != hipSuccess) return e;
     a.g.splits = plan.mm.splits;
     const int rows = plan.parts > 0 ? kJoinRowsSummed : kJoinRows;
-    hipLaunchKernelGGL((fp8_mm_act_join_kernel<OUT>), dim3((a.g.N + 127) / 128, (a.g.M + rows - 1) / rows), dim3(256), 0, s, a,
-                       (const float*)ws, ldp, rows);
+    const dim3 grid((a.g.N + 127) / 128, (a.g.M + rows - 1) / rows);
+    if (a.backward)
+      hipLaunchKernelGGL((fp8_mm_act_join_kernel<OUT, true>), grid, dim3(256), 0, s, a, (const float*)ws, ldp, rows);
+    else
+      hipLaunchKernelGGL((fp8_mm_act_join_kernel<OUT, false>), grid, dim3(256), 0, s, a, (const float*)ws, ldp, rows);
     e = hipGetLastError();
   } else if (plan.mm.bm == 0) {
     e = launch_few<PutAct<OUT>, sizeof(OUT) == 4>(a.g, PutAct<OUT>{a.z, a.g.C, a.g.bias, a.residual, a.ldz, a.g.ldc, a.ldr, a.act,

@@ -20,6 +20,7 @@ struct Fp8ActArgs {
   float* dbias_part;      // sums of a tile's (or a join's) rows, `ldp` floats each, or NULL
   int32_t ldz, ldr, ldp;
   uint8_t act, backward;
+  uint8_t whole;          // N is a multiple of 8, rows of C, z and residual start at multiples of 16 bytes
   DropArgs drop;          // scale: alpha / (1 - p)
 };
 

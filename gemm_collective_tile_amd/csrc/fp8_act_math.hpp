@@ -34,13 +34,17 @@ __device__ __forceinline__ float normal_cdf(float x, float& e) {
 // finite as z^2 leaves 32 bits.
 constexpr float kGeluU = 1.5957691216057308f, kGelu3 = 0.044715f;
 __device__ __forceinline__ float gelu_square(float z) { return __builtin_fminf(z * z, 0x1p100f); }
+__device__ __forceinline__ float gelu_sigmoid(float z, float z2) {   // s(u), the constants and log2 e multiplied beforehand
+  constexpr float c = -1.4426950408889634f * kGeluU;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c * kGelu3, z2, c)));
+}
 
 template <int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
   switch (act) {
     case ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] > 0.0f || v[i] != v[i] ? v[i] : 0.0f;   // NaN stays
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // NaN stays
       break;
     case ACT_GELU:
 #pragma unroll
@@ -51,7 +55,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
       break;
     case ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] *= sigmoid(kGeluU * v[i] * __builtin_fmaf(kGelu3, gelu_square(v[i]), 1.0f));
+      for (int i = 0; i < N; ++i) v[i] *= gelu_sigmoid(v[i], v[i] * v[i]);
       break;
     case ACT_SILU:
 #pragma unroll
@@ -67,7 +71,7 @@ __device__ __forceinline__ void times_slope(int act, const float (&z)[N], float 
   switch (act) {
     case ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = z[i] > 0.0f ? v[i] : (z[i] == z[i] ? 0.0f : z[i]);
+      for (int i = 0; i < N; ++i) v[i] = z[i] > 0.0f ? v[i] : 0.0f;
       break;
     case ACT_GELU:
 #pragma unroll
@@ -80,7 +84,7 @@ __device__ __forceinline__ void times_slope(int act, const float (&z)[N], float 
     case ACT_GELU_TANH:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float z2 = gelu_square(z[i]), s = sigmoid(kGeluU * z[i] * __builtin_fmaf(kGelu3, z2, 1.0f));
+        const float z2 = gelu_square(z[i]), s = gelu_sigmoid(z[i], z2);
         v[i] *= __builtin_fmaf(z[i] * s * (1.0f - s), kGeluU * __builtin_fmaf(3.0f * kGelu3, z2, 1.0f), s);
       }
       break;
