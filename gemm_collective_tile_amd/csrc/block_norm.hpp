@@ -7,7 +7,9 @@
 namespace iris {
 
 constexpr int kNormMaxCols = 16384;
-constexpr int kNormWgs = kFp8Cus;   // workgroups of a backward pass at most: one a compute unit
+// Waves of a backward workgroup whose rows W waves hold each. Registers allow 16 waves a
+// compute unit.
+constexpr int norm_bwd_waves(int W) { return W < 8 ? 8 : W; }
 
 // Parameters of the norms: weights and biases are of y's type or (param32) fp32, the gate too (gate32).
 struct NormParams {

@@ -20,20 +20,20 @@ __global__ __launch_bounds__(1024) void block_norm_join_kernel(NormBwdArgs a, Fa
   const int64_t pitch = (a.cols + 7) & ~7;
   // out = own + rows 0 .. n - 1 of `first` on, each step floats after the one before
   const auto join = [&](const float* own, const float* first, int n, int64_t step, float* out) {
+    const int cc = min(c, a.cols - 1);
+    const float before = own ? own[cc] : 0.0f;
     float v = 0.0f;
-    if (c < a.cols) {
-      for (int i = part; i < n; i += 256) {
-        float x[16];
+    for (int i = part; i < n; i += 256) {
+      float x[16];   // a row past the end reads the last one and drops it: no branch between the loads
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = i + 16 * k < n ? first[(i + 16 * k) * step + c] : 0.0f;
+      for (int k = 0; k < 16; ++k) x[k] = first[min(i + 16 * k, n - 1) * step + cc];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v += x[k];
-      }
+      for (int k = 0; k < 16; ++k) v += i + 16 * k < n ? x[k] : 0.0f;
     }
     sums[part][threadIdx.x & 63] = v;
     __syncthreads();
     if (part == 0 && c < a.cols) {
-      v = own ? own[c] : 0.0f;
+      v = before;
 #pragma unroll
       for (int i = 0; i < 16; ++i) v += sums[i][threadIdx.x & 63];
       out[c] = v;
@@ -70,8 +70,9 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
   int waves = 1;
   while (waves < 16 && 512 * waves < cols) waves *= 2;
   if (rows == 0) return {1, 0, 0};    // the parameters' gradients alone: zeros
-  const int64_t step = 16 / waves;    // rows that a workgroup works on at a time
-  const int64_t share = ((rows + kNormWgs - 1) / kNormWgs + step - 1) / step * step;
+  const int64_t step = norm_bwd_waves(waves) / waves;    // rows that a workgroup works on at a time
+  const int64_t most = kFp8Cus * (16 / norm_bwd_waves(waves));
+  const int64_t share = ((rows + most - 1) / most + step - 1) / step * step;
   NormBwdPlan p{};
   p.wg_rows = (int)share;
   p.wgs = (int)((rows + share - 1) / share);

@@ -63,9 +63,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slot, int w, int 
 template <class T, bool WHOLE>
 __device__ __forceinline__ void load_param(const void* p, bool f32, int col, int cols, float (&v)[8]) {
   if (f32)
-    load_piece<WHOLE>((const float*)p, 0, col, cols, true, false, v);
+    load8<WHOLE>((const float*)p, col, cols, v);
   else
-    load_piece<WHOLE>((const T*)p, 0, col, cols, true, false, v);
+    load8<WHOLE>((const T*)p, col, cols, v);
 }
 
 // values past the last column become 0
@@ -127,13 +127,13 @@ __device__ __forceinline__ void affine(const void* w, const void* b, bool f32, f
 }
 
 template <class T, class X, int W, int P, bool WHOLE>
-__global__ __launch_bounds__(W < 4 ? 256 : W * 64) void block_norm_kernel(NormArgs a, float inv_cols, FastDiv gate_rows) {
+__global__ __launch_bounds__(W < 4 ? 256 : W * 64, P == 1 ? 8 : 4) void block_norm_kernel(NormArgs a, float inv_cols, FastDiv gate_rows) {
   constexpr int RG = W < 4 ? 4 / W : 1;   // rows of a workgroup
   __shared__ float slots[RG][4][W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = wave / W, w = wave % W;
   const int at = blockIdx.x * RG + sub, row = min(at, a.rows - 1);
-  const bool on = at < a.rows, below = at < a.rows - 1;
+  const bool on = at < a.rows;
   int col[P];
 #pragma unroll
   for (int j = 0; j < P; ++j) col[j] = 8 * ((j * W + w) * 64 + lane);
@@ -142,8 +142,8 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void block_norm_kernel(NormAr
     float p[P][8];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      load_piece<WHOLE>((const T*)a.y + (int64_t)row * a.ldy, 0, col[j], a.cols, on, below && a.ldy >= 8, p[j]);
-      load_piece<WHOLE>((const X*)a.x + (int64_t)row * a.ldx, 0, col[j], a.cols, on, below && a.ldx >= 8, v[j]);
+      load8<WHOLE>((const T*)a.y + (int64_t)row * a.ldy, col[j], a.cols, p[j]);
+      load8<WHOLE>((const X*)a.x + (int64_t)row * a.ldx, col[j], a.cols, v[j]);
     }
     f32x2 stat{0.0f, 0.0f};
     if (a.p.post) {
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void block_norm_kernel(NormAr
   } else {
 #pragma unroll
     for (int j = 0; j < P; ++j)
-      load_piece<WHOLE>((const X*)a.x + (int64_t)row * a.ldx, 0, col[j], a.cols, on, below && a.ldx >= 8, v[j]);
+      load8<WHOLE>((const X*)a.x + (int64_t)row * a.ldx, col[j], a.cols, v[j]);
     if (a.stats && on && w == 0 && lane == 0) *(f32x2*)(a.stats + 4 * (int64_t)row) = f32x2{0.0f, 0.0f};
   }
   if (!a.n && !a.q.codes && !a.stats) return;
@@ -193,7 +193,9 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void block_norm_kernel(NormAr
   }
 }
 
-// A workgroup's rows: `rg` of them at a time, each by W of its 16 waves.
+// BIAS: dpre_b or dpost_b is wanted (16 registers a piece more).
+//
+// A workgroup's rows: RG of them at a time, each by W of its waves.
 //
 // With hat = (r - mean) rstd, a = dn pre_w and means over the row:
 //   t = dr + rstd (a - mean(a) - hat mean(a hat))             the gradient of r, and so of x
@@ -207,9 +209,10 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void block_norm_kernel(NormAr
 // those in order: no atomics, the same bits every time. dgate's sums end with each
 // group of rows that shares a gate; a group that lies in one workgroup is done there,
 // what a workgroup has of its first and of its last other group goes to the workspace.
-template <class T, class X, int W, int P, bool WHOLE>
-__global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols, FastDiv gate_rows) {
-  constexpr int RG = 16 / W, WIDE = W * 512 * P;
+template <class T, class X, int W, int P, bool WHOLE, bool BIAS>
+__global__ __launch_bounds__(64 * norm_bwd_waves(W), 4) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols,
+                                                                                   FastDiv gate_rows) {
+  constexpr int WAVES = norm_bwd_waves(W), RG = WAVES / W, WIDE = W * 512 * P;
   __shared__ float slots[2][2][RG][2 * W];   // by turns, so that a row's sums are read before the next row's but one are written
   __shared__ __align__(16) float comb[RG > 1 ? 4 * RG * WIDE : 4];   // 128 KB: a workgroup has the CU to itself by its registers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
                 f32x4{s[k][j][4 * h], s[k][j][4 * h + 1], s[k][j][4 * h + 2], s[k][j][4 * h + 3]};
       }
       __syncthreads();
-      for (int c = 4 * threadIdx.x; c < a.cols; c += 4096) {
+      for (int c = 4 * threadIdx.x; c < a.cols; c += 256 * WAVES) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           if (!to[k]) continue;
@@ -268,13 +271,19 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
     const int end = a.p.gate && g1 < last ? (int)g1 : last;
     for (int base = row0; base < end; base += RG, turn ^= 1) {
       const int at = base + sub, row = min(at, end - 1);
-      const bool on = at < end, below = row < a.rows - 1;
+      const bool on = at < end;
       const f32x4 st = *(const f32x4*)(a.stats + 4 * (int64_t)row);   // mean and rstd of y, of r
+      Raw8<T> y[P];
+      if (a.y) {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          y[j].template load<WHOLE>((const T*)a.y + (int64_t)row * a.ld_y, col[j], a.cols, on);
+      }
       float t[P][8], hat[P][8];
       if (a.dr) {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-          load_piece<WHOLE>((const X*)a.dr + (int64_t)row * a.ld_dr, 0, col[j], a.cols, on, below && a.ld_dr >= 8, t[j]);
+          load8<WHOLE>((const X*)a.dr + (int64_t)row * a.ld_dr, col[j], a.cols, t[j], on);
       } else {
 #pragma unroll
         for (int j = 0; j < P; ++j)
@@ -285,13 +294,13 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
         float d[P][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          load_piece<WHOLE>((const T*)a.dn + (int64_t)row * a.ld_dn, 0, col[j], a.cols, on, below && a.ld_dn >= 8, d[j]);
-          load_piece<WHOLE>((const X*)a.r + (int64_t)row * a.ld_r, 0, col[j], a.cols, on, below && a.ld_r >= 8, hat[j]);
+          load8<WHOLE>((const T*)a.dn + (int64_t)row * a.ld_dn, col[j], a.cols, d[j], on);
+          load8<WHOLE>((const X*)a.r + (int64_t)row * a.ld_r, col[j], a.cols, hat[j], on);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             hat[j][i] = (hat[j][i] - st[2]) * st[3];
             s_pre_w[j][i] = __builtin_fmaf(d[j][i], hat[j][i], s_pre_w[j][i]);
-            s_pre_b[j][i] += d[j][i];
+            if (BIAS) s_pre_b[j][i] += d[j][i];
           }
           affine<T, WHOLE>(a.p.pre_w, nullptr, a.p.param32, a.p.w_offset, col[j], a.cols, d[j]);
 #pragma unroll
@@ -317,7 +326,7 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
       float s[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        load_piece<WHOLE>((const T*)a.y + (int64_t)row * a.ld_y, 0, col[j], a.cols, on, below && a.ld_y >= 8, hat[j]);
+        y[j].values(hat[j]);
         drop.apply((uint32_t)row, (uint32_t)col[j] >> 3, t[j]);
         float p[8];
         if (a.p.post) {
@@ -341,7 +350,7 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             s_post_w[j][i] = __builtin_fmaf(t[j][i], hat[j][i], s_post_w[j][i]);
-            s_post_b[j][i] += t[j][i];
+            if (BIAS) s_post_b[j][i] += t[j][i];
           }
           affine<T, WHOLE>(a.p.post_w, nullptr, a.p.param32, a.p.w_offset, col[j], a.cols, t[j]);
 #pragma unroll
@@ -380,7 +389,7 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(NormBwdArgs a, flo
   float* to[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    to[k] = !outs[k] || a.wgs == 1 ? outs[k] : a.part + ((int64_t)k * a.wgs + blockIdx.x) * pitch;
+    to[k] = !outs[k] || (!BIAS && k % 2 == 1) ? nullptr : a.wgs == 1 ? outs[k] : a.part + ((int64_t)k * a.wgs + blockIdx.x) * pitch;
   put_sums(std::integral_constant<int, 4>{}, {s_pre_w, s_pre_b, s_post_w, s_post_b}, {to[0], to[1], to[2], to[3]});
 }
 
@@ -429,7 +438,11 @@ hipError_t norm_bwd_of(const NormBwdArgs& a, hipStream_t s) {
   const FastDiv gates = FastDiv::make((uint32_t)a.p.rows_per_gate);
   by_width(a.cols, [&](auto waves, auto pieces) {
     constexpr int W = decltype(waves)::value, P = decltype(pieces)::value;
-    hipLaunchKernelGGL((block_norm_bwd_kernel<T, X, W, P, WHOLE>), dim3(a.wgs), dim3(1024), 0, s, a, inv, gates);
+    const dim3 grid(a.wgs), block(64 * norm_bwd_waves(W));
+    if (a.dpre_b || a.dpost_b)
+      hipLaunchKernelGGL((block_norm_bwd_kernel<T, X, W, P, WHOLE, true>), grid, block, 0, s, a, inv, gates);
+    else
+      hipLaunchKernelGGL((block_norm_bwd_kernel<T, X, W, P, WHOLE, false>), grid, block, 0, s, a, inv, gates);
   });
   return hipGetLastError();
 }

@@ -13,11 +13,9 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a, FastDi
   const uint32_t id = blockIdx.x * kThreads + threadIdx.x, row = pieces.div(id);
   if ((int)row >= a.rows) return;
   const int col = 8 * (int)(id - row * pieces.d);
-  const bool below = (int)row < a.rows - 1;
   float v[8], r[8];
-  load_piece<WHOLE>((const T*)a.x + (int64_t)row * a.ldx, 0, col, a.cols, true, below && a.ldx >= 8, v);
-  if (a.residual)
-    load_piece<WHOLE>((const T*)a.residual + (int64_t)row * a.ldr, 0, col, a.cols, true, below && a.ldr >= 8, r);
+  load8<WHOLE>((const T*)a.x + (int64_t)row * a.ldx, col, a.cols, v);
+  if (a.residual) load8<WHOLE>((const T*)a.residual + (int64_t)row * a.ldr, col, a.cols, r);
   Drop(a.drop).apply(a.first_row + row, (uint32_t)col >> 3, v);
   if (a.residual) {
 #pragma unroll

@@ -79,39 +79,100 @@ struct Drop {
   }
 };
 
-// 8 values of a row from column `col` on, at any alignment; those past the last column are 0.
+// 8 values of a row from column `col` (a multiple of 8) on, as they lie in memory; zeros
+// past the last column and where a lane is off.
 template <class T>
-__device__ __forceinline__ void load8(const T* row, int col, int cols, float (&v)[8]) {
-  T t[8];
-  if (col + 8 <= cols) {
-    __builtin_memcpy(t, row + col, sizeof t);
+struct Raw8 {
+  static constexpr int WORDS = 2 * (int)sizeof(T);
+  uint32_t w[WORDS];
+  // WHOLE: the row is 16-byte aligned, and all or none of the 8 are inside. Else any
+  // alignment: the row's last piece is read from 8 columns before its end on and moved
+  // down, so that nothing past the row is read and only that piece's wave does more.
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const T* row, int col, int cols, bool on = true) {
+    if constexpr (WHOLE) {
+      on = on && col < cols;
+      const uint32_t m = on_mask(on);
+      const char* const at = (const char*)row + (on ? col : 0) * (int)sizeof(T);
+#pragma unroll
+      for (int i = 0; i < WORDS / 4; ++i) {
+        const u32x4 v = *(const u32x4*)(at + 16 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e] & m;
+      }
+    } else if (cols >= 8) {
+      const int at = min(col, cols - 8);
+      __builtin_memcpy(w, row + at, sizeof w);
+      const int down = on ? min(col - at, 8) : 8;
+      if (down > 0) move_down(down);
+    } else {
+      T t[8] = {};
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (on && col + i < cols) t[i] = row[col + i];
+      __builtin_memcpy(w, t, sizeof w);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    T t[8];
+    __builtin_memcpy(t, w, sizeof w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = widen(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? widen(row[col + i]) : 0.0f;
   }
+
+ private:
+  // the values from number n (1 to 8) on become the first, zeros follow
+  __device__ __forceinline__ void move_down(int n) {
+    constexpr int E = 4 / (int)sizeof(T);   // values of a word
+#pragma unroll
+    for (int words = WORDS; words >= 1; words /= 2) {
+      const uint32_t keep = on_mask((n & (words * E)) == 0);
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[i] = (w[i] & keep) | ((i + words < WORDS ? w[i + words] : 0u) & ~keep);
+    }
+    if constexpr (E == 2) {
+      const uint32_t bits = (n & 1) * 16;
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[i] = __builtin_amdgcn_alignbit(i + 1 < WORDS ? w[i + 1] : 0u, w[i], bits);
+    }
+  }
+};
+template <bool WHOLE, class T>
+__device__ __forceinline__ void load8(const T* row, int col, int cols, float (&v)[8], bool on = true) {
+  Raw8<T> r;
+  r.template load<WHOLE>(row, col, cols, on);
+  r.values(v);
 }
-// 8 values to a row, each rounded once, none past the last column. WHOLE: 16-byte
-// aligned, and all or none of the 8 are inside.
+// 8 values to a row, each rounded once, none past the last column. WHOLE: as above
 template <bool WHOLE, class T>
 __device__ __forceinline__ void store8(T* row, int col, int cols, const float (&v)[8]) {
-  if (WHOLE ? col < cols : col + 8 <= cols) {
-    T t[8];
+  T t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) narrow(v[i], t[i]);
-    if constexpr (WHOLE) {
-      u32x4 w[sizeof t / 16];
-      __builtin_memcpy(w, t, sizeof t);
+  for (int i = 0; i < 8; ++i) narrow(v[i], t[i]);
+  const int n = cols - col;
+  if constexpr (WHOLE) {
+    u32x4 w[sizeof t / 16];
+    __builtin_memcpy(w, t, sizeof t);
+    if (n > 0) {
 #pragma unroll
       for (int i = 0; i < (int)(sizeof t / 16); ++i) ((u32x4*)(row + col))[i] = w[i];
-    } else {
-      __builtin_memcpy(row + col, t, sizeof t);
     }
-  } else if constexpr (!WHOLE) {
+  } else if (n >= 8) {
+    __builtin_memcpy(row + col, t, sizeof t);
+  } else if (n > 0) {
+    T* to = row + col;
+    if (n & 4) {
+      __builtin_memcpy(to, t, 4 * sizeof(T));
+      to += 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) narrow(v[i], row[col + i]);
+      for (int i = 0; i < 3; ++i) t[i] = t[4 + i];
+    }
+    if (n & 2) {
+      __builtin_memcpy(to, t, 2 * sizeof(T));
+      to += 2;
+      t[0] = t[2];
+    }
+    if (n & 1) to[0] = t[0];
   }
 }
 

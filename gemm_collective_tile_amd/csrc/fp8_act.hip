@@ -27,30 +27,6 @@ __device__ __forceinline__ float same_columns_sum(float v) {
   return __builtin_bit_cast(float, (uint32_t)y[0]) + __builtin_bit_cast(float, (uint32_t)y[1]);
 }
 
-// 8 values as they lie in memory
-template <class T>
-struct Raw8 {
-  static constexpr int WORDS = 2 * (int)sizeof(T);
-  uint32_t w[WORDS];
-  // of a row from column `col` on, at any alignment; those past the last column are 0
-  __device__ __forceinline__ void load(const T* row, int col, int cols) {
-    if (col + 8 <= cols) {
-      __builtin_memcpy(w, row + col, sizeof w);
-    } else {
-      T t[8] = {};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < cols) t[i] = row[col + i];
-      __builtin_memcpy(w, t, sizeof w);
-    }
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    T t[8];
-    __builtin_memcpy(t, w, sizeof w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = widen(t[i]);
-  }
-};
 // the matrix that an epilogue reads beside the sums: z, the residual or none
 template <bool BACKWARD, class OUT>
 struct Beside {
@@ -59,7 +35,7 @@ struct Beside {
   __device__ __forceinline__ explicit Beside(const Fp8ActArgs& a)
       : at((const OUT*)(BACKWARD ? a.z : a.residual)), ld(BACKWARD ? a.ldz : a.ldr) {}
   __device__ __forceinline__ void load(int m, int n, int N, bool on, Raw8<OUT>& r) const {
-    if (at && on) r.load(at + (int64_t)m * ld, n, N);
+    if (at && on) r.template load<false>(at + (int64_t)m * ld, n, N);
   }
 };
 
@@ -147,7 +123,7 @@ template <class OUT>
 __device__ __forceinline__ void load_bias8(const Fp8ActArgs& a, int n, float (&b)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) b[i] = 0.0f;
-  if (a.g.bias && n < a.g.N) load8((const OUT*)a.g.bias, n, a.g.N, b);
+  if (a.g.bias && n < a.g.N) load8<false>((const OUT*)a.g.bias, n, a.g.N, b);
 }
 
 // between the writes and the reads of a strip: of the workgroup's waves where they share
@@ -208,7 +184,7 @@ __global__ __launch_bounds__(256) void fp8_mm_act_kernel(Fp8ActArgs a) {
   f32x16 acc[T::FM][T::FN];
   Raw8<OUT> bias_raw = {};
   tile_sums<EXACT, T>(a.g, lds, pm, pn, acc, [&] {
-    if (!BACKWARD && a.g.bias && n < a.g.N) bias_raw.load((const OUT*)a.g.bias, n, a.g.N);
+    if (!BACKWARD && a.g.bias && n < a.g.N) bias_raw.template load<false>((const OUT*)a.g.bias, n, a.g.N);
   });
 
   float* const strip = (float*)lds + (SHARED ? half : wave) * STRIP;
@@ -412,14 +388,12 @@ __global__ __launch_bounds__(256) void fp8_dbias_kernel(const float* part, int p
   __shared__ float red[4][64];
   const int l = threadIdx.x & 63, c = blockIdx.x * 64 + l, g = threadIdx.x >> 6;
   float v = 0.0f;
-  if (c < N) {
-    for (int i = g; i < parts; i += 64) {
-      float x[16];
+  for (int i = g; i < parts; i += 64) {
+    float x[16];   // a row past the end reads the last one and drops it: no branch between the loads
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = i + 4 * k < parts ? part[(i + 4 * k) * ldp + c] : 0.0f;
+    for (int k = 0; k < 16; ++k) x[k] = part[min(i + 4 * k, parts - 1) * ldp + min(c, N - 1)];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v += x[k];
-    }
+    for (int k = 0; k < 16; ++k) v += i + 4 * k < parts ? x[k] : 0.0f;
   }
   red[g][l] = v;
   __syncthreads();
