@@ -756,8 +756,12 @@ def _any_plain(t, name: str, shape, kind, dev: int):
         _want_shape(t, shape, name)
     if t.dtype is not kind:
         raise TypeError(f"{name} must be {str(kind)[6:]}")
-    ptr, _, ld = _plain(t, name, _FP8_TYPES, shape[0], shape[1], dev)
-    return ptr, ld
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    if dev < 0 or t.get_device() != dev:
+        raise _elsewhere(name, t.get_device(), dev)
+    return t.data_ptr(), (ld if shape[0] > 1 else shape[1])
 
 
 def _call_stream(stream, dev: int):
@@ -768,13 +772,15 @@ def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float
     """out = residual + alpha m x, (rows, cols) float16, bfloat16 or float32 of any row
     pitch; m is dropout's mask. On out's gradient it is its own backward pass."""
     shape = rows, cols = _shape2(x, "x")
-    dev = x.get_device()
-    ptr, kind, ld = _plain(x, "x", _FP8_TYPES, rows, cols, dev)
+    dev, dtype = x.get_device(), x.dtype
+    kind = _FP8_TYPES.get(dtype)
+    if kind is None:
+        raise TypeError(f"x must be one of {', '.join(str(d)[6:] for d in _FP8_TYPES)}")
     if out is None:
         raise ValueError("out is required")
-    op, old = _any_plain(out, "out", shape, x.dtype, dev)
-    rp, rld = _any_plain(residual, "residual", shape, x.dtype, dev)
-    st = _lib.iris_dropout(op, old, ptr, ld, rp, rld, kind, alpha, _drop(dropout, dev), rows, cols, _call_stream(stream, dev))
+    st = _lib.iris_dropout(*_any_plain(out, "out", shape, dtype, dev), *_any_plain(x, "x", shape, dtype, dev),
+                           *_any_plain(residual, "residual", shape, dtype, dev), kind, alpha, _drop(dropout, dev), rows, cols,
+                           _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -874,24 +880,14 @@ def _norm_kind(norm, stream_kind, *tensors):
         raise TypeError("norm must be a BlockNorm")
     for t in tensors:
         if t is not None:
-            if not isinstance(t, torch.Tensor) or t.dtype not in _FP8_HALVES:
+            kind = getattr(t, "dtype", None)
+            if kind not in _FP8_HALVES:
                 raise TypeError("y, n, dn and dy must be float16 or bfloat16 torch tensors")
-            return t.dtype
+            return kind
     for dtype in (stream_kind, norm._param, norm._gate):
         if dtype in _FP8_HALVES:
             return dtype
     return torch.bfloat16
-
-
-def _stats_ptr(stats, rows: int, dev: int):
-    if stats is None:
-        return None
-    _want_shape(stats, (rows, 4), "stats")
-    if stats.dtype != torch.float32 or not stats.is_contiguous():
-        raise TypeError("stats must be a contiguous float32 tensor")
-    if stats.get_device() != dev:
-        raise _elsewhere("stats", stats.get_device(), dev)
-    return stats.data_ptr()
 
 
 def iris_block_norm(x, norm: BlockNorm, y=None, r=None, n=None, q: Optional[Fp8] = None, stats=None, stream=None) -> None:
@@ -900,14 +896,15 @@ def iris_block_norm(x, norm: BlockNorm, y=None, r=None, n=None, q: Optional[Fp8]
     and n (float16, bfloat16); stats (rows, 4) float32 receives what the backward pass
     needs. Outputs that are not wanted are None."""
     shape = rows, cols = _shape2(x, "x")
-    dev = x.get_device()
-    kind = _norm_kind(norm, x.dtype, y, n)
+    dev, dtype = x.get_device(), x.dtype
+    kind = _norm_kind(norm, dtype, y, n)
     norm._for(rows, cols, dev)
-    p = norm._struct(kind, x.dtype)
-    xp, _, xld = _plain(x, "x", _FP8_TYPES, rows, cols, dev)
-    st = _lib.iris_block_norm(*_any_plain(r, "r", shape, x.dtype, dev), *_any_plain(n, "n", shape, kind, dev),
-                              None if q is None else _fp8(q, shape, "q", dev), _stats_ptr(stats, rows, dev), xp, xld,
-                              *_any_plain(y, "y", shape, kind, dev), p, rows, cols, _call_stream(stream, dev))
+    p = norm._structs.get((kind, dtype)) or norm._struct(kind, dtype)
+    st = _lib.iris_block_norm(*_any_plain(r, "r", shape, dtype, dev), *_any_plain(n, "n", shape, kind, dev),
+                              None if q is None else _fp8(q, shape, "q", dev),
+                              None if stats is None else _sums(stats, "stats", (rows, 4), dev),
+                              *_any_plain(x, "x", shape, dtype, dev), *_any_plain(y, "y", shape, kind, dev), p, rows, cols,
+                              _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -932,20 +929,19 @@ def iris_block_norm_bwd(dx, r, stats, norm: BlockNorm, dn=None, dr=None, y=None,
     what reaches r from elsewhere. dx (dtype of r), dy (of y); the parameters' gradients
     in float32, dgate of the gate's shape. What is not wanted is None."""
     shape = rows, cols = _shape2(r, "r")
-    dev = r.get_device()
-    kind = _norm_kind(norm, r.dtype, y, dn, dy)
+    dev, dtype = r.get_device(), r.dtype
+    kind = _norm_kind(norm, dtype, y, dn, dy)
     norm._for(rows, cols, dev)
-    p = norm._struct(kind, r.dtype)
+    p = norm._structs.get((kind, dtype)) or norm._struct(kind, dtype)
     if dgate is not None and norm.gate is None:
         raise ValueError("dgate needs a gate")
-    rp, _, rld = _plain(r, "r", _FP8_TYPES, rows, cols, dev)
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
     st = _lib.iris_block_norm_bwd(
-        *_any_plain(dx, "dx", shape, r.dtype, dev), *_any_plain(dy, "dy", shape, kind, dev),
+        *_any_plain(dx, "dx", shape, dtype, dev), *_any_plain(dy, "dy", shape, kind, dev),
         _sums(dpre_w, "dpre_w", (cols,), dev), _sums(dpre_b, "dpre_b", (cols,), dev), _sums(dpost_w, "dpost_w", (cols,), dev),
         _sums(dpost_b, "dpost_b", (cols,), dev), None if dgate is None else _sums(dgate, "dgate", norm.gate.shape, dev),
-        *_any_plain(dn, "dn", shape, kind, dev), *_any_plain(dr, "dr", shape, r.dtype, dev), rp, rld,
-        *_any_plain(y, "y", shape, kind, dev), _stats_ptr(stats, rows, dev), p, rows, cols, ws, wsb, _call_stream(stream, dev))
+        *_any_plain(dn, "dn", shape, kind, dev), *_any_plain(dr, "dr", shape, dtype, dev), *_any_plain(r, "r", shape, dtype, dev),
+        *_any_plain(y, "y", shape, kind, dev), None if stats is None else _sums(stats, "stats", (rows, 4), dev), p, rows, cols, ws, wsb, _call_stream(stream, dev))
     if st:
         _check(st)
 

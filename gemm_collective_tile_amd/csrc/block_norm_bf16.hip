@@ -1,4 +1,6 @@
 // The block norms of bf16 activations, and the joining of the column sums.
+#include <algorithm>
+
 #include "block_norm_kernels.hpp"
 
 namespace iris {
@@ -10,11 +12,16 @@ namespace {
 
 constexpr int kJoinGates = 16;
 
+struct JoinArgs {   // short: the host writes a kernel's arguments for every launch
+  float *dpre_w, *dpre_b, *dpost_w, *dpost_b, *dgate;
+  const float* part;
+  int32_t rows, cols, rows_per_gate, wgs, wg_rows, groups;
+};
+
 // Adds the workgroups' sums, 64 columns at a time, 16 waves a sixteenth of the workgroups
 // each with up to 16 loads under way. blockIdx.y: 0 to 3 the parameters' gradients; from
-// 4 on the gates' whose rows several workgroups share, each by the workgroup that has
-// its first row.
-__global__ __launch_bounds__(1024) void block_norm_join_kernel(NormBwdArgs a, FastDiv gate_rows) {
+// 4 on the gates' whose rows several workgroups share.
+__global__ __launch_bounds__(1024) void block_norm_join_kernel(JoinArgs a, FastDiv gate_rows, FastDiv wg_rows) {
   __shared__ float sums[16][64];
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
   const int64_t pitch = (a.cols + 7) & ~7;
@@ -49,18 +56,18 @@ __global__ __launch_bounds__(1024) void block_norm_join_kernel(NormBwdArgs a, Fa
     if (out) join(nullptr, a.part + (int64_t)blockIdx.y * a.wgs * pitch, a.wgs, pitch, out);
     return;
   }
+  // by group where there are fewer groups than workgroups, else by the workgroup a group begins in
   const float* const gates = a.part + (int64_t)4 * a.wgs * pitch;
-  for (int w = blockIdx.y - 4; w < a.wgs - 1; w += kJoinGates) {
-    const int next = (w + 1) * a.wg_rows;                    // the first row of the next workgroup
-    const uint32_t g = gate_rows.div(next - 1);
-    const int64_t g0 = (int64_t)g * a.p.rows_per_gate;
-    const int g1 = (int)min(g0 + a.p.rows_per_gate, (int64_t)a.rows);
-    if (g1 > next && g0 >= next - a.wg_rows) {               // goes on there, and begins here
-      const int n = (g1 - 1) / a.wg_rows - w;                // further workgroups: their first share each
-      join(gates + (2 * w + (g0 == next - a.wg_rows ? 0 : 1)) * pitch, gates + 2 * (w + 1) * pitch, n, 2 * pitch,
-           a.dgate + (int64_t)g * a.cols);
-    }
-    if (a.p.rows_per_gate >= a.rows) break;                  // one gate: the first workgroup's
+  const int64_t every = a.rows_per_gate;
+  const bool by_group = a.groups < a.wgs;
+  for (int k = blockIdx.y - 4; k < (by_group ? a.groups : a.wgs - 1); k += gridDim.y - 4) {
+    const int64_t g = by_group ? k : gate_rows.div((k + 1) * a.wg_rows - 1);
+    const int64_t g0 = g * every, g1 = min(g0 + every, (int64_t)a.rows);
+    const int w = by_group ? (int)wg_rows.div((uint32_t)g0) : k, next = min((w + 1) * a.wg_rows, a.rows);
+    if (g1 <= next || g0 < (int64_t)w * a.wg_rows) continue;   // ends here, or began before
+    const int n = (int)wg_rows.div((uint32_t)(g1 - 1)) - w;    // further workgroups: their first share each
+    join(gates + (2 * w + (g0 == (int64_t)w * a.wg_rows ? 0 : 1)) * pitch, gates + 2 * (w + 1) * pitch, n, 2 * pitch,
+         a.dgate + g * a.cols);
   }
 }
 
@@ -82,9 +89,10 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
 
 hipError_t launch_norm_join(const NormBwdArgs& a, hipStream_t s) {
   if (a.wgs <= 1) return hipSuccess;
-  const int gates = !a.dgate ? 0 : a.p.rows_per_gate >= a.rows ? 1 : kJoinGates;
-  hipLaunchKernelGGL(block_norm_join_kernel, dim3((a.cols + 63) / 64, 4 + gates), dim3(1024), 0, s, a,
-                     FastDiv::make((uint32_t)a.p.rows_per_gate));
+  const JoinArgs j{a.dpre_w, a.dpre_b, a.dpost_w, a.dpost_b, a.dgate, a.part, a.rows, a.cols, a.p.rows_per_gate, a.wgs, a.wg_rows,
+                   a.dgate ? (a.rows + a.p.rows_per_gate - 1) / a.p.rows_per_gate : 0};
+  hipLaunchKernelGGL(block_norm_join_kernel, dim3((a.cols + 63) / 64, 4 + std::min(j.groups, kJoinGates)), dim3(1024), 0, s, j,
+                     FastDiv::make((uint32_t)j.rows_per_gate), FastDiv::make((uint32_t)j.wg_rows));
   return hipGetLastError();
 }
 

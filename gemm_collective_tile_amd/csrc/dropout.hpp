@@ -106,11 +106,17 @@ struct Raw8 {
       const int down = on ? min(col - at, 8) : 8;
       if (down > 0) move_down(down);
     } else {
-      T t[8] = {};
 #pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (on && col + i < cols) t[i] = row[col + i];
-      __builtin_memcpy(w, t, sizeof w);
+      for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll 1
+      for (int i = on && col == 0 ? cols - 1 : -1; i >= 0; --i) {   // from the last on, each pushes the others up
+        T t[2] = {row[i], {}};
+        uint32_t first = 0;
+        __builtin_memcpy(&first, t, sizeof first);
+#pragma unroll
+        for (int k = WORDS - 1; k > 0; --k) w[k] = sizeof(T) == 4 ? w[k - 1] : __builtin_amdgcn_alignbit(w[k], w[k - 1], 16);
+        w[0] = sizeof(T) == 4 ? first : (w[0] << 16) | first;
+      }
     }
   }
   __device__ __forceinline__ void values(float (&v)[8]) const {
