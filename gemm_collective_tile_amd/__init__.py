@@ -176,7 +176,7 @@ def _load() -> ctypes.CDLL:
         "iris_fp8_mm": [vp, i32, i64, f8, f8, vp, i64, i64, i64, i32, vp, sz, vp],
         "iris_fp8_swiglu": [f8, f8, f8, vp, vp, i32, i64, i64, i64, i64, vp],
         "iris_fp8_swiglu_bwd": [f8, f8, f8, f8, f8, vp, i32, i64, f8, f8, i64, i64, vp],
-        "iris_dropout": [vp, i64, vp, i64, vp, i64, i32, f32, drop, i64, i64, vp],
+        "iris_dropout": [vp, i64, vp, i64, vp, i64, i32, f32, drop, vp, i64, i64, vp, sz, vp],
         "iris_block_norm": [vp, i64, vp, i64, f8, vp, vp, i64, vp, i64, norm, i64, i64, vp],
         "iris_block_norm_bwd": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, norm, i64, i64,
                                 vp, sz, vp],
@@ -205,6 +205,8 @@ def _load() -> ctypes.CDLL:
     lib.iris_workspace_size.restype = sz
     lib.iris_fp8_mm_workspace_size.argtypes = [i64, i64, i64]
     lib.iris_fp8_mm_workspace_size.restype = sz
+    lib.iris_dropout_workspace_size.argtypes = [i64, i64]
+    lib.iris_dropout_workspace_size.restype = sz
     lib.iris_block_norm_bwd_workspace_size.argtypes = [i64, i64]
     lib.iris_block_norm_bwd_workspace_size.restype = sz
     lib.iris_fp8_mm_act_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
@@ -764,13 +766,29 @@ def _any_plain(t, name: str, shape, kind, dev: int):
     return t.data_ptr(), (ld if shape[0] > 1 else shape[1])
 
 
+def _vector(t, name: str, N: int, kind, dev: int):
+    if t is None:
+        return None
+    _want_shape(t, (N,), name)
+    if t.dtype != kind:
+        raise TypeError(f"{name} must be {str(kind)[6:]}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise _elsewhere(name, t.get_device(), dev)
+    return t.data_ptr()
+
+
 def _call_stream(stream, dev: int):
     return _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev)
 
 
-def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float = 1.0, stream=None) -> None:
+def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float = 1.0, sums=None, workspace=None,
+                 stream=None) -> None:
     """out = residual + alpha m x, (rows, cols) float16, bfloat16 or float32 of any row
-    pitch; m is dropout's mask. On out's gradient it is its own backward pass."""
+    pitch; m is dropout's mask. On out's gradient it is its own backward pass; `sums`
+    (cols values of x's dtype) then receives the gradient of a bias of x: out's sums over
+    the rows."""
     shape = rows, cols = _shape2(x, "x")
     dev, dtype = x.get_device(), x.dtype
     kind = _FP8_TYPES.get(dtype)
@@ -778,11 +796,17 @@ def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float
         raise TypeError(f"x must be one of {', '.join(str(d)[6:] for d in _FP8_TYPES)}")
     if out is None:
         raise ValueError("out is required")
+    ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
     st = _lib.iris_dropout(*_any_plain(out, "out", shape, dtype, dev), *_any_plain(x, "x", shape, dtype, dev),
-                           *_any_plain(residual, "residual", shape, dtype, dev), kind, alpha, _drop(dropout, dev), rows, cols,
+                           *_any_plain(residual, "residual", shape, dtype, dev), kind, alpha, _drop(dropout, dev),
+                           None if sums is None else _vector(sums, "sums", cols, dtype, dev), rows, cols, ws, wsb,
                            _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
+
+
+def iris_dropout_workspace_size(rows: int, cols: int) -> int:
+    return int(_lib.iris_dropout_workspace_size(rows, cols))
 
 
 _NORM_KINDS = {"rms": IRIS_NORM_RMS, "layer": IRIS_NORM_LAYER, IRIS_NORM_RMS: IRIS_NORM_RMS, IRIS_NORM_LAYER: IRIS_NORM_LAYER}
@@ -972,19 +996,6 @@ def _mm_operands(A, B, act):
     return M, N, K, A._device, code
 
 
-def _mm_vector(t, name: str, N: int, kind, dev: int):
-    if t is None:
-        return None
-    _want_shape(t, (N,), name)
-    if t.dtype != kind:
-        raise TypeError(f"{name} must be {kind} as C is")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise _elsewhere(name, t.get_device(), dev)
-    return t.data_ptr()
-
-
 def iris_fp8_mm_act(C, A: Fp8, B: Fp8, act="none", bias=None, z=None, residual=None, alpha: float = 1.0,
                     dropout: Optional[Dropout] = None, q: Optional[Fp8] = None, dtype=None, workspace=None, stream=None) -> None:
     """C = residual + alpha m act(A @ B^T + bias), C (M, N) float16, bfloat16 or float32;
@@ -1006,7 +1017,7 @@ def iris_fp8_mm_act(C, A: Fp8, B: Fp8, act="none", bias=None, z=None, residual=N
     zp, ldz = _any_plain(z, "z", shape, kind, dev)
     rp, ldr = _any_plain(residual, "residual", shape, kind, dev)
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
-    e = _Epilogue(code, alpha, _mm_vector(bias, "bias", N, kind, dev), zp, ldz, rp, ldr,
+    e = _Epilogue(code, alpha, _vector(bias, "bias", N, kind, dev), zp, ldz, rp, ldr,
                   None if q is None else _fp8(q, shape, "q", dev), _drop(dropout, dev))
     st = _lib.iris_fp8_mm_act(cp, c_type, ldc, ap, bp, e, M, N, K, ws, wsb, _call_stream(stream, dev))
     if st:
@@ -1030,7 +1041,7 @@ def iris_fp8_mm_act_bwd(C, A: Fp8, B: Fp8, z, act, alpha: float = 1.0, dropout: 
     cp, ldc = _any_plain(C, "C", shape, kind, dev)
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
     st = _lib.iris_fp8_mm_act_bwd(cp, c_type, ldc,
-                                  _mm_vector(dbias, "dbias", N, kind, dev), ap, bp, *_any_plain(z, "z", shape, kind, dev), code,
+                                  _vector(dbias, "dbias", N, kind, dev), ap, bp, *_any_plain(z, "z", shape, kind, dev), code,
                                   alpha, _drop(dropout, dev), M, N, K, ws, wsb, _call_stream(stream, dev))
     if st:
         _check(st)

@@ -154,20 +154,35 @@ int run_mm(const iris::Fp8ActArgs& a, const iris::Fp8ActPlan& plan, void* dbias,
 
 extern "C" {
 
+size_t iris_dropout_workspace_size(int64_t rows, int64_t cols) try {
+  if (check_rows(rows, cols) || rows == 0 || cols == 0) return 0;
+  return iris::dropout_plan(rows, cols).ws_bytes;
+} catch (const std::exception&) {
+  return 0;
+}
+
 int iris_dropout(void* out, int64_t ld_out, const void* x, int64_t ldx, const void* residual, int64_t ld_residual, int32_t type,
-                 float alpha, const iris_drop_t* drop, int64_t rows, int64_t cols, void* stream) try {
+                 float alpha, const iris_drop_t* drop, void* sums, int64_t rows, int64_t cols, void* workspace,
+                 size_t workspace_bytes, void* stream) try {
   iris::set_error(IRIS_OK, "");
   int st;
   iris::DropoutArgs a{};
   if ((st = check_rows(rows, cols)) || (st = check_plain(out, type, true, ld_out, rows, cols, "out")) ||
       (st = check_plain(x, type, true, ldx, rows, cols, "x")) ||
-      (st = check_optional(residual, type, ld_residual, rows, cols, "residual")) || (st = check_drop(drop, alpha, &a.drop)))
+      (st = check_optional(residual, type, ld_residual, rows, cols, "residual")) || (st = check_vector(sums, type, "sums")) ||
+      (st = check_drop(drop, alpha, &a.drop)))
     return st;
-  if (rows == 0 || cols == 0) return IRIS_OK;
-  if ((st = check_distinct({{out, "out", true}, {x, "x", false}, {residual, "residual", false},
-                            {drop ? (const void*)drop->offset_at : nullptr, "offset_at", false}})))
+  if (cols == 0 || (rows == 0 && !sums)) return IRIS_OK;
+  iris::DropoutPlan plan{};
+  if (sums) plan = iris::dropout_plan(rows, cols);
+  if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes))) return st;
+  if ((st = check_distinct({{out, "out", true}, {sums, "sums", true}, {workspace, "workspace", true}, {x, "x", false},
+                            {residual, "residual", false}, {drop ? (const void*)drop->offset_at : nullptr, "offset_at", false}})))
     return st;
-  if ((st = ready())) return st;
+  int dev = 0, cus = 0;
+  if ((st = iris::use_device(&dev, &cus))) return st;
+  std::unique_lock<std::mutex> hold;   // over both launches
+  if (plan.ws_bytes > 0 && !workspace && (st = iris::fp8_own_workspace(dev, stream, plan.ws_bytes, &workspace, &hold))) return st;
   a.x = x;
   a.residual = residual;
   a.out = out;
@@ -179,7 +194,7 @@ int iris_dropout(void* out, int64_t ld_out, const void* x, int64_t ldx, const vo
   a.type = type;
   a.vec = rows16_or_none(x, ldx, type, rows) && rows16_or_none(out, ld_out, type, rows) &&
           rows16_or_none(residual, ld_residual, type, rows);
-  return launched(iris::launch_dropout(a, (hipStream_t)stream), "iris_dropout");
+  return launched(iris::launch_dropout(a, plan, sums, workspace, (hipStream_t)stream), "iris_dropout");
 } catch (const std::exception& e) {
   return caught(e);
 }

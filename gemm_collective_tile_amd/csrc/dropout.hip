@@ -1,6 +1,7 @@
 // out = residual + alpha m x, the mask computed on the way (dropout.hpp).
 #include <algorithm>
 
+#include "column_sums.hpp"
 #include "dropout.hpp"
 #include "fp8.hpp"
 
@@ -22,6 +23,51 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a, FastDi
     for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
   store8<WHOLE>((T*)a.out + (int64_t)row * a.ldo, col, a.cols, v);
+}
+
+// The same with the sums of out over its rows, before its rounding: a workgroup takes 128
+// columns of a share of the rows, 16 rows at a time, and leaves a row of partial sums.
+template <class T, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void dropout_sums_kernel(DropoutArgs a, int share, float* part, int64_t ldp) {
+  __shared__ float red[4][128];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 128 + 8 * (lane & 15), from = blockIdx.y * share, to = min(from + share, a.rows);
+  const Drop drop(a.drop);
+  float sums[8] = {};
+  for (int base = from; base < to; base += 16) {
+    const int at = base + (threadIdx.x >> 4), row = min(at, to - 1);
+    const bool on = at < to;
+    float v[8], r[8];
+    load8<WHOLE>((const T*)a.x + (int64_t)row * a.ldx, col, a.cols, v);
+    if (a.residual) load8<WHOLE>((const T*)a.residual + (int64_t)row * a.ldr, col, a.cols, r);
+    drop.apply((uint32_t)row, (uint32_t)col >> 3, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (a.residual) v[i] += r[i];
+      sums[i] += on ? v[i] : 0.0f;
+    }
+    if (on) store8<WHOLE>((T*)a.out + (int64_t)row * a.ldo, col, a.cols, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[i] = same_columns_sum<16>(sums[i]);
+  if (lane < 16) __builtin_memcpy(&red[wave][8 * lane], sums, sizeof sums);
+  __syncthreads();
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && c < a.cols) {
+    const int t = threadIdx.x;
+    part[(int64_t)blockIdx.y * ldp + c] = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]);
+  }
+}
+
+template <class T, bool WHOLE>
+hipError_t dropout_sums(const DropoutArgs& a, const DropoutPlan& plan, void* sums, void* ws, hipStream_t s) {
+  if (a.rows > 0) {
+    hipLaunchKernelGGL((dropout_sums_kernel<T, WHOLE>), dim3((a.cols + 127) / 128, plan.parts), dim3(kThreads), 0, s, a, plan.share,
+                       (float*)ws, (int64_t)plan.pitch);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return join_columns((const float*)ws, plan.parts, (int64_t)plan.pitch, a.cols, (T*)sums, s);
 }
 
 template <class T, bool WHOLE>
@@ -47,17 +93,30 @@ hipError_t dropout(const DropoutArgs& args, hipStream_t s) {
 }
 
 template <class T>
-hipError_t of_type(const DropoutArgs& a, hipStream_t s) {
-  return a.vec && a.cols % 8 == 0 ? dropout<T, true>(a, s) : dropout<T, false>(a, s);
+hipError_t of_type(const DropoutArgs& a, const DropoutPlan& plan, void* sums, void* ws, hipStream_t s) {
+  const bool whole = a.vec && a.cols % 8 == 0;
+  if (sums) return whole ? dropout_sums<T, true>(a, plan, sums, ws, s) : dropout_sums<T, false>(a, plan, sums, ws, s);
+  return whole ? dropout<T, true>(a, s) : dropout<T, false>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s) {
+// Enough workgroups to fill the chip eight times over, shares of whole steps of 16 rows.
+DropoutPlan dropout_plan(int64_t rows, int64_t cols) {
+  const int64_t blocks = (cols + 127) / 128, most = std::max<int64_t>(1, 8 * kFp8Cus / blocks);
+  DropoutPlan p{};
+  p.share = (int32_t)(((rows + most - 1) / most + 15) / 16 * 16);
+  p.parts = rows > 0 ? (int32_t)((rows + p.share - 1) / p.share) : 0;
+  p.pitch = (int32_t)((cols + 3) / 4 * 4);
+  p.ws_bytes = (size_t)p.parts * p.pitch * 4;
+  return p;
+}
+
+hipError_t launch_dropout(const DropoutArgs& a, const DropoutPlan& plan, void* sums, void* ws, hipStream_t s) {
   switch (a.type) {
-    case T_FP16: return of_type<f16>(a, s);
-    case T_BF16: return of_type<bf16>(a, s);
-    default: return of_type<float>(a, s);
+    case T_FP16: return of_type<f16>(a, plan, sums, ws, s);
+    case T_BF16: return of_type<bf16>(a, plan, sums, ws, s);
+    default: return of_type<float>(a, plan, sums, ws, s);
   }
 }
 

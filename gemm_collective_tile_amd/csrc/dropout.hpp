@@ -191,6 +191,13 @@ struct DropoutArgs {
   uint32_t first_row;         // of this launch's rows (set by the launch)
   DropArgs drop;
 };
-hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
+// with sums over the rows: shares of the rows, a row of partial sums each
+struct DropoutPlan {
+  int32_t share, parts, pitch;
+  size_t ws_bytes;
+};
+DropoutPlan dropout_plan(int64_t rows, int64_t cols);
+// sums: `cols` values of the type, or NULL (then plan and ws are of no account)
+hipError_t launch_dropout(const DropoutArgs& a, const DropoutPlan& plan, void* sums, void* ws, hipStream_t s);
 
 }  // namespace iris

@@ -7,25 +7,13 @@
 // lanes hold a block of 128 of an 8-bit output and agree on its scale among themselves.
 #include <algorithm>
 
+#include "column_sums.hpp"
 #include "fp8_act_math.hpp"
 #include "fp8_gemm_few.hpp"
 #include "fp8_gemm_tile.hpp"
 
 namespace iris {
 namespace {
-
-// the sum over the lanes that hold the same columns, `lanes` of them side by side to a row
-template <int LANES>
-__device__ __forceinline__ float same_columns_sum(float v) {
-  static_assert(LANES == 8 || LANES == 16, "");
-  if constexpr (LANES == 8) v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xf, 0xf, true));
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  const auto x = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  v = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
-  const uint32_t t = __builtin_bit_cast(uint32_t, v);
-  const auto y = __builtin_amdgcn_permlane32_swap(t, t, false, false);
-  return __builtin_bit_cast(float, (uint32_t)y[0]) + __builtin_bit_cast(float, (uint32_t)y[1]);
-}
 
 // the matrix that an epilogue reads beside the sums: z, the residual or none
 template <bool BACKWARD, class OUT>
@@ -382,24 +370,6 @@ __global__ __launch_bounds__(256) void fp8_mm_act_join_kernel(Fp8ActArgs a, cons
   }
 }
 
-// dbias = the partial sums, added in order: a wave a quarter of them, 16 loads under way
-template <class OUT>
-__global__ __launch_bounds__(256) void fp8_dbias_kernel(const float* part, int parts, int64_t ldp, int N, OUT* dbias) {
-  __shared__ float red[4][64];
-  const int l = threadIdx.x & 63, c = blockIdx.x * 64 + l, g = threadIdx.x >> 6;
-  float v = 0.0f;
-  for (int i = g; i < parts; i += 64) {
-    float x[16];   // a row past the end reads the last one and drops it: no branch between the loads
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = part[min(i + 4 * k, parts - 1) * ldp + min(c, N - 1)];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v += i + 4 * k < parts ? x[k] : 0.0f;
-  }
-  red[g][l] = v;
-  __syncthreads();
-  if (g == 0 && c < N) narrow((red[0][l] + red[1][l]) + (red[2][l] + red[3][l]), dbias[c]);
-}
-
 constexpr int kJoinRows = 16, kJoinRowsSummed = 64;   // without and with column sums
 
 template <class OUT, int BM, int BN>
@@ -420,18 +390,12 @@ hipError_t launch_tiles(const Fp8ActArgs& a, hipStream_t s) {
 }
 
 template <class OUT>
-hipError_t join_dbias(const float* part, int parts, int64_t ldp, int N, OUT* dbias, hipStream_t s) {
-  hipLaunchKernelGGL((fp8_dbias_kernel<OUT>), dim3((N + 63) / 64), dim3(256), 0, s, part, parts, ldp, N, dbias);
-  return hipGetLastError();
-}
-
-template <class OUT>
 hipError_t run(const Fp8ActArgs& args, const Fp8ActPlan& plan, OUT* dbias, void* ws, hipStream_t s) {
   Fp8ActArgs a = args;
   hipError_t e = hipSuccess;
   a.g.splits = 1;
   a.ldp = (int32_t)fp8_sums_pitch(a.g.N);
-  if (a.g.M == 0) return join_dbias(nullptr, 0, 0, a.g.N, dbias, s);
+  if (a.g.M == 0) return join_columns(nullptr, 0, 0, a.g.N, dbias, s);
   a.dbias_part = plan.parts > 0 ? (float*)((char*)ws + plan.part_at) : nullptr;
   if (plan.sums) {
     const int64_t ldp = a.ldp;
@@ -457,7 +421,7 @@ hipError_t run(const Fp8ActArgs& args, const Fp8ActPlan& plan, OUT* dbias, void*
     e = plan.mm.bm == 128 ? launch_tiles<OUT, 128, 64>(a, s) : launch_tiles<OUT, 64, 64>(a, s);
   }
   if (e != hipSuccess || plan.parts == 0) return e;
-  return join_dbias(a.dbias_part, plan.parts, a.ldp, a.g.N, dbias, s);
+  return join_columns(a.dbias_part, plan.parts, a.ldp, a.g.N, dbias, s);
 }
 
 }  // namespace

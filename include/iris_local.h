@@ -434,9 +434,16 @@ typedef struct iris_drop {
  * out = residual + alpha m x, m the mask above (alpha times the kept value's factor is
  * rounded to 32 bits once). residual may be NULL. All (rows, cols) of `type` (fp16, bf16
  * or fp32). Its own backward pass with respect to x: the same call on out's gradient.
+ * sums: `cols` values of type, or NULL: out's sums over the rows, in 32 bits before out's
+ * rounding; of a gradient, that of a bias which was added to x's rows (the down
+ * projection's in iris_fp8_mm_act with dropout and a residual). workspace: for the sums
+ * alone, at least iris_dropout_workspace_size() bytes, 256-byte aligned, for one call at a
+ * time; NULL: the library's own, as with iris_fp8_mm.
  */
 int iris_dropout(void* out, int64_t ld_out, const void* x, int64_t ldx, const void* residual, int64_t ld_residual,
-                 int32_t type, float alpha, const iris_drop_t* drop, int64_t rows, int64_t cols, void* stream);
+                 int32_t type, float alpha, const iris_drop_t* drop, void* sums, int64_t rows, int64_t cols,
+                 void* workspace, size_t workspace_bytes, void* stream);
+size_t iris_dropout_workspace_size(int64_t rows, int64_t cols);
 
 #define IRIS_NORM_RMS 1   /* v / sqrt(mean(v^2) + eps) */
 #define IRIS_NORM_LAYER 2 /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */

@@ -117,6 +117,37 @@ def test_dropout(rows, cols, pitch, offset, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,cols,pitch,offset", [(1, 1, None, 0), (1, 4096, None, 0), (5, 129, 131, 1), (16, 128, None, 0),
+                                                    (37, 1376, None, 0), (200, 333, 340, 3), (5000, 40, None, 0), (2000, 264, 272, 8)])
+def test_dropout_sums(rows, cols, pitch, offset, dtype):
+    note(f"dropout with sums {rows}x{cols} {dtype} pitch {pitch} offset {offset}")
+    x, xv = on_gpu(sample(rows, cols, rows + cols), dtype, pitch, offset)
+    res, rv = on_gpu(sample(rows, cols, rows + cols + 1), dtype, pitch, offset)
+    for p, residual, alpha in ((0.1, True, 0.7), (0.0, False, 1.0), (0.6, False, 0.5)):
+        m = bref.mask(rows, cols, p, SEED, OFFSET)
+        want, size = alpha * m * xv, np.abs(alpha * m * xv)
+        if residual:
+            want, size = want + rv, size + np.abs(rv)
+        two = []
+        for _ in range(2):
+            out, untouched = out_of(rows, cols, dtype, pitch, offset)
+            sums = torch.full((cols,), float("nan"), dtype=DT[dtype], device="cuda")
+            il.iris_dropout(out, x, il.Dropout(p, SEED, OFFSET), residual=res if residual else None, alpha=alpha, sums=sums)
+            two.append(sums)
+            assert untouched()
+        close(out, want, 3 * bref.EPS32 * size, dtype, (p, residual))
+        close(sums, want.sum(0), ((rows + 32) * bref.EPS32 * size).sum(0), dtype, "sums")
+        assert torch.equal(*two)
+    ws = torch.full((il.iris_dropout_workspace_size(rows, cols),), 0xFF, dtype=torch.uint8, device="cuda")
+    il.iris_dropout(out, x, il.Dropout(p, SEED, OFFSET), alpha=alpha, sums=two[0], workspace=ws)
+    assert torch.equal(*two)
+    none = torch.empty((0, cols), dtype=DT[dtype], device="cuda")
+    il.iris_dropout(torch.empty_like(none), none, None, sums=sums)
+    assert bool((sums == 0).all())
+
+
+@pytest.mark.gpu
 def test_dropout_drops_what_is_not_finite_and_keeps_the_rest_so():
     x = torch.full((64, 256), float("inf"), dtype=torch.bfloat16, device="cuda")
     x[::2] = float("nan")
@@ -542,8 +573,10 @@ def block_step():
     q = fresh(33, 1000)
     out["codes"] = q.codes.view(torch.uint8)
     drop = il.Dropout(0.2, 1, 2)
+    out |= {"dropped": torch.empty_like(n), "sums": torch.empty(1376, dtype=torch.bfloat16, device="cuda")}
 
     def run():
+        il.iris_dropout(out["dropped"], t["y"], drop, sums=out["sums"])
         il.iris_block_norm(t["x"], norm, y=t["y"], r=r, n=n, stats=stats)
         il.iris_block_norm_bwd(out["dx"], r, stats, norm, dn=n, dr=r, y=t["y"], dy=out["dy"], dpre_w=out["dpre_w"],
                                dpost_w=out["dpost_w"], dgate=out["dgate"])
