@@ -135,12 +135,6 @@ class _Norm(ctypes.Structure):
                 ("rows_per_gate", ctypes.c_int64), ("drop", ctypes.POINTER(_Drop))]
 
 
-class _Epilogue(ctypes.Structure):
-    _fields_ = [("act", ctypes.c_int32), ("alpha", ctypes.c_float), ("bias", ctypes.c_void_p), ("z", ctypes.c_void_p),
-                ("ld_z", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
-                ("q", ctypes.POINTER(_Fp8)), ("drop", ctypes.POINTER(_Drop))]
-
-
 class _PredictParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in (
         "gemm_tflops_per_cu", "tile_overhead_us", "comm_gbps_per_cu", "comm_gbps_chip", "unit_overhead_us",
@@ -180,7 +174,7 @@ def _load() -> ctypes.CDLL:
         "iris_block_norm": [vp, i64, vp, i64, f8, vp, vp, i64, vp, i64, norm, i64, i64, vp],
         "iris_block_norm_bwd": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, norm, i64, i64,
                                 vp, sz, vp],
-        "iris_fp8_mm_act": [vp, i32, i64, f8, f8, ctypes.POINTER(_Epilogue), i64, i64, i64, vp, sz, vp],
+        "iris_fp8_mm_act": [vp, i32, i64, vp, i64, f8, f8, f8, vp, i32, f32, drop, vp, i64, i64, i64, i64, vp, sz, vp],
         "iris_fp8_mm_act_bwd": [vp, i32, i64, vp, f8, f8, vp, i64, i32, f32, drop, i64, i64, i64, vp, sz, vp],
         "iris_grid_size": [ctypes.c_int32, cfgp],
         "iris_tune_gemm_wgs": [ctypes.POINTER(_OpArgs), ctypes.POINTER(i32), i32, i32, i32,
@@ -766,21 +760,17 @@ def _any_plain(t, name: str, shape, kind, dev: int):
     return t.data_ptr(), (ld if shape[0] > 1 else shape[1])
 
 
-def _vector(t, name: str, N: int, kind, dev: int):
-    if t is None:
-        return None
-    _want_shape(t, (N,), name)
-    if t.dtype != kind:
+def _vector(t, name: str, n: int, kind, dev: int):
+    """Pointer of a contiguous vector of one type."""
+    if not isinstance(t, torch.Tensor) or t.shape != (n,):
+        _want_shape(t, (n,), name)
+    if t.dtype is not kind:
         raise TypeError(f"{name} must be {str(kind)[6:]}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
+    if dev < 0 or t.get_device() != dev:
         raise _elsewhere(name, t.get_device(), dev)
     return t.data_ptr()
-
-
-def _call_stream(stream, dev: int):
-    return _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev)
 
 
 def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float = 1.0, sums=None, workspace=None,
@@ -789,7 +779,9 @@ def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float
     pitch; m is dropout's mask. On out's gradient it is its own backward pass; `sums`
     (cols values of x's dtype) then receives the gradient of a bias of x: out's sums over
     the rows."""
-    shape = rows, cols = _shape2(x, "x")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _shape2(x, "x")
+    shape = rows, cols = x.shape
     dev, dtype = x.get_device(), x.dtype
     kind = _FP8_TYPES.get(dtype)
     if kind is None:
@@ -797,8 +789,10 @@ def iris_dropout(out, x, dropout: Optional[Dropout], residual=None, alpha: float
     if out is None:
         raise ValueError("out is required")
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
-    st = _lib.iris_dropout(*_any_plain(out, "out", shape, dtype, dev), *_any_plain(x, "x", shape, dtype, dev),
-                           *_any_plain(residual, "residual", shape, dtype, dev), kind, alpha, _drop(dropout, dev),
+    op, old = _any_plain(out, "out", shape, dtype, dev)
+    xp, ldx = _any_plain(x, "x", shape, dtype, dev)
+    rp, ldr = (None, 0) if residual is None else _any_plain(residual, "residual", shape, dtype, dev)
+    st = _lib.iris_dropout(op, old, xp, ldx, rp, ldr, kind, alpha, None if dropout is None else _drop(dropout, dev),
                            None if sums is None else _vector(sums, "sums", cols, dtype, dev), rows, cols, ws, wsb,
                            _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
@@ -919,30 +913,33 @@ def iris_block_norm(x, norm: BlockNorm, y=None, r=None, n=None, q: Optional[Fp8]
     bits (n), in 8 (q) or both; without y, n = norm(x). x, r: float32 or the dtype of y
     and n (float16, bfloat16); stats (rows, 4) float32 receives what the backward pass
     needs. Outputs that are not wanted are None."""
-    shape = rows, cols = _shape2(x, "x")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _shape2(x, "x")
+    shape = rows, cols = x.shape
     dev, dtype = x.get_device(), x.dtype
     kind = _norm_kind(norm, dtype, y, n)
     norm._for(rows, cols, dev)
     p = norm._structs.get((kind, dtype)) or norm._struct(kind, dtype)
-    st = _lib.iris_block_norm(*_any_plain(r, "r", shape, dtype, dev), *_any_plain(n, "n", shape, kind, dev),
-                              None if q is None else _fp8(q, shape, "q", dev),
-                              None if stats is None else _sums(stats, "stats", (rows, 4), dev),
-                              *_any_plain(x, "x", shape, dtype, dev), *_any_plain(y, "y", shape, kind, dev), p, rows, cols,
+    sp = None if stats is None else _sums(stats, "stats", (rows, 4), dev)
+    xp, ldx = _any_plain(x, "x", shape, dtype, dev)
+    yp, ldy = (None, 0) if y is None else _any_plain(y, "y", shape, kind, dev)
+    rp, ldr = (None, 0) if r is None else _any_plain(r, "r", shape, dtype, dev)
+    np, ldn = (None, 0) if n is None else _any_plain(n, "n", shape, kind, dev)
+    st = _lib.iris_block_norm(rp, ldr, np, ldn, None if q is None else _fp8(q, shape, "q", dev),
+                              sp, xp, ldx, yp, ldy, p, rows, cols,
                               _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
 
 def _sums(t, name: str, shape, dev: int):
-    if t is None:
-        return None
     if not isinstance(t, torch.Tensor) or t.shape != shape:
         _want_shape(t, shape, name)
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
+    if dev < 0 or t.get_device() != dev:
         raise _elsewhere(name, t.get_device(), dev)
     return t.data_ptr()
 
@@ -962,10 +959,13 @@ def iris_block_norm_bwd(dx, r, stats, norm: BlockNorm, dn=None, dr=None, y=None,
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
     st = _lib.iris_block_norm_bwd(
         *_any_plain(dx, "dx", shape, dtype, dev), *_any_plain(dy, "dy", shape, kind, dev),
-        _sums(dpre_w, "dpre_w", (cols,), dev), _sums(dpre_b, "dpre_b", (cols,), dev), _sums(dpost_w, "dpost_w", (cols,), dev),
-        _sums(dpost_b, "dpost_b", (cols,), dev), None if dgate is None else _sums(dgate, "dgate", norm.gate.shape, dev),
+        None if dpre_w is None else _sums(dpre_w, "dpre_w", (cols,), dev),
+        None if dpre_b is None else _sums(dpre_b, "dpre_b", (cols,), dev),
+        None if dpost_w is None else _sums(dpost_w, "dpost_w", (cols,), dev),
+        None if dpost_b is None else _sums(dpost_b, "dpost_b", (cols,), dev), None if dgate is None else _sums(dgate, "dgate", norm.gate.shape, dev),
         *_any_plain(dn, "dn", shape, kind, dev), *_any_plain(dr, "dr", shape, dtype, dev), *_any_plain(r, "r", shape, dtype, dev),
-        *_any_plain(y, "y", shape, kind, dev), None if stats is None else _sums(stats, "stats", (rows, 4), dev), p, rows, cols, ws, wsb, _call_stream(stream, dev))
+        *_any_plain(y, "y", shape, kind, dev), None if stats is None else _sums(stats, "stats", (rows, 4), dev), p, rows, cols,
+        ws, wsb, _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -1004,22 +1004,21 @@ def iris_fp8_mm_act(C, A: Fp8, B: Fp8, act="none", bias=None, z=None, residual=N
     activation. act: "none", "relu", "gelu", "gelu_tanh", "silu". Precision: as iris_fp8_mm."""
     M, N, K, dev, code = _mm_operands(A, B, act)
     shape = (M, N)
-    kind = dtype
-    for t in (C, z, residual, bias):
-        if t is not None and (kind is None or t is C):
-            kind = getattr(t, "dtype", None)
-    kind = torch.float16 if kind is None else kind
+    if C is not None:
+        kind = getattr(C, "dtype", None)
+    else:
+        kind = dtype or next((getattr(t, "dtype", None) for t in (z, residual, bias) if t is not None), torch.float16)
     c_type = _FP8_TYPES.get(kind)
     if c_type is None:
         raise TypeError("C must be one of float16, bfloat16, float32")
-    ap, bp = _fp8(A, A.shape, "A", dev), _fp8(B, B.shape, "B", dev)
-    cp, ldc = _any_plain(C, "C", shape, kind, dev)
-    zp, ldz = _any_plain(z, "z", shape, kind, dev)
-    rp, ldr = _any_plain(residual, "residual", shape, kind, dev)
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
-    e = _Epilogue(code, alpha, _vector(bias, "bias", N, kind, dev), zp, ldz, rp, ldr,
-                  None if q is None else _fp8(q, shape, "q", dev), _drop(dropout, dev))
-    st = _lib.iris_fp8_mm_act(cp, c_type, ldc, ap, bp, e, M, N, K, ws, wsb, _call_stream(stream, dev))
+    cp, ldc = (None, 0) if C is None else _any_plain(C, "C", shape, kind, dev)
+    zp, ldz = (None, 0) if z is None else _any_plain(z, "z", shape, kind, dev)
+    rp, ldr = (None, 0) if residual is None else _any_plain(residual, "residual", shape, kind, dev)
+    st = _lib.iris_fp8_mm_act(cp, c_type, ldc, zp, ldz, None if q is None else _fp8(q, shape, "q", dev), A._p,
+                              _fp8(B, (N, K), "B", dev), None if bias is None else _vector(bias, "bias", N, kind, dev), code, alpha,
+                              None if dropout is None else _drop(dropout, dev), rp, ldr, M, N, K, ws, wsb,
+                              _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 
@@ -1037,12 +1036,12 @@ def iris_fp8_mm_act_bwd(C, A: Fp8, B: Fp8, z, act, alpha: float = 1.0, dropout: 
     c_type = _FP8_TYPES.get(kind)
     if c_type is None:
         raise TypeError("C must be one of float16, bfloat16, float32")
-    ap, bp = _fp8(A, A.shape, "A", dev), _fp8(B, B.shape, "B", dev)
-    cp, ldc = _any_plain(C, "C", shape, kind, dev)
     ws, wsb = (None, 0) if workspace is None else _fp8_ws(workspace, dev)
-    st = _lib.iris_fp8_mm_act_bwd(cp, c_type, ldc,
-                                  _vector(dbias, "dbias", N, kind, dev), ap, bp, *_any_plain(z, "z", shape, kind, dev), code,
-                                  alpha, _drop(dropout, dev), M, N, K, ws, wsb, _call_stream(stream, dev))
+    cp, ldc = _any_plain(C, "C", shape, kind, dev)
+    st = _lib.iris_fp8_mm_act_bwd(cp, c_type, ldc, None if dbias is None else _vector(dbias, "dbias", N, kind, dev), A._p,
+                                  _fp8(B, (N, K), "B", dev), *_any_plain(z, "z", shape, kind, dev), code, alpha,
+                                  None if dropout is None else _drop(dropout, dev), M, N, K, ws, wsb,
+                                  _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))
     if st:
         _check(st)
 

@@ -332,39 +332,40 @@ size_t iris_fp8_mm_act_workspace_size(int64_t M, int64_t N, int64_t K, int32_t c
   return 0;
 }
 
-int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B, const iris_epilogue_t* e,
-                    int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) try {
+int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, void* z, int64_t ld_z, const iris_fp8_t* q, const iris_fp8_t* A,
+                    const iris_fp8_t* B, const void* bias, int32_t act, float alpha, const iris_drop_t* drop, const void* residual,
+                    int64_t ld_residual, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                    void* stream) try {
   iris::set_error(IRIS_OK, "");
   int st;
-  if (!e) return fail(IRIS_ERR_INVALID_ARG, "epilogue is NULL");
-  if ((st = check_mm(c_type, A, B, M, N, K, e->act))) return st;
-  if (M > 0 && N > 0 && !C && !e->q) return fail(IRIS_ERR_INVALID_ARG, "C and q are both NULL");
-  iris::DropArgs drop;
-  if ((st = check_optional(C, c_type, ldc, M, N, "C")) || (st = check_optional(e->z, c_type, e->ld_z, M, N, "z")) ||
-      (st = check_optional(e->residual, c_type, e->ld_residual, M, N, "residual")) || (st = check_vector(e->bias, c_type, "bias")) ||
-      (st = check_drop(e->drop, e->alpha, &drop)))
+  if ((st = check_mm(c_type, A, B, M, N, K, act))) return st;
+  if (M > 0 && N > 0 && !C && !q) return fail(IRIS_ERR_INVALID_ARG, "C and q are both NULL");
+  iris::DropArgs d;
+  if ((st = check_optional(C, c_type, ldc, M, N, "C")) || (st = check_optional(z, c_type, ld_z, M, N, "z")) ||
+      (st = check_optional(residual, c_type, ld_residual, M, N, "residual")) || (st = check_vector(bias, c_type, "bias")) ||
+      (st = check_drop(drop, alpha, &d)))
     return st;
-  if (e->q && (st = check_blocks1(e->q, M, N, "q"))) return st;
+  if (q && (st = check_blocks1(q, M, N, "q"))) return st;
   if (M == 0 || N == 0) return IRIS_OK;
-  const iris::Fp8ActPlan plan = iris::fp8_mm_act_plan(M, N, K, c_type == IRIS_TYPE_FP32, e->q != nullptr, false);
+  const iris::Fp8ActPlan plan = iris::fp8_mm_act_plan(M, N, K, c_type == IRIS_TYPE_FP32, q != nullptr, false);
   if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes))) return st;
-  if ((st = check_distinct({{C, "C", true}, {e->z, "z", true}, {e->q, "q", true}, {workspace, "workspace", true}, {A, "A", false},
-                            {B, "B", false}, {e->bias, "bias", false}, {e->residual, "residual", false},
-                            {e->drop ? (const void*)e->drop->offset_at : nullptr, "offset_at", false}})))
+  if ((st = check_distinct({{C, "C", true}, {z, "z", true}, {q, "q", true}, {workspace, "workspace", true}, {A, "A", false},
+                            {B, "B", false}, {bias, "bias", false}, {residual, "residual", false},
+                            {drop ? (const void*)drop->offset_at : nullptr, "offset_at", false}})))
     return st;
-  iris::Fp8ActArgs a = mm_args(C, c_type, ldc, A, B, M, N, K, e->act);
-  a.g.bias = e->bias;
-  a.z = e->z;
-  a.ldz = (int32_t)e->ld_z;
-  a.residual = e->residual;
-  a.ldr = (int32_t)e->ld_residual;
-  a.q = mat(e->q);
-  a.drop = drop;
-  a.whole = N % 8 == 0 && rows16_or_none(C, ldc, c_type, M) && rows16_or_none(e->z, e->ld_z, c_type, M) &&
-            rows16_or_none(e->residual, e->ld_residual, c_type, M);
+  iris::Fp8ActArgs a = mm_args(C, c_type, ldc, A, B, M, N, K, act);
+  a.g.bias = bias;
+  a.z = z;
+  a.ldz = (int32_t)ld_z;
+  a.residual = residual;
+  a.ldr = (int32_t)ld_residual;
+  a.q = mat(q);
+  a.drop = d;
+  a.whole = N % 8 == 0 && rows16_or_none(C, ldc, c_type, M) && rows16_or_none(z, ld_z, c_type, M) &&
+            rows16_or_none(residual, ld_residual, c_type, M);
   return run_mm(a, plan, nullptr, workspace, stream, "iris_fp8_mm_act");
-} catch (const std::exception& error) {
-  return caught(error);
+} catch (const std::exception& e) {
+  return caught(e);
 }
 
 int iris_fp8_mm_act_bwd(void* C, int32_t c_type, int64_t ldc, void* dbias, const iris_fp8_t* A, const iris_fp8_t* B, const void* z,

@@ -518,20 +518,9 @@ size_t iris_block_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  * the value before the activation, for the backward pass. q: C in 8 bits too (block 1,
  * from 32 bits), or instead of C (C NULL; c_type then is that of the others).
  */
-typedef struct iris_epilogue {
-  int32_t act;
-  float alpha;
-  const void* bias;
-  void* z;
-  int64_t ld_z;
-  const void* residual;
-  int64_t ld_residual;
-  const iris_fp8_t* q;
-  const iris_drop_t* drop;
-} iris_epilogue_t;
-
-int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, const iris_fp8_t* A, const iris_fp8_t* B,
-                    const iris_epilogue_t* epilogue, int64_t M, int64_t N, int64_t K, void* workspace,
+int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, void* z, int64_t ld_z, const iris_fp8_t* q, const iris_fp8_t* A,
+                    const iris_fp8_t* B, const void* bias, int32_t act, float alpha, const iris_drop_t* drop,
+                    const void* residual, int64_t ld_residual, int64_t M, int64_t N, int64_t K, void* workspace,
                     size_t workspace_bytes, void* stream);
 
 /*

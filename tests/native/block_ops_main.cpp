@@ -126,9 +126,8 @@ int backward() {
 }
 const iris_fp8_t A{(void*)0x1000000, (void*)0x2000000, 256, 4, 1}, B{(void*)0x3000000, (void*)0x4000000, 256, 4, 128};
 int product() {
-  iris_epilogue_t e{};
-  e.alpha = 1.0f;
-  return iris_fp8_mm_act((void*)0x500000, IRIS_TYPE_FP16, 64, &A, &B, &e, 16, 64, 256, nullptr, 0, nullptr);
+  return iris_fp8_mm_act((void*)0x500000, IRIS_TYPE_FP16, 64, nullptr, 0, nullptr, &A, &B, nullptr, IRIS_ACT_GELU, 1.0f, nullptr,
+                         nullptr, 0, 16, 64, 256, nullptr, 0, nullptr);
 }
 int product_bwd() {
   return iris_fp8_mm_act_bwd((void*)0x500000, IRIS_TYPE_FP16, 64, nullptr, &A, &B, (void*)0x600000, 64, IRIS_ACT_SILU, 1.0f, nullptr,

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import gemm_collective_tile_amd as il
-from gemm_collective_tile_amd import _Drop, _Epilogue, _Fp8, _lib, _Norm
+from gemm_collective_tile_amd import _Drop, _Fp8, _lib, _Norm
 
 P, Q, R, S, ODD = 0x100000, 0x200000, 0x300000, 0x400000, 0x100001
 INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = 1, 2, 4, 7
@@ -181,14 +181,12 @@ def test_block_norm_bwd_status_codes():
     assert max(il.iris_block_norm_bwd_workspace_size(r, c) for r in (1, 300, 1 << 30) for c in (1, 4096, 8192, 16384)) <= 128 << 20
 
 
-def call_mm(C=P, t=2, A=None, B=None, M=6, N=30, K=200, ws=None, wsb=0, ldc=None, **kw):
+def call_mm(C=P, t=2, A=None, B=None, M=6, N=30, K=200, ws=None, wsb=0, ldc=None, z=None, ld_z=30, q=None, bias=None, act=2,
+            alpha=1.0, drop=None, residual=None, ld_residual=30):
     A = _Fp8(0x1000000, 0x2000000, 208, 4, 1) if A is None else A
     B = _Fp8(0x3000000, 0x4000000, 208, 4, 128) if B is None else B
-    e = _Epilogue(act=2, alpha=1.0)
-    for k, v in kw.items():
-        setattr(e, k, v)
-    return _lib.iris_fp8_mm_act(C, t, N if ldc is None else ldc, ctypes.byref(A), ctypes.byref(B), ctypes.byref(e), M, N, K, ws, wsb,
-                                None)
+    return _lib.iris_fp8_mm_act(C, t, N if ldc is None else ldc, z, ld_z, q, ctypes.byref(A), ctypes.byref(B), bias, act, alpha, drop,
+                                residual, ld_residual, M, N, K, ws, wsb, None)
 
 
 def test_mm_act_status_codes():
