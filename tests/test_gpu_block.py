@@ -358,6 +358,87 @@ def test_block_norm_gates_of_every_length(rows, every):
 
 
 @pytest.mark.gpu
+def test_block_norm_of_more_rows_than_a_launch_holds():
+    """2^20 rows and more go in several launches: the mask's and the gate's rows go on. The backward pass takes them at once."""
+    rows, cols, every, part = (1 << 20) + 77, 24, 1000, 1 << 20
+    note("block norm of 2^20 rows")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x, y = (torch.randn((rows, cols), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    gate = torch.randn((-(-rows // every), cols), device="cuda", generator=g)
+    norm = il.BlockNorm(gate=gate, rows_per_gate=every, dropout=il.Dropout(0.2, 5, 6))
+    r, n, stats, q = torch.empty_like(x), torch.empty_like(x), torch.empty((rows, 4), device="cuda"), il.iris_fp8_empty(rows, cols)
+    il.iris_block_norm(x, norm, y=y, r=r, n=n, q=q, stats=stats)
+    dx, dy, dgate, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gate), torch.empty(cols, device="cuda")
+    il.iris_block_norm_bwd(dx, r, stats, norm, dn=n, y=y, dy=dy, dgate=dgate, dpre_w=dw)
+    for at in (0, 512 * 1024, part - 40, rows - 80):
+        some = slice(at, at + 80)
+        m = bref.mask(80, cols, 0.2, 5, 6, row0=at)
+        wide = values(gate)[np.arange(at, at + 80) // every]
+        want, off = bref.block_norm(values(x[some]), values(y[some]), gate=wide, m=m)
+        close(r[some], want["r"], off["r"], "bf16", "r")
+        close(n[some], want["n"], off["n"], "bf16", "n")
+        close(stats[some], want["stats"], off["stats"], "fp32", "stats")
+        part8 = il.Fp8(q.codes[some], q.scales[some])
+        got = ref.values(*parts(part8))
+        assert np.all(np.abs(got - want["n"]) <= 2.0 ** -4 * np.abs(want["n"]) + 2.0 ** -10 * np.abs(want["n"]).max() + off["n"])
+        back, boff = bref.block_norm_bwd(values(r[some]), values(stats[some]), values(n[some]), None, values(y[some]), gate=wide, m=m,
+                                         group=np.arange(80))
+        close(dx[some], back["dx"], boff["dx"], "bf16", "dx")
+        close(dy[some], back["dy"], boff["dy"], "bf16", "dy")
+    # gates of the first rows, of rows that two workgroups share, and the last, shorter one
+    t = values(dx)
+    for k in (0, 1, 2, 3, 500, gate.shape[0] - 1):
+        rows_k = slice(k * every, min((k + 1) * every, rows))
+        m = bref.mask(rows_k.stop - rows_k.start, cols, 0.2, 5, 6, row0=rows_k.start)
+        each = m * t[rows_k] * values(y[rows_k])
+        # dx was rounded to bf16, half a step of each term
+        bound = (np.abs(each) * (2.0 ** -8 + 1200 * bref.EPS32)).sum(0)
+        assert np.all(np.abs(values(dgate[k]) - each.sum(0)) <= bound), k
+    hat = (values(r) - values(stats)[:, 2:3]) * values(stats)[:, 3:]
+    each = values(n) * hat
+    assert np.all(np.abs(values(dw) - each.sum(0)) <= np.abs(each).sum(0) * (2048 + 600) * bref.EPS32)
+
+
+@pytest.mark.gpu
+def test_column_sums_in_graphs_side_by_side_in_workspaces_of_their_own():
+    """Two graphs that replay at the same time on two streams, each with its own workspace."""
+    graphs, wanted = [], []
+    for k in range(2):
+        t, v, plain, norm, group, stream = norm_case(900, 2048, NORM_WAYS[0], "bf16", 40 + k)
+        stats = torch.ones((900, 4), device="cuda")
+        dw, dg = torch.empty(2048, device="cuda"), torch.empty(2048, device="cuda")
+        ws = torch.empty(il.iris_block_norm_bwd_workspace_size(900, 2048), dtype=torch.uint8, device="cuda")
+        out, sums = torch.empty_like(t["y"]), torch.empty(2048, dtype=torch.bfloat16, device="cuda")
+        ws2 = torch.empty(il.iris_dropout_workspace_size(900, 2048), dtype=torch.uint8, device="cuda")
+
+        def run(t=t, norm=norm, stats=stats, dw=dw, dg=dg, ws=ws, out=out, sums=sums, ws2=ws2):
+            il.iris_block_norm_bwd(None, t["x"], stats, norm, dn=t["y"], y=t["y"], dpre_w=dw, dgate=dg, workspace=ws)
+            il.iris_dropout(out, t["y"], norm.dropout, sums=sums, workspace=ws2)
+        run()
+        torch.cuda.synchronize()
+        wanted.append([x.clone() for x in (dw, dg, sums)])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(10):
+                run()
+        graphs.append((g, s, (dw, dg, sums), run))   # run holds what the graph reads
+    for _ in range(4):
+        for _, _, outs, _ in graphs:
+            for x in outs:
+                x.zero_()
+        torch.cuda.synchronize()
+        for g, s, _, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, _, outs, _), want in zip(graphs, wanted):
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.gpu
 def test_block_norm_of_zeros_and_of_what_is_not_finite():
     """A row of zeros has a finite norm (eps); NaN and infinities stay in their row."""
     x = torch.randn((9, 600), device="cuda").to(torch.float16)
