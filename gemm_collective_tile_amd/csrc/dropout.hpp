@@ -56,20 +56,27 @@ struct Drop {
     }
     return u32x4{a, b, c, d};
   }
-  // v: columns 8 piece .. + 7 of a row. What is dropped becomes 0, whatever it was.
-  __device__ __forceinline__ void apply(uint32_t row, uint32_t piece, float (&v)[8]) const {
+  // v: columns 8 piece .. + 7 of U rows. What is dropped becomes 0, whatever it was.
+  template <int U>
+  __device__ __forceinline__ void apply(const int (&row)[U], uint32_t piece, float (&v)[U][8]) const {
     if (threshold == 0) {
       if (scale == 1.0f) return;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      for (int k = 0; k < 8 * U; ++k) v[k / 8][k % 8] *= scale;
       return;
     }
-    const u32x4 w = bits(row, piece);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
-      v[i] = u >= threshold ? v[i] * scale : 0.0f;
+    for (int r = 0; r < U; ++r) {
+      const u32x4 w = bits((uint32_t)row[r], piece);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
+        v[r][i] = u >= threshold ? v[r][i] * scale : 0.0f;
+      }
     }
+  }
+  __device__ __forceinline__ void apply(uint32_t row, uint32_t piece, float (&v)[8]) const {
+    apply<1>({(int)row}, piece, *(float (*)[1][8])&v);
   }
   __device__ __forceinline__ float apply(uint32_t row, uint32_t col, float v) const {
     if (threshold == 0) return v * scale;

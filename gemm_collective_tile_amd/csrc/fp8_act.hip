@@ -31,14 +31,14 @@ struct Beside {
 template <class OUT>
 struct PutRagged {
   static constexpr bool WHOLE = false;
-  const Fp8ActArgs& a;
+  const Fp8ActArgs* a;
   int m, n;
   bool on;
   __device__ __forceinline__ void z(const float (&v)[8]) const {
-    if (on) store8<false>((OUT*)a.z + (int64_t)m * a.ldz, n, a.g.N, v);
+    if (on) store8<false>((OUT*)a->z + (int64_t)m * a->ldz, n, a->g.N, v);
   }
   __device__ __forceinline__ void c(const float (&v)[8]) const {
-    if (on) store8<false>((OUT*)a.g.C + (int64_t)m * a.g.ldc, n, a.g.N, v);
+    if (on) store8<false>((OUT*)a->g.C + (int64_t)m * a->g.ldc, n, a->g.N, v);
   }
 };
 // whole, aligned pieces through buffers, which drop a lane's that is off: no branch
@@ -61,48 +61,75 @@ struct PutWhole {
   __device__ __forceinline__ void c(const float (&v)[8]) const { put(c_rows, c_at, v); }
 };
 
-// 8 sums of row m, columns n .. n + 7, through the epilogue; on: they lie inside C. All
-// 16 lanes of a block of 128 columns call it together where q is wanted. `beside`: their
-// values of z (backward) or of the residual, in memory's form.
-template <bool BACKWARD, class OUT, class PUT>
-__device__ __forceinline__ void finish8(const Fp8ActArgs& a, const Drop& drop, int m, int n, bool on, const float (&bias)[8],
-                                        const Raw8<OUT>& beside, const PUT& put, float (&v)[8], float (&sums)[8]) {
+// U times 8 sums, of rows m[u], columns n .. n + 7, through the epilogue; on: they lie
+// inside C. All 16 lanes of a block of 128 columns call it together where q is wanted.
+// `beside`: their values of z (backward) or of the residual, in memory's form. Each step
+// is taken for all U before the next: what is not wanted is branched over once for them
+// (with one wave a SIMD a branch taken costs as much as seven instructions: 8192 x 11008 x
+// 4096 without an activation 356 us with U = 1, 336 with 4, as the plain product).
+template <bool BACKWARD, class OUT, class PUT, int U>
+__device__ __forceinline__ void finish(const Fp8ActArgs& a, const Drop& drop, const int (&m)[U], int n, const bool (&on)[U],
+                                       const float (&bias)[8], const Raw8<OUT> (&beside)[U], const PUT (&put)[U],
+                                       float (&v)[U][8], float (&sums)[8]) {
   const int N = a.g.N;
   if constexpr (BACKWARD) {
-    float z[8];
-    beside.values(z);
+    float z[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) beside[u].values(z[u]);
     times_slope(a.act, z, v);
-    drop.apply((uint32_t)m, (uint32_t)n >> 3, v);
+    drop.apply(m, (uint32_t)n >> 3, v);
     if (a.dbias_part) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[i] += on ? v[i] : 0.0f;
+      for (int u = 0; u < U; ++u) {
+        if (__all(on[u])) {   // all but the last tiles: no select for each value
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sums[i] += v[u][i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sums[i] += on[u] ? v[u][i] : 0.0f;
+        }
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += bias[i];
-    if (a.z) put.z(v);
-    activate(a.act, v);
-    drop.apply((uint32_t)m, (uint32_t)n >> 3, v);
-    if (a.residual) {
-      float r[8];
-      beside.values(r);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
+      for (int i = 0; i < 8; ++i) v[u][i] += bias[i];
+    if (a.z) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) put[u].z(v[u]);
+    }
+    activate(a.act, v);
+    drop.apply(m, (uint32_t)n >> 3, v);
+    if (a.residual) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float r[8];
+        beside[u].values(r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] += r[i];
+      }
     }
   }
-  if (BACKWARD || a.g.C) put.c(v);
-  if (!BACKWARD && a.q.codes) {
-    // what lies outside has no say in the scale, and its codes go nowhere
-    if constexpr (!PUT::WHOLE) {
+  if (BACKWARD || a.g.C) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = n + i < N ? v[i] : 0.0f;
-    }
-    const uint32_t s = scale_byte(group_max<16>(piece_amax(v) & on_mask(on)));
-    uint32_t w[2];
-    encode_piece(v, scale_value(s), w);
-    if (on) {
-      store_codes<PUT::WHOLE, 8>(a.q.codes + (int64_t)m * a.q.ld, 0, n, N, w);
-      if (n % kFp8Block == 0) a.q.scales[(int64_t)m * a.q.lds + n / kFp8Block] = (uint8_t)s;
+    for (int u = 0; u < U; ++u) put[u].c(v[u]);
+  }
+  if (!BACKWARD && a.q.codes) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // what lies outside has no say in the scale, and its codes go nowhere
+      if constexpr (!PUT::WHOLE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = n + i < N ? v[u][i] : 0.0f;
+      }
+      const uint32_t s = scale_byte(group_max<16>(piece_amax(v[u]) & on_mask(on[u])));
+      uint32_t w[2];
+      encode_piece(v[u], scale_value(s), w);
+      if (on[u]) {
+        store_codes<PUT::WHOLE, 8>(a.q.codes + (int64_t)m[u] * a.q.ld, 0, n, N, w);
+        if (n % kFp8Block == 0) a.q.scales[(int64_t)m[u] * a.q.lds + n / kFp8Block] = (uint8_t)s;
+      }
     }
   }
 }
@@ -150,7 +177,7 @@ __device__ __forceinline__ void wait_vmem(int n) {
 // the compiler, and the wait counts the stores of C that are surely behind them. Else
 // they wait in registers, and are waited for as the compiler does it.
 template <class OUT, int BM, int BN, bool WHOLE, bool BACKWARD>
-__global__ __launch_bounds__(256) void fp8_mm_act_kernel(Fp8ActArgs a) {
+__global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void fp8_mm_act_kernel(Fp8ActArgs a) {
   using T = Tile<BM, BN>;
   constexpr bool EXACT = sizeof(OUT) == 4;
   __shared__ __align__(16) char lds[T::LDS];
@@ -244,37 +271,44 @@ __global__ __launch_bounds__(256) void fp8_mm_act_kernel(Fp8ActArgs a) {
     }
     strip_barrier<SHARED>();
     const int top = first_row(i);
-    PutWhole<OUT> whole;
-    if constexpr (WHOLE) {
-      whole.c_rows = make_rsrc((const OUT*)a.g.C + (int64_t)top * a.g.ldc + nw, 0x7fffffffu);
-      whole.z_rows = make_rsrc((const OUT*)a.z + (int64_t)top * a.ldz + nw, 0x7fffffffu);
-    }
-    // the next pass's values are on their way while this one's go through the epilogue
-    float next[8];
-    Raw8<OUT> next_raw;
-    const auto read = [&](int p) {
-      __builtin_memcpy(next, strip + (lane_row + RPI * p) * PITCH + c, sizeof next);
+    const __amdgpu_buffer_rsrc_t c_rows = make_rsrc((const OUT*)a.g.C + (int64_t)top * a.g.ldc + nw, 0x7fffffffu);
+    const __amdgpu_buffer_rsrc_t z_rows = make_rsrc((const OUT*)a.z + (int64_t)top * a.ldz + nw, 0x7fffffffu);
+    constexpr int U = PASSES < 4 ? PASSES : 4;
+#pragma unroll 1
+    for (int p0 = 0; p0 < PASSES; p0 += U) {
+      int m[U];
+      bool on[U];
+      float v[U][8];
+      Raw8<OUT> here[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = lane_row + RPI * (p0 + u);
+        m[u] = top + row;
+        on[u] = m[u] < a.g.M && n < a.g.N;
+        __builtin_memcpy(v[u], strip + row * PITCH + c, sizeof v[u]);
+      }
       if (beside.at) {
 #pragma unroll
-        for (int h = 0; h < PIECES; ++h) __builtin_memcpy(next_raw.w + 4 * h, raw_at + (p * PIECES + h) * 1024, 16);
-      }
-    };
-    read(0);
-#pragma unroll 4
-    for (int p = 0; p < PASSES; ++p) {
-      const int row = lane_row + RPI * p, m = top + row;
-      const bool on = m < a.g.M && n < a.g.N;
-      float v[8];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = next[e];
-      const Raw8<OUT> here = next_raw;
-      read(min(p + 1, PASSES - 1));
+          for (int h = 0; h < PIECES; ++h) __builtin_memcpy(here[u].w + 4 * h, raw_at + ((p0 + u) * PIECES + h) * 1024, 16);
+      }
       if constexpr (WHOLE) {
-        whole.c_at = on ? ((uint32_t)row * (uint32_t)a.g.ldc + c) * (uint32_t)sizeof(OUT) : kOob;
-        whole.z_at = on ? ((uint32_t)row * (uint32_t)a.ldz + c) * (uint32_t)sizeof(OUT) : kOob;
-        finish8<BACKWARD, OUT>(a, drop, m, n, on, bias, here, whole, v, sums);
+        PutWhole<OUT> put[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t row = (uint32_t)(m[u] - top);
+          put[u].c_rows = c_rows;
+          put[u].z_rows = z_rows;
+          put[u].c_at = on[u] ? (row * (uint32_t)a.g.ldc + c) * (uint32_t)sizeof(OUT) : kOob;
+          put[u].z_at = on[u] ? (row * (uint32_t)a.ldz + c) * (uint32_t)sizeof(OUT) : kOob;
+        }
+        finish<BACKWARD, OUT>(a, drop, m, n, on, bias, here, put, v, sums);
       } else {
-        finish8<BACKWARD, OUT>(a, drop, m, n, on, bias, here, PutRagged<OUT>{a, m, n, on}, v, sums);
+        PutRagged<OUT> put[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) put[u] = PutRagged<OUT>{&a, m[u], n, on[u]};
+        finish<BACKWARD, OUT>(a, drop, m, n, on, bias, here, put, v, sums);
       }
     }
     strip_barrier<SHARED>();
@@ -303,21 +337,21 @@ struct PutAct {
   uint8_t act, backward;
   DropArgs drop;
   __device__ __forceinline__ void put(const Fp8MmArgs&, int m, int n, float s) const {
-    float v[1] = {s};
+    float v[1][1] = {{s}};
     const Drop d(drop);
     OUT* const at = z ? (OUT*)z + (int64_t)m * ldz + n : nullptr;
     if (backward) {
-      const float y[1] = {widen(*at)};
+      const float y[1][1] = {{widen(*at)}};
       times_slope(act, y, v);
-      v[0] = d.apply((uint32_t)m, (uint32_t)n, v[0]);
+      v[0][0] = d.apply((uint32_t)m, (uint32_t)n, v[0][0]);
     } else {
-      if (bias) v[0] += widen(((const OUT*)bias)[n]);
-      if (at) narrow(v[0], *at);
+      if (bias) v[0][0] += widen(((const OUT*)bias)[n]);
+      if (at) narrow(v[0][0], *at);
       activate(act, v);
-      v[0] = d.apply((uint32_t)m, (uint32_t)n, v[0]);
-      if (residual) v[0] += widen(((const OUT*)residual)[(int64_t)m * ldr + n]);
+      v[0][0] = d.apply((uint32_t)m, (uint32_t)n, v[0][0]);
+      if (residual) v[0][0] += widen(((const OUT*)residual)[(int64_t)m * ldr + n]);
     }
-    narrow(v[0], ((OUT*)c)[(int64_t)m * ldc + n]);
+    narrow(v[0][0], ((OUT*)c)[(int64_t)m * ldc + n]);
   }
 };
 // its sums alone
@@ -339,24 +373,25 @@ __global__ __launch_bounds__(256) void fp8_mm_act_join_kernel(Fp8ActArgs a, cons
   float bias[8], sums[8] = {};
   load_bias8<OUT>(a, n, bias);
   for (int base = from; base < to; base += 16) {
-    const int m = base + (threadIdx.x >> 4);
-    const bool on = m < to && n < a.g.N;
-    float v[8] = {};
-    if (on) {
-      const float* p = part + (int64_t)m * ldp + n;
+    const int m[1] = {base + (int)(threadIdx.x >> 4)};
+    const bool on[1] = {m[0] < to && n < a.g.N};
+    float v[1][8] = {};
+    if (on[0]) {
+      const float* p = part + (int64_t)m[0] * ldp + n;
       for (int s = 0; s < a.g.splits; ++s, p += (int64_t)a.g.M * ldp) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (n + 4 * h >= a.g.N) continue;   // the pitch is a multiple of 4
           const f32x4 x = *(const f32x4*)(p + 4 * h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * h + e] += x[e];
+          for (int e = 0; e < 4; ++e) v[0][4 * h + e] += x[e];
         }
       }
     }
-    Raw8<OUT> here;
-    beside.load(m, n, a.g.N, on, here);
-    finish8<BACKWARD, OUT>(a, drop, m, n, on, bias, here, PutRagged<OUT>{a, m, n, on}, v, sums);
+    Raw8<OUT> here[1];
+    beside.load(m[0], n, a.g.N, on[0], here[0]);
+    const PutRagged<OUT> put[1] = {{&a, m[0], n, on[0]}};
+    finish<BACKWARD, OUT>(a, drop, m, n, on, bias, here, put, v, sums);
   }
   if (!a.dbias_part) return;
 #pragma unroll

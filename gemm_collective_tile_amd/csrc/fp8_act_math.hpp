@@ -39,60 +39,60 @@ __device__ __forceinline__ float gelu_sigmoid(float z, float z2) {   // s(u), th
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c * kGelu3, z2, c)));
 }
 
-template <int N>
-__device__ __forceinline__ void activate(int act, float (&v)[N]) {
+template <int U, int N>
+__device__ __forceinline__ void activate(int act, float (&v)[U][N]) {
   switch (act) {
     case ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // NaN stays
+      for (int k = 0; k < U * N; ++k) v[k / N][k % N] = v[k / N][k % N] < 0.0f ? 0.0f : v[k / N][k % N];   // NaN stays
       break;
     case ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+      for (int k = 0; k < U * N; ++k) {
         float e;
-        v[i] *= normal_cdf(v[i], e);
+        v[k / N][k % N] *= normal_cdf(v[k / N][k % N], e);
       }
       break;
     case ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] *= gelu_sigmoid(v[i], v[i] * v[i]);
+      for (int k = 0; k < U * N; ++k) v[k / N][k % N] *= gelu_sigmoid(v[k / N][k % N], v[k / N][k % N] * v[k / N][k % N]);
       break;
     case ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] *= sigmoid(v[i]);
+      for (int k = 0; k < U * N; ++k) v[k / N][k % N] *= sigmoid(v[k / N][k % N]);
       break;
     default: break;
   }
 }
 
 // v *= act'(z)
-template <int N>
-__device__ __forceinline__ void times_slope(int act, const float (&z)[N], float (&v)[N]) {
+template <int U, int N>
+__device__ __forceinline__ void times_slope(int act, const float (&z)[U][N], float (&v)[U][N]) {
   switch (act) {
     case ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = z[i] > 0.0f ? v[i] : 0.0f;
+      for (int k = 0; k < U * N; ++k) v[k / N][k % N] = z[k / N][k % N] > 0.0f ? v[k / N][k % N] : 0.0f;
       break;
     case ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+      for (int k = 0; k < U * N; ++k) {
         float e;
-        const float c = normal_cdf(z[i], e);
-        v[i] *= __builtin_fmaf(z[i] * 0.39894228040143268f, e, c);
+        const float c = normal_cdf(z[k / N][k % N], e);
+        v[k / N][k % N] *= __builtin_fmaf(z[k / N][k % N] * 0.39894228040143268f, e, c);
       }
       break;
     case ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float z2 = gelu_square(z[i]), s = gelu_sigmoid(z[i], z2);
-        v[i] *= __builtin_fmaf(z[i] * s * (1.0f - s), kGeluU * __builtin_fmaf(3.0f * kGelu3, z2, 1.0f), s);
+      for (int k = 0; k < U * N; ++k) {
+        const float z2 = gelu_square(z[k / N][k % N]), s = gelu_sigmoid(z[k / N][k % N], z2);
+        v[k / N][k % N] *= __builtin_fmaf(z[k / N][k % N] * s * (1.0f - s), __builtin_fmaf(3.0f * kGelu3 * kGeluU, z2, kGeluU), s);
       }
       break;
     case ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float s = sigmoid(z[i]);
-        v[i] *= s * __builtin_fmaf(z[i], 1.0f - s, 1.0f);
+      for (int k = 0; k < U * N; ++k) {
+        const float s = sigmoid(z[k / N][k % N]);
+        v[k / N][k % N] *= s * __builtin_fmaf(z[k / N][k % N], 1.0f - s, 1.0f);
       }
       break;
     default: break;
