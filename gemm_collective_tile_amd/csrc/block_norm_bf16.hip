@@ -20,7 +20,9 @@ struct JoinArgs {   // short: the host writes a kernel's arguments for every lau
 
 // Adds the workgroups' sums, 64 columns at a time, 16 waves a sixteenth of the workgroups
 // each with up to 16 loads under way. blockIdx.y: 0 to 3 the parameters' gradients; from
-// 4 on the gates' whose rows several workgroups share.
+// 4 on the gates' whose rows several workgroups share. Bound by latency, so many loads at
+// a time: four gradients of 4096 columns from 512 workgroups 6.4 us (with one load at a
+// time 23.7), from 42 workgroups 2.8.
 __global__ __launch_bounds__(1024) void block_norm_join_kernel(JoinArgs a, FastDiv gate_rows, FastDiv wg_rows) {
   __shared__ float sums[16][64];
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;

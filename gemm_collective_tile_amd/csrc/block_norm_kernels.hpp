@@ -126,6 +126,12 @@ __device__ __forceinline__ void affine(const void* w, const void* b, bool f32, f
   }
 }
 
+// Rows of up to 512 columns take a wave, wider ones one for each 512 (a value read once
+// and 8 of them a lane: 64 registers, so eight waves on a vector unit, hide the row's
+// four round trips to memory, LDS and back), beyond 8192 columns two pieces a lane.
+// 8192 x 4096 in bf16 with both norms, a gate, dropout, an fp32 stream and 8-bit n:
+// 437 MB, 82 us, 5.3 TB/s, a copy's rate. 1 x 4096 in fp16 2.3 us (a launch 2.2). Rows at
+// odd addresses cost the memory path more: 1023 x 4093 9.4-10.5 us, 1024 x 4096 8.1.
 template <class T, class X, int W, int P, bool WHOLE>
 __global__ __launch_bounds__(W < 4 ? 256 : W * 64, P == 1 ? 8 : 4) void block_norm_kernel(NormArgs a, float inv_cols, FastDiv gate_rows) {
   constexpr int RG = W < 4 ? 4 / W : 1;   // rows of a workgroup
@@ -209,12 +215,17 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64, P == 1 ? 8 : 4) void block_no
 // those in order: no atomics, the same bits every time. dgate's sums end with each
 // group of rows that shares a gate; a group that lies in one workgroup is done there,
 // what a workgroup has of its first and of its last other group goes to the workspace.
+//
+// Bound by memory: 4096 x 4096 in bf16 with both norms, a gate, dropout and fp32 streams,
+// 302 MB and 25 MB of partial sums, 74 us (4.4 TB/s) and 6.2 to join them. 128 registers:
+// two workgroups of 8 waves a CU (of one with 16 the waves wait for each other: 2 %
+// slower). 333 x 1376 in fp16 as a layer norm with all gradients 9.1 us and 2.8.
 template <class T, class X, int W, int P, bool WHOLE, bool BIAS>
 __global__ __launch_bounds__(64 * norm_bwd_waves(W), 4) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols,
                                                                                    FastDiv gate_rows) {
   constexpr int WAVES = norm_bwd_waves(W), RG = WAVES / W, WIDE = W * 512 * P;
   __shared__ float slots[2][2][RG][2 * W];   // by turns, so that a row's sums are read before the next row's but one are written
-  __shared__ __align__(16) float comb[RG > 1 ? 4 * RG * WIDE : 4];   // 128 KB: a workgroup has the CU to itself by its registers
+  __shared__ __align__(16) float comb[RG > 1 ? 4 * RG * WIDE : 4];   // 64 KB, for two workgroups a CU
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = wave / W, w = wave % W;
   const int first = blockIdx.x * a.wg_rows, last = min(first + a.wg_rows, a.rows);

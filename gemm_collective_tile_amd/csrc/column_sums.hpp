@@ -21,7 +21,8 @@ __device__ __forceinline__ float same_columns_sum(float v) {
   return __builtin_bit_cast(float, (uint32_t)y[0]) + __builtin_bit_cast(float, (uint32_t)y[1]);
 }
 
-// out = the partial sums, added in order: a wave a quarter of them, 16 loads under way
+// out = the partial sums, added in order: a wave a quarter of them, 16 loads under way.
+// Bound by latency: 16 rows of 11008 4.1 us.
 template <class OUT>
 __global__ __launch_bounds__(256) void join_columns_kernel(const float* part, int parts, int64_t ldp, int N, OUT* out) {
   __shared__ float red[4][64];

@@ -8,7 +8,10 @@
 namespace iris {
 namespace {
 
-// A thread takes 8 columns of a row: one call of the generator.
+// A thread takes 8 columns of a row: one call of the generator (10 rounds of two 32-bit
+// products, some 70 instructions), 16 bytes a load. Bound by memory: 8192 x 11008 in
+// bf16 with a residual, 541 MB, 91 us (5.9 TB/s, part of it the cache's; a plain copy
+// of 1 GiB reaches 5.2); 1001 x 1376 in fp16 2.9 us, of which 2.2 are the launch's.
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a, FastDiv pieces) {
   const uint32_t id = blockIdx.x * kThreads + threadIdx.x, row = pieces.div(id);
@@ -26,7 +29,8 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a, FastDi
 }
 
 // The same with the sums of out over its rows, before its rounding: a workgroup takes 128
-// columns of a share of the rows, 16 rows at a time, and leaves a row of partial sums.
+// columns of a share of the rows, 16 rows at a time, and leaves a row of partial sums
+// (no atomics: the order of the sums is always the same), which join_columns adds.
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void dropout_sums_kernel(DropoutArgs a, int share, float* part, int64_t ldp) {
   __shared__ float red[4][128];

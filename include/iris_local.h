@@ -455,7 +455,8 @@ size_t iris_dropout_workspace_size(int64_t rows, int64_t cols);
  *   r = x + alpha gate m p                                   the residual stream
  *   n = norm(r) (pre_w + w_offset) + pre_b                   the next block's input
  * A NULL weight counts as 1 (w_offset is not added to it), a NULL bias as 0, a NULL gate
- * as 1. n is formed from r before r is rounded.
+ * as 1. n is formed from r before r is rounded. The squares' sum is in 32 bits: from
+ * magnitudes of some 2^57 on it is infinite, and norm(v) 0.
  *   type         of y and n: fp16 or bf16
  *   stream_type  of x and r: type or fp32
  *   param_type   of weights and biases (cols values each), type or fp32
