@@ -25,6 +25,7 @@ int check_drop(const iris_drop_t* d, float alpha, iris::DropArgs* out) {
   out->offset_at = d->offset_at;
   out->threshold = (uint32_t)t;
   out->scale = (float)((double)alpha * 65536.0 / (65536.0 - t));
+  if (!std::isfinite(out->scale)) return fail(IRIS_ERR_INVALID_ARG, "dropout: alpha / (1 - p) leaves 32 bits (alpha %g)", (double)alpha);
   return IRIS_OK;
 }
 

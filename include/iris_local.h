@@ -432,7 +432,7 @@ typedef struct iris_drop {
 
 /*
  * out = residual + alpha m x, m the mask above (alpha times the kept value's factor is
- * rounded to 32 bits once). residual may be NULL. All (rows, cols) of `type` (fp16, bf16
+ * rounded to 32 bits once and has to be finite). residual may be NULL. All (rows, cols) of `type` (fp16, bf16
  * or fp32). Its own backward pass with respect to x: the same call on out's gradient.
  * sums: `cols` values of type, or NULL: out's sums over the rows, in 32 bits before out's
  * rounding; of a gradient, that of a bias which was added to x's rows (the down

@@ -125,6 +125,14 @@ def test_dropout_status_codes():
     assert call_dropout(rows=0, out=None, x=None) == 0 and call_dropout(cols=0, out=None, x=None) == 0
 
 
+def test_a_factor_that_leaves_32_bits_is_refused():
+    """alpha is finite, alpha / (1 - p) in 32 bits is not: 0 times it would be NaN."""
+    top = torch.finfo(torch.float32).max
+    assert call_dropout(rows=0, alpha=top, d=drop(0.0)) == 0 and call_dropout(rows=0, alpha=top, d=drop(0.5)) == INVALID
+    half = drop(0.5)
+    assert call_norm(norm_args(alpha=top, drop=ctypes.pointer(half)), y=R) == INVALID
+
+
 def norm_args(**kw):
     a = dict(kind=1, type=2, stream_type=2, param_type=2, gate_type=2, post=0, eps=1e-6, w_offset=0.0, alpha=1.0)
     a.update(kw)
