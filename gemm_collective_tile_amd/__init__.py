@@ -710,7 +710,7 @@ class Dropout:
     offset (a graph that is replayed takes new masks by it). The mask goes by these and
     a value's row and column alone; operators on matrices of one size that are given
     the same Dropout drop the same values. `offset` may be set anew between calls."""
-    __slots__ = ("p", "seed", "counter", "_c", "_p", "_device")
+    __slots__ = ("_counter", "_c", "_p", "_device")
 
     def __init__(self, p: float, seed: int, offset: int = 0, counter: Optional[torch.Tensor] = None):
         if not 0.0 <= p < 1.0:
@@ -721,9 +721,13 @@ class Dropout:
                 raise TypeError("counter must be an int64 torch tensor")
             _want_numel(counter, 1, "counter")
             at, self._device = counter.data_ptr(), counter.get_device()
-        self.p, self.seed, self.counter = float(p), int(seed) % 2 ** 64, counter
-        self._c = _Drop(self.p, self.seed, int(offset) % 2 ** 64, at)
+        self._counter = counter
+        self._c = _Drop(float(p), int(seed) % 2 ** 64, int(offset) % 2 ** 64, at)
         self._p = ctypes.pointer(self._c)
+
+    p = property(lambda self: self._c.p)
+    seed = property(lambda self: self._c.seed)
+    counter = property(lambda self: self._counter)
 
     @property
     def offset(self) -> int:
@@ -813,7 +817,7 @@ class BlockNorm:
     matrix whose row i / rows_per_gate goes with row i. A handle: it reads the
     tensors' addresses once and holds the tensors, so their memory must not be
     exchanged under it; their values may change between calls."""
-    __slots__ = ("cols", "post", "gate", "rows_per_gate", "dropout", "_fields", "_held", "_param", "_gate", "_structs", "_device")
+    __slots__ = ("_cols", "_post", "_gate", "_every", "_dropout", "_fields", "_held", "_param", "_gate_type", "_structs", "_device")
 
     def __init__(self, kind="rms", eps: float = 1e-6, pre_w=None, pre_b=None, post: bool = False, post_w=None, post_b=None,
                  gate=None, rows_per_gate: Optional[int] = None, alpha: float = 1.0, dropout: Optional[Dropout] = None,
@@ -825,24 +829,24 @@ class BlockNorm:
         if not post and (post_w is not None or post_b is not None):
             raise ValueError("post_w and post_b need post")
         given = {k: v for k, v in (("pre_w", pre_w), ("pre_b", pre_b), ("post_w", post_w), ("post_b", post_b)) if v is not None}
-        self.cols = self._param = self._device = None
+        self._cols = self._param = self._device = None
         for name, t in given.items():
             if not isinstance(t, torch.Tensor) or t.dtype not in _FP8_TYPES:
                 raise TypeError(f"{name} must be a float16, bfloat16 or float32 torch tensor")
-            if t.dim() != 1 or (self.cols is not None and t.numel() != self.cols):
-                raise ValueError(f"{name} must be a vector" + ("" if self.cols is None else f" of {self.cols} values"))
+            if t.dim() != 1 or (self._cols is not None and t.numel() != self._cols):
+                raise ValueError(f"{name} must be a vector" + ("" if self._cols is None else f" of {self._cols} values"))
             if t.numel() > 1 and t.stride(0) != 1:
                 raise ValueError(f"{name} must be contiguous")
             if self._param is not None and t.dtype != self._param:
                 raise TypeError("weights and biases must have one dtype")
             self._at(t, name)
-            self.cols, self._param = t.numel(), t.dtype
-        self._gate, ld = None, 0
+            self._cols, self._param = t.numel(), t.dtype
+        self._gate_type, ld = None, 0
         if gate is not None:
             if not isinstance(gate, torch.Tensor) or gate.dtype not in _FP8_TYPES:
                 raise TypeError("gate must be a float16, bfloat16 or float32 torch tensor")
-            if gate.dim() not in (1, 2) or (self.cols is not None and gate.shape[-1] != self.cols):
-                raise ValueError("gate must be a vector or a matrix" + ("" if self.cols is None else f" of {self.cols} columns"))
+            if gate.dim() not in (1, 2) or (self._cols is not None and gate.shape[-1] != self._cols):
+                raise ValueError("gate must be a vector or a matrix" + ("" if self._cols is None else f" of {self._cols} columns"))
             if gate.shape[-1] > 1 and gate.stride(-1) != 1:
                 raise ValueError("gate must be contiguous along its rows")
             if gate.dim() == 2 and rows_per_gate is None and gate.shape[0] != 1:
@@ -850,15 +854,21 @@ class BlockNorm:
             if rows_per_gate is not None and rows_per_gate < 1:
                 raise ValueError(f"rows_per_gate must be positive (got {rows_per_gate})")
             self._at(gate, "gate")
-            self.cols, self._gate = gate.shape[-1], gate.dtype
+            self._cols, self._gate_type = gate.shape[-1], gate.dtype
             ld = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else gate.shape[-1]
-        self.post, self.gate, self.dropout = bool(post), gate, dropout
-        self.rows_per_gate = (1 << 62) if gate is None or rows_per_gate is None else int(rows_per_gate)
+        self._post, self._gate, self._dropout = bool(post), gate, dropout
+        self._every = (1 << 62) if gate is None or rows_per_gate is None else int(rows_per_gate)
         self._held = given
         at = [given[k].data_ptr() if k in given else None for k in ("pre_w", "pre_b", "post_w", "post_b")]
-        self._fields = (_NORM_KINDS[kind], int(self.post), eps, w_offset, alpha, at, None if gate is None else gate.data_ptr(), ld,
-                        self.rows_per_gate, None if dropout is None else dropout._p)
+        self._fields = (_NORM_KINDS[kind], int(self._post), eps, w_offset, alpha, at, None if gate is None else gate.data_ptr(), ld,
+                        self._every, None if dropout is None else dropout._p)
         self._structs = {}
+
+    cols = property(lambda self: self._cols)
+    post = property(lambda self: self._post)
+    gate = property(lambda self: self._gate)
+    rows_per_gate = property(lambda self: self._every)
+    dropout = property(lambda self: self._dropout)
 
     def _at(self, t, name: str) -> None:
         if self._device is not None and t.get_device() != self._device:
@@ -870,7 +880,7 @@ class BlockNorm:
         p = self._structs.get((kind, stream_kind))
         if p is None:
             types = []
-            for dtype, name in ((stream_kind, "the stream (x, r)"), (self._param, "weights and biases"), (self._gate, "the gate")):
+            for dtype, name in ((stream_kind, "the stream (x, r)"), (self._param, "weights and biases"), (self._gate_type, "the gate")):
                 if dtype is not None and dtype not in (kind, torch.float32):
                     raise TypeError(f"{name} must be {str(kind)[6:]} as y and n are, or float32")
                 types.append(_FP8_TYPES[dtype or kind])
@@ -880,16 +890,16 @@ class BlockNorm:
         return p
 
     def _for(self, rows: int, cols: int, dev: int) -> None:
-        if self.cols is not None and self.cols != cols:
-            raise ValueError(f"the norm's parameters have {self.cols} columns, the activations {cols}")
+        if self._cols is not None and self._cols != cols:
+            raise ValueError(f"the norm's parameters have {self._cols} columns, the activations {cols}")
         if self._device is not None and self._device != dev:
             raise _elsewhere("the norm's parameters", self._device, dev)
-        if self.gate is not None and self.gate.dim() == 2 and rows > 0 and self.gate.shape[0] != -(-rows // self.rows_per_gate):
-            raise ValueError(f"gate has {self.gate.shape[0]} rows, expected {-(-rows // self.rows_per_gate)}")
-        if self.gate is not None and self.gate.dim() == 1 and self.rows_per_gate < rows:
+        if self._gate is not None and self._gate.dim() == 2 and rows > 0 and self._gate.shape[0] != -(-rows // self._every):
+            raise ValueError(f"gate has {self._gate.shape[0]} rows, expected {-(-rows // self._every)}")
+        if self._gate is not None and self._gate.dim() == 1 and self._every < rows:
             raise ValueError("a gate for every rows_per_gate rows must be a matrix")
-        if self.dropout is not None:
-            _drop(self.dropout, dev)
+        if self._dropout is not None:
+            _drop(self._dropout, dev)
 
 
 def _norm_kind(norm, stream_kind, *tensors):
@@ -902,7 +912,7 @@ def _norm_kind(norm, stream_kind, *tensors):
             if kind not in _FP8_HALVES:
                 raise TypeError("y, n, dn and dy must be float16 or bfloat16 torch tensors")
             return kind
-    for dtype in (stream_kind, norm._param, norm._gate):
+    for dtype in (stream_kind, norm._param, norm._gate_type):
         if dtype in _FP8_HALVES:
             return dtype
     return torch.bfloat16

@@ -63,6 +63,19 @@ def test_block_norm_handle_refuses():
     expect(ValueError, "contiguous along", n, gate=torch.zeros(40, 2).t(), rows_per_gate=3)
 
 
+def test_handles_are_not_changed_under_their_pointers():
+    """What a handle was made of is read once: set anew it would be passed over in
+    silence, or its memory freed while the kernels still read it."""
+    d = il.Dropout(0.25, 7)
+    norm = il.BlockNorm(post=True, gate=torch.zeros(2, 40), rows_per_gate=3, dropout=d)
+    assert (d.p, d.seed, d.counter) == (0.25, 7, None)
+    assert (norm.cols, norm.post, norm.rows_per_gate) == (40, True, 3) and norm.gate.shape == (2, 40) and norm.dropout is d
+    for handle, names in ((d, ("p", "seed", "counter")), (norm, ("cols", "post", "gate", "rows_per_gate", "dropout"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(handle, name, None)
+
+
 def test_block_norm_refuses():
     x, norm = torch.zeros((6, 40), dtype=torch.float16), il.BlockNorm(pre_w=torch.zeros(40, dtype=torch.float16))
     f, b = il.iris_block_norm, il.iris_block_norm_bwd
