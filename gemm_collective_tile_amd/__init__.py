@@ -894,8 +894,9 @@ class BlockNorm:
             raise ValueError(f"the norm's parameters have {self._cols} columns, the activations {cols}")
         if self._device is not None and self._device != dev:
             raise _elsewhere("the norm's parameters", self._device, dev)
-        if self._gate is not None and self._gate.dim() == 2 and rows > 0 and self._gate.shape[0] != -(-rows // self._every):
-            raise ValueError(f"gate has {self._gate.shape[0]} rows, expected {-(-rows // self._every)}")
+        if self._gate is not None and self._gate.dim() == 2 and self._gate.shape[0] != -(-rows // self._every):
+            if rows > 0 or self._gate.shape[0] != 1:
+                raise ValueError(f"gate has {self._gate.shape[0]} rows, expected {-(-rows // self._every)}")
         if self._gate is not None and self._gate.dim() == 1 and self._every < rows:
             raise ValueError("a gate for every rows_per_gate rows must be a matrix")
         if self._dropout is not None:

@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "block_norm_kernels.hpp"
+#include "column_sums.hpp"
 
 namespace iris {
 
@@ -90,6 +91,7 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_norm_join(const NormBwdArgs& a, hipStream_t s) {
+  if (a.rows == 0 && a.dgate) return join_columns(nullptr, 0, 0, a.cols, a.dgate, s);   // zeros, as the kernel gives the others
   if (a.wgs <= 1) return hipSuccess;
   const JoinArgs j{a.dpre_w, a.dpre_b, a.dpost_w, a.dpost_b, a.dgate, a.part, a.rows, a.cols, a.p.rows_per_gate, a.wgs, a.wg_rows,
                    a.dgate ? (a.rows + a.p.rows_per_gate - 1) / a.p.rows_per_gate : 0};

@@ -277,7 +277,7 @@ int iris_block_norm_bwd(void* dx, int64_t ld_dx, void* dy, int64_t ld_dy, float*
   } sums[] = {{dpre_w, "dpre_w"}, {dpre_b, "dpre_b"}, {dpost_w, "dpost_w"}, {dpost_b, "dpost_b"}, {dgate, "dgate"}};
   for (const auto& v : sums)
     if ((st = check_vector(v.p, IRIS_TYPE_FP32, v.name))) return st;
-  if (cols == 0 || (rows == 0 && !dpre_w && !dpre_b && !dpost_w && !dpost_b)) return IRIS_OK;
+  if (cols == 0 || (rows == 0 && !dpre_w && !dpre_b && !dpost_w && !dpost_b && !dgate)) return IRIS_OK;
   const iris::NormBwdPlan plan = iris::norm_bwd_plan(rows, cols);
   if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes))) return st;
   if ((st = check_distinct({{dx, "dx", true}, {dy, "dy", true}, {dpre_w, "dpre_w", true}, {dpre_b, "dpre_b", true},
@@ -303,7 +303,7 @@ int iris_block_norm_bwd(void* dx, int64_t ld_dx, void* dy, int64_t ld_dy, float*
   a.dpre_b = dpre_b;
   a.dpost_w = dpost_w;
   a.dpost_b = dpost_b;
-  a.dgate = rows > 0 ? dgate : nullptr;
+  a.dgate = dgate;
   a.ld_dn = (int32_t)ld_dn;
   a.ld_dr = (int32_t)ld_dr;
   a.ld_r = (int32_t)ld_r;

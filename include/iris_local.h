@@ -490,7 +490,8 @@ int iris_block_norm(void* r, int64_t ld_r, void* n, int64_t ld_n, const iris_fp8
  * Its backward pass, at the given r, y and stats: dn is n's gradient, dr what reaches r
  * from elsewhere; either may be NULL (0). Gradients, each NULL if not wanted: dx (which
  * is all of r's), dy, and in 32 bits dpre_w, dpre_b, dpost_w, dpost_b (cols) and dgate
- * (contiguous rows of cols, one for each gate row that the rows use). r is needed with dn,
+ * (contiguous rows of cols, one for each gate row that the rows use; without rows one of
+ * zeros, as the others are). r is needed with dn,
  * y with dy, dgate, dpost_w or dpost_b. dx, dr, r of stream_type; dy, dn, y of type.
  * Sums over the rows run in 32 bits in an order that the sizes alone decide.
  * workspace: at least iris_block_norm_bwd_workspace_size() bytes (at most 101 MB), 256-byte

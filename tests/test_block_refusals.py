@@ -76,6 +76,12 @@ def test_handles_are_not_changed_under_their_pointers():
                 setattr(handle, name, None)
 
 
+def test_block_norm_refuses_gates_that_no_rows_use():
+    x = torch.zeros((0, 40), dtype=torch.float16)
+    norm = il.BlockNorm(gate=torch.zeros(2, 40, dtype=torch.float16), rows_per_gate=3)
+    expect(ValueError, "gate has 2 rows, expected 0", il.iris_block_norm, x, norm, y=x, r=x.clone())
+
+
 def test_block_norm_refuses():
     x, norm = torch.zeros((6, 40), dtype=torch.float16), il.BlockNorm(pre_w=torch.zeros(40, dtype=torch.float16))
     f, b = il.iris_block_norm, il.iris_block_norm_bwd

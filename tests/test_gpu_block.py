@@ -469,6 +469,21 @@ def test_block_norm_rows_of_nothing():
     il.iris_block_norm(none, il.BlockNorm(), n=torch.empty_like(none))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("gates", [None, 0, 1])
+def test_block_norm_bwd_gives_zeros_for_a_gate_without_rows(gates):
+    """One gate (a vector, or a matrix of one row) that no row uses has a gradient of
+    zeros, as weights have; a gate matrix without rows has none."""
+    gate = torch.ones(40 if gates is None else (gates, 40), device="cuda")
+    norm = il.BlockNorm(gate=gate, rows_per_gate=None if gates is None else 3)
+    x, stats = torch.empty((0, 40), dtype=torch.bfloat16, device="cuda"), torch.empty((0, 4), device="cuda")
+    wide = torch.full((3, 40), float("nan"), device="cuda")
+    dgate = wide[1].view(gate.shape) if gate.numel() else wide[1:1]
+    il.iris_block_norm_bwd(None, x, stats, norm, dr=x, y=x, dgate=dgate)
+    assert bool((dgate == 0).all()) and bool(wide[[0, 2]].isnan().all())
+    assert gate.numel() > 0 or bool(wide.isnan().all())
+
+
 # ---------------------------------------------------------- product, epilogue
 
 ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
