@@ -7,9 +7,13 @@
 namespace iris {
 
 constexpr int kNormMaxCols = 16384;
-// Waves of a backward workgroup whose rows W waves hold each. Registers allow 16 waves a
-// compute unit.
+// Waves of a backward workgroup whose rows W waves hold each. 8 of them with 256 registers
+// a lane where rows are whole, up to 4096 columns: the parameters and the next row fit.
+// 16 a compute unit, with 128 each, where they don't, and for ragged rows, which gain
+// nothing (4096 x 4096 in bf16 with fp32 streams 79.5 us with 128, 73.3 with 256; 2048 x
+// 8192 78.4 with 128, 88.0 with 256; 4095 x 4093, streams in bf16, 63.4 and 73.4).
 constexpr int norm_bwd_waves(int W) { return W < 8 ? 8 : W; }
+constexpr bool norm_bwd_ahead(int W, bool whole) { return W <= 8 && whole; }
 
 // Parameters of the norms: weights and biases are of y's type or (param32) fp32, the gate too (gate32).
 struct NormParams {
@@ -50,7 +54,7 @@ struct NormBwdPlan {
   int wgs, wg_rows;
   size_t ws_bytes;
 };
-NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols);
+NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols, bool whole);
 
 // by the type of y (T), the stream's (x, r: fp32 or T) and whether all rows are whole and aligned
 template <class T>

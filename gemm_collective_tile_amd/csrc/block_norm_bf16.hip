@@ -23,7 +23,7 @@ struct JoinArgs {   // short: the host writes a kernel's arguments for every lau
 // each with up to 16 loads under way. blockIdx.y: 0 to 3 the parameters' gradients; from
 // 4 on the gates' whose rows several workgroups share. Bound by latency, so many loads at
 // a time: four gradients of 4096 columns from 512 workgroups 6.4 us (with one load at a
-// time 23.7), from 42 workgroups 2.8.
+// time 23.7), from 256 4.0.
 __global__ __launch_bounds__(1024) void block_norm_join_kernel(JoinArgs a, FastDiv gate_rows, FastDiv wg_rows) {
   __shared__ float sums[16][64];
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
@@ -76,17 +76,20 @@ __global__ __launch_bounds__(1024) void block_norm_join_kernel(JoinArgs a, FastD
 
 }  // namespace
 
-NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols) {
+NormBwdPlan norm_bwd_plan(int64_t rows, int64_t cols, bool whole) {
   int waves = 1;
   while (waves < 16 && 512 * waves < cols) waves *= 2;
   if (rows == 0) return {1, 0, 0};    // the parameters' gradients alone: zeros
   const int64_t step = norm_bwd_waves(waves) / waves;    // rows that a workgroup works on at a time
-  const int64_t most = kFp8Cus * (16 / norm_bwd_waves(waves));
-  const int64_t share = ((rows + most - 1) / most + step - 1) / step * step;
   NormBwdPlan p{};
-  p.wg_rows = (int)share;
-  p.wgs = (int)((rows + share - 1) / share);
+  const auto share = [&](bool ahead) {   // of the rows, for as many workgroups as the chip holds
+    const int64_t most = kFp8Cus * (ahead ? 1 : 16 / norm_bwd_waves(waves)), n = ((rows + most - 1) / most + step - 1) / step * step;
+    p.wg_rows = (int)n;
+    p.wgs = (int)((rows + n - 1) / n);
+  };
+  share(false);   // the larger number: the workspace's
   p.ws_bytes = p.wgs > 1 ? (size_t)6 * p.wgs * ((cols + 7) / 8 * 8) * 4 : 0;
+  if (norm_bwd_ahead(waves, whole)) share(true);
   return p;
 }
 

@@ -217,15 +217,18 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64, P == 1 ? 8 : 4) void block_no
 // what a workgroup has of its first and of its last other group goes to the workspace.
 //
 // Bound by memory: 4096 x 4096 in bf16 with both norms, a gate, dropout and fp32 streams,
-// 302 MB and 25 MB of partial sums, 74 us (4.4 TB/s) and 6.2 to join them. 128 registers:
-// two workgroups of 8 waves a CU (of one with 16 the waves wait for each other: 2 %
-// slower). 333 x 1376 in fp16 as a layer norm with all gradients 9.1 us and 2.8.
+// 302 MB and 12 MB of partial sums, 69 us (4.6 TB/s) and 4.0 to join them. A row is a chain
+// of loads, two reductions over the waves and stores; the next row's loads go out ahead
+// of it, and the parameters stay in registers, as a load of them would be waited for
+// behind the next row's (without either, two workgroups a CU with 128 registers: 74 and
+// 6.2). 333 x 1376 in fp16 as a layer norm with all gradients 9.2 us and 2.8.
 template <class T, class X, int W, int P, bool WHOLE, bool BIAS>
-__global__ __launch_bounds__(64 * norm_bwd_waves(W), 4) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols,
+__global__ __launch_bounds__(64 * norm_bwd_waves(W), norm_bwd_ahead(W, WHOLE) ? 2 : 4) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols,
                                                                                    FastDiv gate_rows) {
   constexpr int WAVES = norm_bwd_waves(W), RG = WAVES / W, WIDE = W * 512 * P;
+  constexpr bool AHEAD = norm_bwd_ahead(W, WHOLE);   // 256 registers a lane: the next row is under way while one is worked on
   __shared__ float slots[2][2][RG][2 * W];   // by turns, so that a row's sums are read before the next row's but one are written
-  __shared__ __align__(16) float comb[RG > 1 ? 4 * RG * WIDE : 4];   // 64 KB, for two workgroups a CU
+  __shared__ __align__(16) float comb[RG > 1 ? 4 * RG * WIDE : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sub = wave / W, w = wave % W;
   const int first = blockIdx.x * a.wg_rows, last = min(first + a.wg_rows, a.rows);
@@ -273,49 +276,124 @@ __global__ __launch_bounds__(64 * norm_bwd_waves(W), 4) void block_norm_bwd_kern
     }
   };
 
+  // AHEAD: the next row, as it lies in memory
+  struct {
+    f32x4 st;   // mean and rstd of y, of r
+    Raw8<T> y, dn;
+    Raw8<X> dr, r;
+  } in;
+  const auto fetch = [&](int base, int end) {
+    const int row = min(base + sub, end - 1);
+    const bool on = base + sub < end;
+    in.st = *(const f32x4*)(a.stats + 4 * (int64_t)row);
+    if (a.dn) {
+      in.dn.template fetch<WHOLE>((const T*)a.dn + (int64_t)row * a.ld_dn, col[0], a.cols, on);
+      in.r.template fetch<WHOLE>((const X*)a.r + (int64_t)row * a.ld_r, col[0], a.cols, on);
+    }
+    if (a.dr) in.dr.template fetch<WHOLE>((const X*)a.dr + (int64_t)row * a.ld_dr, col[0], a.cols, on);
+    if (a.y) in.y.template fetch<WHOLE>((const T*)a.y + (int64_t)row * a.ld_y, col[0], a.cols, on);
+  };
+  // v times a weight's columns, with a bias's; times a row of gates
+  const auto times_weight = [&](const void* w, const void* b, int j, float (&v)[8]) {
+    affine<T, WHOLE>(w, b, a.p.param32, a.p.w_offset, col[j], a.cols, v);
+  };
+  const auto times_gate = [&](uint32_t group, int j, float (&v)[8]) {
+    if (!a.p.gate) return;
+    float g[8];
+    load_param<T, WHOLE>((const char*)a.p.gate + (int64_t)group * a.p.ld_gate * (a.p.gate32 ? 4 : (int)sizeof(T)), a.p.gate32,
+                         col[j], a.cols, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= g[i];
+  };
+
   float s_pre_w[P][8] = {}, s_pre_b[P][8] = {}, s_post_w[P][8] = {}, s_post_b[P][8] = {}, s_gate[P][8] = {};
+  float pre_w[8], post_w[8], post_b[8], gate[8];   // AHEAD: held over the rows
+  const auto fill = [](float (&v)[8], float with) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = with;
+  };
+  const auto group_end = [&](int row0) {
+    const int64_t g1 = a.p.gate ? ((int64_t)gate_rows.div(row0) + 1) * a.p.rows_per_gate : last;
+    return g1 < last ? (int)g1 : last;
+  };
+  if constexpr (AHEAD) {
+    if (first < last) fetch(first, group_end(first));
+    fill(pre_w, 1.0f), fill(post_w, 1.0f), fill(post_b, 0.0f);
+    times_weight(a.p.pre_w, nullptr, 0, pre_w);
+    times_weight(a.p.post_w, nullptr, 0, post_w);
+    if (a.dgate) times_weight(nullptr, a.p.post_b, 0, post_b);
+  }
   const Drop drop(a.p.drop);
   int turn = 0;
   for (int row0 = first; row0 < last;) {
     const uint32_t group = a.p.gate ? gate_rows.div(row0) : 0;
     const int64_t g0 = (int64_t)group * a.p.rows_per_gate, g1 = g0 + a.p.rows_per_gate;
-    const int end = a.p.gate && g1 < last ? (int)g1 : last;
+    const int end = AHEAD ? group_end(row0) : a.p.gate && g1 < last ? (int)g1 : last;
+    if constexpr (AHEAD) {
+      fill(gate, 1.0f);
+      times_gate(group, 0, gate);
+    }
     for (int base = row0; base < end; base += RG, turn ^= 1) {
       const int at = base + sub, row = min(at, end - 1);
       const bool on = at < end;
-      const f32x4 st = *(const f32x4*)(a.stats + 4 * (int64_t)row);   // mean and rstd of y, of r
+      f32x4 st;
       Raw8<T> y[P];
-      if (a.y) {
+      float t[P][8], hat[P][8], d[P][8];
+      if constexpr (AHEAD) {
+        st = in.st;
+        if (a.dn) {
+          in.dn.template settle<WHOLE>(col[0], a.cols, on);
+          in.r.template settle<WHOLE>(col[0], a.cols, on);
+          in.dn.values(d[0]);
+          in.r.values(hat[0]);
+        }
+        if (a.dr) {
+          in.dr.template settle<WHOLE>(col[0], a.cols, on);
+          in.dr.values(t[0]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < P; ++j)
-          y[j].template load<WHOLE>((const T*)a.y + (int64_t)row * a.ld_y, col[j], a.cols, on);
-      }
-      float t[P][8], hat[P][8];
-      if (a.dr) {
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-          load8<WHOLE>((const X*)a.dr + (int64_t)row * a.ld_dr, col[j], a.cols, t[j], on);
+          for (int i = 0; i < 8; ++i) t[0][i] = 0.0f;
+        }
+        if (a.y) {
+          in.y.template settle<WHOLE>(col[0], a.cols, on);
+          y[0] = in.y;
+        }
+        const int next = base + RG < end ? base + RG : end;
+        if (next < last) fetch(next, next < end ? end : group_end(next));
       } else {
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[j][i] = 0.0f;
-      }
-      if (a.dn) {
-        float d[P][8], s[2] = {0.0f, 0.0f};
+        st = *(const f32x4*)(a.stats + 4 * (int64_t)row);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          load8<WHOLE>((const T*)a.dn + (int64_t)row * a.ld_dn, col[j], a.cols, d[j], on);
-          load8<WHOLE>((const X*)a.r + (int64_t)row * a.ld_r, col[j], a.cols, hat[j], on);
+          if (a.y) y[j].template load<WHOLE>((const T*)a.y + (int64_t)row * a.ld_y, col[j], a.cols, on);
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          if (a.dr) {
+            load8<WHOLE>((const X*)a.dr + (int64_t)row * a.ld_dr, col[j], a.cols, t[j], on);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[j][i] = 0.0f;
+          }
+        }
+      }
+      if (a.dn) {
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          if constexpr (!AHEAD) {
+            load8<WHOLE>((const T*)a.dn + (int64_t)row * a.ld_dn, col[j], a.cols, d[j], on);
+            load8<WHOLE>((const X*)a.r + (int64_t)row * a.ld_r, col[j], a.cols, hat[j], on);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             hat[j][i] = (hat[j][i] - st[2]) * st[3];
             s_pre_w[j][i] = __builtin_fmaf(d[j][i], hat[j][i], s_pre_w[j][i]);
             if (BIAS) s_pre_b[j][i] += d[j][i];
           }
-          affine<T, WHOLE>(a.p.pre_w, nullptr, a.p.param32, a.p.w_offset, col[j], a.cols, d[j]);
+          if constexpr (!AHEAD) times_weight(a.p.pre_w, nullptr, j, d[j]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            if constexpr (AHEAD) d[j][i] *= pre_w[i];
             s[0] += d[j][i];
             s[1] = __builtin_fmaf(d[j][i], hat[j][i], s[1]);
           }
@@ -339,23 +417,22 @@ __global__ __launch_bounds__(64 * norm_bwd_waves(W), 4) void block_norm_bwd_kern
       for (int j = 0; j < P; ++j) {
         y[j].values(hat[j]);
         drop.apply((uint32_t)row, (uint32_t)col[j] >> 3, t[j]);
-        float p[8];
         if (a.p.post) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) hat[j][i] = (hat[j][i] - st[0]) * st[1];
         }
-        if (a.p.gate) {
-          if (a.dgate) {
+        if (a.dgate) {
+          float p[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = hat[j][i];
-            if (a.p.post) affine<T, WHOLE>(a.p.post_w, a.p.post_b, a.p.param32, a.p.w_offset, col[j], a.cols, p);
+          for (int i = 0; i < 8; ++i) p[i] = AHEAD ? __builtin_fmaf(hat[j][i], post_w[i], post_b[i]) : hat[j][i];
+          if constexpr (!AHEAD) times_weight(a.p.post_w, a.p.post_b, j, p);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s_gate[j][i] = __builtin_fmaf(t[j][i], p[i], s_gate[j][i]);
-          }
-          const int64_t skip = (int64_t)group * a.p.ld_gate * (a.p.gate32 ? 4 : (int)sizeof(T));
-          load_param<T, WHOLE>((const char*)a.p.gate + skip, a.p.gate32, col[j], a.cols, p);
+          for (int i = 0; i < 8; ++i) s_gate[j][i] = __builtin_fmaf(t[j][i], p[i], s_gate[j][i]);
+        }
+        if constexpr (!AHEAD) times_gate(group, j, t[j]);
+        if constexpr (AHEAD) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t[j][i] *= p[i];
+          for (int i = 0; i < 8; ++i) t[j][i] *= gate[i];
         }
         if (a.p.post) {
 #pragma unroll
@@ -363,9 +440,10 @@ __global__ __launch_bounds__(64 * norm_bwd_waves(W), 4) void block_norm_bwd_kern
             s_post_w[j][i] = __builtin_fmaf(t[j][i], hat[j][i], s_post_w[j][i]);
             if (BIAS) s_post_b[j][i] += t[j][i];
           }
-          affine<T, WHOLE>(a.p.post_w, nullptr, a.p.param32, a.p.w_offset, col[j], a.cols, t[j]);
+          if constexpr (!AHEAD) times_weight(a.p.post_w, nullptr, j, t[j]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            if constexpr (AHEAD) t[j][i] *= post_w[i];
             s[0] += t[j][i];
             s[1] = __builtin_fmaf(t[j][i], hat[j][i], s[1]);
           }

@@ -243,7 +243,7 @@ int iris_block_norm(void* r, int64_t ld_r, void* n, int64_t ld_n, const iris_fp8
 
 size_t iris_block_norm_bwd_workspace_size(int64_t rows, int64_t cols) try {
   if (check_rows(rows, cols) || cols > iris::kNormMaxCols || rows == 0 || cols == 0) return 0;
-  return iris::norm_bwd_plan(rows, cols).ws_bytes;
+  return iris::norm_bwd_plan(rows, cols, false).ws_bytes;
 } catch (const std::exception&) {
   return 0;
 }
@@ -278,7 +278,10 @@ int iris_block_norm_bwd(void* dx, int64_t ld_dx, void* dy, int64_t ld_dy, float*
   for (const auto& v : sums)
     if ((st = check_vector(v.p, IRIS_TYPE_FP32, v.name))) return st;
   if (cols == 0 || (rows == 0 && !dpre_w && !dpre_b && !dpost_w && !dpost_b && !dgate)) return IRIS_OK;
-  const iris::NormBwdPlan plan = iris::norm_bwd_plan(rows, cols);
+  const bool whole = cols % 8 == 0 && params16(norm, a.p, rows) && rows16_or_none(dx, ld_dx, xt, rows) &&
+                     rows16_or_none(dy, ld_dy, type, rows) && rows16_or_none(dn, ld_dn, type, rows) &&
+                     rows16_or_none(dr, ld_dr, xt, rows) && rows16_or_none(r, ld_r, xt, rows) && rows16_or_none(y, ld_y, type, rows);
+  const iris::NormBwdPlan plan = iris::norm_bwd_plan(rows, cols, whole);
   if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes))) return st;
   if ((st = check_distinct({{dx, "dx", true}, {dy, "dy", true}, {dpre_w, "dpre_w", true}, {dpre_b, "dpre_b", true},
                             {dpost_w, "dpost_w", true}, {dpost_b, "dpost_b", true}, {dgate, "dgate", true},
@@ -315,9 +318,6 @@ int iris_block_norm_bwd(void* dx, int64_t ld_dx, void* dy, int64_t ld_dy, float*
   a.wg_rows = plan.wg_rows;
   a.wgs = plan.wgs;
   a.part = (float*)workspace;
-  const bool whole = cols % 8 == 0 && params16(norm, a.p, rows) && rows16_or_none(dx, ld_dx, xt, rows) &&
-                     rows16_or_none(dy, ld_dy, type, rows) && rows16_or_none(dn, ld_dn, type, rows) &&
-                     rows16_or_none(dr, ld_dr, xt, rows) && rows16_or_none(r, ld_r, xt, rows) && rows16_or_none(y, ld_y, type, rows);
   const auto launch = type == IRIS_TYPE_FP16 ? iris::launch_norm_bwd<iris::f16> : iris::launch_norm_bwd<iris::bf16>;
   hipError_t e = launch(a, xt == IRIS_TYPE_FP32, whole, (hipStream_t)stream);
   if (e == hipSuccess && (dpre_w || dpre_b || dpost_w || dpost_b || a.dgate)) e = iris::launch_norm_join(a, (hipStream_t)stream);

@@ -97,21 +97,33 @@ struct Raw8 {
   // down, so that nothing past the row is read and only that piece's wave does more.
   template <bool WHOLE>
   __device__ __forceinline__ void load(const T* row, int col, int cols, bool on = true) {
+    fetch<WHOLE>(row, col, cols, on);
+    settle<WHOLE>(col, cols, on);
+  }
+  // the same in two steps: the values are waited for in the second
+  template <bool WHOLE>
+  __device__ __forceinline__ void settle(int col, int cols, bool on) {
     if constexpr (WHOLE) {
-      on = on && col < cols;
-      const uint32_t m = on_mask(on);
-      const char* const at = (const char*)row + (on ? col : 0) * (int)sizeof(T);
+      const uint32_t m = on_mask(on && col < cols);
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[i] &= m;
+    } else if (cols >= 8) {
+      const int down = on ? min(col - min(col, cols - 8), 8) : 8;
+      if (down > 0) move_down(down);
+    }
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void fetch(const T* row, int col, int cols, bool on) {
+    if constexpr (WHOLE) {
+      const char* const at = (const char*)row + (on && col < cols ? col : 0) * (int)sizeof(T);
 #pragma unroll
       for (int i = 0; i < WORDS / 4; ++i) {
         const u32x4 v = *(const u32x4*)(at + 16 * i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e] & m;
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e];
       }
     } else if (cols >= 8) {
-      const int at = min(col, cols - 8);
-      __builtin_memcpy(w, row + at, sizeof w);
-      const int down = on ? min(col - at, 8) : 8;
-      if (down > 0) move_down(down);
+      __builtin_memcpy(w, row + min(col, cols - 8), sizeof w);
     } else {
 #pragma unroll
       for (int i = 0; i < WORDS; ++i) w[i] = 0;

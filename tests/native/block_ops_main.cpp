@@ -83,7 +83,7 @@ DropoutPlan dropout_plan(int64_t, int64_t) { return {16, 1, 64, need}; }
 hipError_t launch_dropout(const DropoutArgs&, const DropoutPlan&, void* sums, void* ws, hipStream_t) {
   return sums ? work(ws) : hipSuccess;
 }
-NormBwdPlan norm_bwd_plan(int64_t, int64_t) { return {4, 16, need}; }
+NormBwdPlan norm_bwd_plan(int64_t, int64_t, bool) { return {4, 16, need}; }
 template <class T>
 hipError_t launch_norm(const NormArgs&, bool, bool, hipStream_t) { return hipSuccess; }
 template <class T>
