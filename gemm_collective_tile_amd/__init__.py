@@ -973,7 +973,8 @@ def iris_block_norm_bwd(dx, r, stats, norm: BlockNorm, dn=None, dr=None, y=None,
         None if dpre_w is None else _sums(dpre_w, "dpre_w", (cols,), dev),
         None if dpre_b is None else _sums(dpre_b, "dpre_b", (cols,), dev),
         None if dpost_w is None else _sums(dpost_w, "dpost_w", (cols,), dev),
-        None if dpost_b is None else _sums(dpost_b, "dpost_b", (cols,), dev), None if dgate is None else _sums(dgate, "dgate", norm.gate.shape, dev),
+        None if dpost_b is None else _sums(dpost_b, "dpost_b", (cols,), dev),
+        None if dgate is None else _sums(dgate, "dgate", norm.gate.shape, dev),
         *_any_plain(dn, "dn", shape, kind, dev), *_any_plain(dr, "dr", shape, dtype, dev), *_any_plain(r, "r", shape, dtype, dev),
         *_any_plain(y, "y", shape, kind, dev), None if stats is None else _sums(stats, "stats", (rows, 4), dev), p, rows, cols,
         ws, wsb, _current_stream(dev) if stream is None and _current_device() == dev else _fp8_stream(stream, dev))

@@ -223,8 +223,8 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64, P == 1 ? 8 : 4) void block_no
 // behind the next row's (without either, two workgroups a CU with 128 registers: 74 and
 // 6.2). 333 x 1376 in fp16 as a layer norm with all gradients 9.2 us and 2.8.
 template <class T, class X, int W, int P, bool WHOLE, bool BIAS>
-__global__ __launch_bounds__(64 * norm_bwd_waves(W), norm_bwd_ahead(W, WHOLE) ? 2 : 4) void block_norm_bwd_kernel(NormBwdArgs a, float inv_cols,
-                                                                                   FastDiv gate_rows) {
+__global__ __launch_bounds__(64 * norm_bwd_waves(W), norm_bwd_ahead(W, WHOLE) ? 2 : 4) void block_norm_bwd_kernel(
+    NormBwdArgs a, float inv_cols, FastDiv gate_rows) {
   constexpr int WAVES = norm_bwd_waves(W), RG = WAVES / W, WIDE = W * 512 * P;
   constexpr bool AHEAD = norm_bwd_ahead(W, WHOLE);   // 256 registers a lane: the next row is under way while one is worked on
   __shared__ float slots[2][2][RG][2 * W];   // by turns, so that a row's sums are read before the next row's but one are written
