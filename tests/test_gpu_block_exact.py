@@ -2,7 +2,8 @@
 whole numbers beside them and a dropout of one half, whose factor is 2. All sums stay
 below 256, which bf16 holds, so every output has one right value in every type and any
 order of the sums, on each tile, whole and ragged, and each way to split and join. A row
-that is missing, read twice or taken from another strip shows.
+that is missing, read twice or taken from another strip shows, in the bias's
+gradient too: its sums stay below 2^24, and C's type rounds them once.
 
 The activations that are not exact follow in the largest tile, with the bounds of
 test_gpu_block.
@@ -112,6 +113,28 @@ def test_mm_act_to_the_bit(dtype, M, N, K, want, way):
         il.iris_fp8_quantize(c.float(), q2)
         assert all(np.array_equal(a, b) for a, b in zip(parts(q), parts(q2))), "8-bit output"
         assert_untouched(q, "8-bit output")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dropped,with_dbias", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("dtype,M,N,K,want", ACT_OF_EACH_PLAN)
+def test_mm_act_bwd_to_the_bit(dtype, M, N, K, want, dropped, with_dbias):
+    assert plan_act(M, N, K, dtype) == want
+    note(f"exact mm act backward {M}x{N}x{K} {dtype} {want} dropout {dropped} dbias {with_dbias}")
+    A, B, v = operands(M, N, K, 128 if dropped else 1)
+    (pc, pz, _), offset = layout(N)
+    z = whole_numbers(M, N, 4, 3)
+    c = torch.where(z > 0, v, torch.zeros_like(v))   # relu's slope is 0 at 0
+    c = c * mask(M, N) if dropped else c
+    assert float(c.abs().max()) <= 256 and float(c.abs().sum(0).max()) < 2 ** 24, "the case is not exact"
+    C, c_in = out_of(M, N, dtype, pc, offset)
+    dbias = torch.full((N,), float("nan"), dtype=DT[dtype], device="cuda") if with_dbias else None
+    il.iris_fp8_mm_act_bwd(C, A, B, placed(z, dtype, pz, offset), "relu", dbias=dbias,
+                           dropout=il.Dropout(0.5, SEED, OFFSET) if dropped else None)
+    same(C, c, "C")
+    assert c_in()
+    if with_dbias:
+        same(dbias, c.sum(0), "dbias")
 
 
 @pytest.mark.gpu
