@@ -78,6 +78,13 @@ struct Drop {
   __device__ __forceinline__ void apply(uint32_t row, uint32_t piece, float (&v)[8]) const {
     apply<1>({(int)row}, piece, *(float (*)[1][8])&v);
   }
+  // v without what is dropped, which becomes 0, as it is. Its product with a dropped gradient
+  // is then 0 whatever v held, and not 0 times an infinity.
+  __device__ __forceinline__ void clear(uint32_t row, uint32_t piece, float (&v)[8]) const {
+    const u32x4 w = bits(row, piece);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu) >= threshold ? v[i] : 0.0f;
+  }
   __device__ __forceinline__ float apply(uint32_t row, uint32_t col, float v) const {
     if (threshold == 0) return v * scale;
     const u32x4 w = bits(row, col >> 3);
