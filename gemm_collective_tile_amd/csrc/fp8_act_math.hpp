@@ -65,6 +65,10 @@ __device__ __forceinline__ void activate(int act, float (&v)[U][N]) {
   }
 }
 
+// z as a factor of what is 0 far out, where z may be infinite (fp16 holds a kept z of 65520 and
+// more so): the slope there is its limit, 1 or 0. A NaN is in the other factor too.
+__device__ __forceinline__ float held(float z) { return __builtin_amdgcn_fmed3f(z, -0x1p60f, 0x1p60f); }
+
 // v *= act'(z)
 template <int U, int N>
 __device__ __forceinline__ void times_slope(int act, const float (&z)[U][N], float (&v)[U][N]) {
@@ -78,21 +82,21 @@ __device__ __forceinline__ void times_slope(int act, const float (&z)[U][N], flo
       for (int k = 0; k < U * N; ++k) {
         float e;
         const float c = normal_cdf(z[k / N][k % N], e);
-        v[k / N][k % N] *= __builtin_fmaf(z[k / N][k % N] * 0.39894228040143268f, e, c);
+        v[k / N][k % N] *= __builtin_fmaf(held(z[k / N][k % N]) * 0.39894228040143268f, e, c);
       }
       break;
     case ACT_GELU_TANH:
 #pragma unroll
       for (int k = 0; k < U * N; ++k) {
         const float z2 = gelu_square(z[k / N][k % N]), s = gelu_sigmoid(z[k / N][k % N], z2);
-        v[k / N][k % N] *= __builtin_fmaf(z[k / N][k % N] * s * (1.0f - s), __builtin_fmaf(3.0f * kGelu3 * kGeluU, z2, kGeluU), s);
+        v[k / N][k % N] *= __builtin_fmaf(held(z[k / N][k % N]) * s * (1.0f - s), __builtin_fmaf(3.0f * kGelu3 * kGeluU, z2, kGeluU), s);
       }
       break;
     case ACT_SILU:
 #pragma unroll
       for (int k = 0; k < U * N; ++k) {
         const float s = sigmoid(z[k / N][k % N]);
-        v[k / N][k % N] *= s * __builtin_fmaf(z[k / N][k % N], 1.0f - s, 1.0f);
+        v[k / N][k % N] *= s * __builtin_fmaf(held(z[k / N][k % N]), 1.0f - s, 1.0f);
       }
       break;
     default: break;

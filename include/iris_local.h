@@ -529,8 +529,9 @@ int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, void* z, int64_t ld_z,
  * The product whose result goes back through an activation (not IRIS_ACT_NONE):
  *   C = alpha m (A @ B^T) act'(z),  dbias[j] = sum over the rows i of C[i][j]
  * A: the output's gradient, B: the transposed weight of the next product, z: what the
- * forward pass kept (M, N; relu's slope is 0 at 0). dbias: N values of c_type, or NULL;
- * summed in 32 bits before C's rounding.
+ * forward pass kept (M, N; relu's slope is 0 at 0, every slope 1 or 0 at infinities, which
+ * fp16 holds from 65520 on). dbias: N values of c_type, or NULL; summed in 32 bits before
+ * C's rounding.
  */
 int iris_fp8_mm_act_bwd(void* C, int32_t c_type, int64_t ldc, void* dbias, const iris_fp8_t* A, const iris_fp8_t* B,
                         const void* z, int64_t ld_z, int32_t act, float alpha, const iris_drop_t* drop, int64_t M,

@@ -1,13 +1,14 @@
 """The block operators where values are not finite."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import block_ref as bref
 import gemm_collective_tile_amd as il
 from gpu_util import note
-from test_gpu_block import OFFSET, SEED
+from test_gpu_block import OFFSET, SEED, values
 from test_gpu_fp8 import DT
 
 INF, NAN = float("inf"), float("nan")
@@ -43,3 +44,46 @@ def test_dropped_values_that_are_not_finite_leave_the_gates_gradient_alone(rows,
     kept[i, j] = INF
     il.iris_block_norm_bwd(None, r, stats, norm, dr=x, y=kept, dgate=dgate)
     assert not math.isfinite(float(dgate[i // every, j])) and int((~dgate.isfinite()).sum()) == 1
+
+
+def slopes(act, z, dtype, M):
+    """act'(z) by way of the backward product of ones."""
+    n = len(z)
+    ones, one = il.iris_fp8_empty(M, 1), il.iris_fp8_empty(n, 1)
+    il.iris_fp8_quantize(torch.ones((M, 1), device="cuda"), ones)
+    il.iris_fp8_quantize(torch.ones((n, 1), device="cuda"), one)
+    C = torch.full((M, n), NAN, dtype=DT[dtype], device="cuda")
+    il.iris_fp8_mm_act_bwd(C, ones, one, torch.tensor(z, device="cuda").expand(M, n).to(DT[dtype]).contiguous(), act)
+    return C
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M", [3, 90, 200])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_slopes_at_infinity(act, M, dtype):
+    """1 and 0, the limits: fp16 holds a z of 65520 and more as an infinity."""
+    note(f"slope of {act} at infinity, {M} rows, {dtype}")
+    C = slopes(act, [INF, -INF, 0.5], dtype, M)
+    assert bool((C[:, 0] == 1).all()) and bool((C[:, 1] == 0).all()), (C[0], C[-1])
+    assert np.all(np.abs(values(C)[:, 2] - bref.slope(np.array(0.5), act)) <= 2.0 ** -8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_a_kept_z_beyond_fp16_has_a_gradient(act):
+    """The forward pass gives 90000 in 8 bits and keeps z in fp16, as an infinity; the backward pass goes on from it."""
+    A, B = il.iris_fp8_empty(200, 1), il.iris_fp8_empty(16, 1)
+    il.iris_fp8_quantize(torch.full((200, 1), 300.0, device="cuda"), A)
+    il.iris_fp8_quantize(torch.tensor([300.0, -300.0] * 8, device="cuda").reshape(16, 1), B)
+    z, q = torch.empty((200, 16), dtype=torch.float16, device="cuda"), il.iris_fp8_empty(200, 16)
+    il.iris_fp8_mm_act(None, A, B, act=act, z=z, q=q, dtype=torch.float16)
+    assert bool(z[:, ::2].isposinf().all()) and bool(z[:, 1::2].isneginf().all())
+    h = q.codes.float() * q.scales.float()
+    assert bool(((h[:, ::2] - 288.0 ** 2).abs() <= 2.0 ** -4 * 288.0 ** 2).all()) and bool((h[:, 1::2] == 0).all())
+    dh, C = il.iris_fp8_empty(200, 1), torch.full_like(z, NAN)
+    il.iris_fp8_quantize(torch.ones((200, 1), device="cuda"), dh)
+    one = il.iris_fp8_empty(16, 1)
+    il.iris_fp8_quantize(torch.ones((16, 1), device="cuda"), one)
+    il.iris_fp8_mm_act_bwd(C, dh, one, z, act)
+    assert bool((C[:, ::2] == 1).all()) and bool((C[:, 1::2] == 0).all())
