@@ -73,10 +73,20 @@ __device__ __forceinline__ float held(float z) { return __builtin_amdgcn_fmed3f(
 template <int U, int N>
 __device__ __forceinline__ void times_slope(int act, const float (&z)[U][N], float (&v)[U][N]) {
   switch (act) {
-    case ACT_RELU:
+    case ACT_RELU: {
 #pragma unroll
       for (int k = 0; k < U * N; ++k) v[k / N][k % N] = z[k / N][k % N] > 0.0f ? v[k / N][k % N] : 0.0f;
+      // NaN stays: looked for in all values at once (v_maximum3_f32 takes two and passes a NaN on),
+      // for a comparison and a choice of each would cost 2.5 % at 4095 x 11008 x 4096
+      float most = z[0][0];
+#pragma unroll
+      for (int k = 1; k < U * N; ++k) most = __builtin_elementwise_maximum(most, z[k / N][k % N]);
+      if (most != most) {
+#pragma unroll
+        for (int k = 0; k < U * N; ++k) v[k / N][k % N] = z[k / N][k % N] != z[k / N][k % N] ? z[k / N][k % N] : v[k / N][k % N];
+      }
       break;
+    }
     case ACT_GELU:
 #pragma unroll
       for (int k = 0; k < U * N; ++k) {

@@ -87,3 +87,16 @@ def test_a_kept_z_beyond_fp16_has_a_gradient(act):
     il.iris_fp8_quantize(torch.ones((16, 1), device="cuda"), one)
     il.iris_fp8_mm_act_bwd(C, dh, one, z, act)
     assert bool((C[:, ::2] == 1).all()) and bool((C[:, 1::2] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M", [3, 90, 200])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_slopes_at_nan(act, M, dtype):
+    """The backward pass shows a NaN where the forward pass does."""
+    note(f"slope of {act} at NaN, {M} rows, {dtype}")
+    C = slopes(act, [1.0, NAN, -1.0, 0.0], dtype, M)
+    assert bool(C[:, 1].isnan().all()) and bool(C[:, [0, 2, 3]].isfinite().all())
+    if act == "relu":
+        assert C[0, [0, 2, 3]].tolist() == [1.0, 0.0, 0.0]
