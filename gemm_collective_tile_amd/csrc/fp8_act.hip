@@ -76,7 +76,7 @@ __device__ __forceinline__ void finish(const Fp8ActArgs& a, const Drop& drop, co
     float z[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) beside[u].values(z[u]);
-    times_slope(a.act, z, v);
+    times_slope<sizeof(OUT) == 4>(a.act, z, v);
     drop.apply(m, (uint32_t)n >> 3, v);
     if (a.dbias_part) {
 #pragma unroll
@@ -99,7 +99,7 @@ __device__ __forceinline__ void finish(const Fp8ActArgs& a, const Drop& drop, co
 #pragma unroll
       for (int u = 0; u < U; ++u) put[u].z(v[u]);
     }
-    activate(a.act, v);
+    activate<sizeof(OUT) == 4>(a.act, v);
     drop.apply(m, (uint32_t)n >> 3, v);
     if (a.residual) {
 #pragma unroll
@@ -351,12 +351,12 @@ struct PutAct {
     OUT* const at = z ? (OUT*)z + (int64_t)m * ldz + n : nullptr;
     if (backward) {
       const float y[1][1] = {{widen(*at)}};
-      times_slope(act, y, v);
+      times_slope<sizeof(OUT) == 4>(act, y, v);
       v[0][0] = d.apply((uint32_t)m, (uint32_t)n, v[0][0]);
     } else {
       if (bias) v[0][0] += widen(((const OUT*)bias)[n]);
       if (at) narrow(v[0][0], *at);
-      activate(act, v);
+      activate<sizeof(OUT) == 4>(act, v);
       v[0][0] = d.apply((uint32_t)m, (uint32_t)n, v[0][0]);
       if (residual) v[0][0] += widen(((const OUT*)residual)[(int64_t)m * ldr + n]);
     }

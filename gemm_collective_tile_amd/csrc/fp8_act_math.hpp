@@ -5,17 +5,34 @@
 
 namespace iris {
 
+// z as a factor of what is 0 far out, where z may be infinite (fp16 holds a kept z of 65520 and
+// more so): the slope there is its limit, 1 or 0. A NaN is in the other factor too.
+__device__ __forceinline__ float held(float z) { return __builtin_amdgcn_fmed3f(z, -0x1p60f, 0x1p60f); }
+
 // The normal distribution's upper tail Q(a) = erfc(a / sqrt 2) / 2, a >= 0, as
 // exp(-a^2 / 2) t P(t) with t = 1 / (1 + 0.28 a): P of degree 8 fitted to the least
 // relative error, 9.0e-8 over 0 <= a <= 40 (a weighted least-squares fit on Chebyshev
-// points of t). Of the normal distribution itself, in 32 bits, 4.2e-7 at most, in
-// the far tail (the exponent's rounding); that keeps small values of gelu's negative
-// side exact to their type, where 1 + erf would cancel.
+// points of t). A small value of gelu's negative side keeps its digits so, where 1 + erf
+// would cancel. What 32 bits add grows with the exponent, whose roundings (of the square,
+// of its product and of the constant) count |x^2| / 2 times 2^-24 and more: of the
+// distribution 8e-7 for |x| up to 4, 2.0e-6 to 6, 7.4e-6 to 12.9, far below half a step of a
+// 16-bit type. EXACT, for an fp32 C: the exponent's rest is carried along, 4.3e-7 anywhere
+// (with an exact exp2 and reciprocal, in either form; theirs are good to an ulp).
 // e: exp(-x^2 / 2). Returns the distribution at x.
+template <bool EXACT>
 __device__ __forceinline__ float normal_cdf(float x, float& e) {
+  constexpr double kHalfLog2e = -0.72134752044448170;
+  constexpr float c = (float)kHalfLog2e;
   const float a = __builtin_fabsf(x);
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.28f, a, 1.0f));
-  e = __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f);
+  const float y = EXACT ? held(x) : x;   // no infinity among the rests
+  const float square = y * y, power = square * c;
+  e = __builtin_amdgcn_exp2f(power);
+  if constexpr (EXACT) {
+    constexpr float c_rest = (float)(kHalfLog2e - (double)c);
+    const float rest = __builtin_fmaf(square, c_rest, __builtin_fmaf(__builtin_fmaf(y, y, -square), c, __builtin_fmaf(square, c, -power)));
+    e = __builtin_fmaf(e, rest * 0.69314718055994531f, e);
+  }
   float p = 0.025858724489808083f;
   p = __builtin_fmaf(p, t, -0.09804520010948181f);
   p = __builtin_fmaf(p, t, 0.09953682124614716f);
@@ -39,7 +56,8 @@ __device__ __forceinline__ float gelu_sigmoid(float z, float z2) {   // s(u), th
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c * kGelu3, z2, c)));
 }
 
-template <int U, int N>
+// EXACT: for an fp32 C
+template <bool EXACT, int U, int N>
 __device__ __forceinline__ void activate(int act, float (&v)[U][N]) {
   switch (act) {
     case ACT_RELU:
@@ -50,7 +68,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[U][N]) {
 #pragma unroll
       for (int k = 0; k < U * N; ++k) {
         float e;
-        v[k / N][k % N] *= normal_cdf(v[k / N][k % N], e);
+        v[k / N][k % N] *= normal_cdf<EXACT>(v[k / N][k % N], e);
       }
       break;
     case ACT_GELU_TANH:
@@ -65,12 +83,8 @@ __device__ __forceinline__ void activate(int act, float (&v)[U][N]) {
   }
 }
 
-// z as a factor of what is 0 far out, where z may be infinite (fp16 holds a kept z of 65520 and
-// more so): the slope there is its limit, 1 or 0. A NaN is in the other factor too.
-__device__ __forceinline__ float held(float z) { return __builtin_amdgcn_fmed3f(z, -0x1p60f, 0x1p60f); }
-
 // v *= act'(z)
-template <int U, int N>
+template <bool EXACT, int U, int N>
 __device__ __forceinline__ void times_slope(int act, const float (&z)[U][N], float (&v)[U][N]) {
   switch (act) {
     case ACT_RELU: {
@@ -91,7 +105,7 @@ __device__ __forceinline__ void times_slope(int act, const float (&z)[U][N], flo
 #pragma unroll
       for (int k = 0; k < U * N; ++k) {
         float e;
-        const float c = normal_cdf(z[k / N][k % N], e);
+        const float c = normal_cdf<EXACT>(z[k / N][k % N], e);
         v[k / N][k % N] *= __builtin_fmaf(held(z[k / N][k % N]) * 0.39894228040143268f, e, c);
       }
       break;

@@ -1,4 +1,4 @@
-"""The block operators where values are not finite."""
+"""The block operators where values are not finite, and in the far tails."""
 import math
 
 import numpy as np
@@ -100,3 +100,26 @@ def test_slopes_at_nan(act, M, dtype):
     assert bool(C[:, 1].isnan().all()) and bool(C[:, [0, 2, 3]].isfinite().all())
     if act == "relu":
         assert C[0, [0, 2, 3]].tolist() == [1.0, 0.0, 0.0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [2, 200])
+def test_gelus_far_tail_keeps_its_digits_in_fp32(M):
+    """Relative to its value. The tail's polynomial is within 9.0e-8, its steps and the product with exp add up to
+    4.3e-7 with it (in 32 bits with an exact exp and quotient); exp2 and the quotient are good to an ulp, 1.2e-7, the
+    latter counted twice for what follows from it; the last product 6e-8: 8.5e-7, so 16 * 2^-24."""
+    z = -np.linspace(0.0, 12.8, 4099).astype(np.float32)[1:]
+    n = len(z)
+    A, B = il.iris_fp8_empty(M, 0), il.iris_fp8_empty(n, 0)
+    C = torch.full((M, n), NAN, device="cuda")
+    il.iris_fp8_mm_act(C, A, B, act="gelu", bias=torch.from_numpy(z).cuda())
+    want = bref.act(z.astype(np.float64), "gelu")
+    rel = np.abs(values(C) / want - 1.0).max()
+    assert rel <= 16 * 2.0 ** -24, rel
+    # the slope, of what it is the difference of: Phi and z phi
+    C = slopes("gelu", z.tolist(), "fp32", M)
+    zd = z.astype(np.float64)
+    phi = np.exp(-0.5 * zd * zd) / math.sqrt(2.0 * math.pi)
+    size = bref.act(zd, "gelu") / zd + np.abs(zd) * phi
+    rel = (np.abs(values(C) - bref.slope(zd, "gelu")) / size).max()
+    assert rel <= 16 * 2.0 ** -24, rel
