@@ -153,20 +153,6 @@ __device__ __forceinline__ void strip_barrier() {
   }
 }
 
-// until at most n of this wave's vector memory operations are under way
-__device__ __forceinline__ void wait_vmem(int n) {
-  switch (n) {
-    case 0: wait_loads<0>(); break;
-    case 2: wait_loads<2>(); break;
-    case 4: wait_loads<4>(); break;
-    case 6: wait_loads<6>(); break;
-    case 8: wait_loads<8>(); break;
-    case 12: wait_loads<12>(); break;
-    case 16: wait_loads<16>(); break;
-    default: wait_loads<0>(); break;
-  }
-}
-
 // WHOLE: N is a multiple of 8 and all rows of C, z and the residual start at multiples of
 // 16 bytes.
 //
@@ -244,8 +230,23 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void fp8_mm_act_k
       }
     }
   };
-  // stores that every strip surely has, whatever else is stored
-  const int stores = WHOLE && a.g.C ? PASSES * PIECES : 0;
+  // Until strip i has landed. Behind its loads, of this wave's, are surely the stores of C that strip
+  // i - 1 sent after them (whatever else it stored) and the next strip's loads, LOADS of each.
+  constexpr int LOADS = PASSES * PIECES;
+  static_assert(2 * LOADS < 64, "more than a wait can count");
+  const auto wait_for = [&](int i) {
+    if constexpr (AHEAD == 1) {
+      wait_loads<0>();
+    } else {
+      const bool stored = i > 0 && a.g.C, more = i + 1 < T::FM;
+      if (stored && more)
+        wait_loads<2 * LOADS>();
+      else if (stored || more)
+        wait_loads<LOADS>();
+      else
+        wait_loads<0>();
+    }
+  };
   if (beside.at) {
     fetch(0);
     if constexpr (AHEAD == 2) fetch(1);
@@ -267,8 +268,7 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void fp8_mm_act_k
     char* const raw_at = lds + raw_wave + (i % AHEAD) * RAW + 16 * lane;
     if (beside.at) {
       if constexpr (WHOLE) {
-        // behind strip i's loads: the stores of strip i - 1 if they went out ahead of it, and the next strip's loads
-        wait_vmem((i >= AHEAD - 1 && i > 0 && AHEAD == 2 ? stores : 0) + (AHEAD == 2 && i + 1 < T::FM ? PASSES * PIECES : 0));
+        wait_for(i);
       } else {
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
