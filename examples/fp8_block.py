@@ -43,19 +43,24 @@ def forward(block, x, dropout, keep):
     il.iris_fp8_mm_act(None, n8, block.w1_8.fwd, act="gelu", bias=block.b1.detach().to(half), z=z, q=h8, dtype=half)
     il.iris_fp8_mm_act(y, h8, block.w2_8.fwd, bias=block.b2.detach().to(half))
     il.iris_block_norm(x, after, y=y, r=r, stats=stats[1])
-    return r, (x, y, z, n8, h8, stats, before, after)
+    return r, (y, z, n8, h8, stats, before, after)
 
 
 class BlockFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, block, dropout, x, *params):
-        r, kept = forward(block, x, dropout, any(ctx.needs_input_grad))
-        ctx.block, ctx.kept, ctx.versions = block, kept, (block.w1_8.version, block.w2_8.version)
+        keep = any(ctx.needs_input_grad)
+        r, kept = forward(block, x, dropout, keep)
+        if keep:
+            # what the backward pass reads of the caller's: autograd refuses it if it has changed by then
+            ctx.save_for_backward(x, block.pre_w, block.post_w, block.gate)
+            ctx.block, ctx.kept, ctx.versions = block, kept, (block.w1_8.version, block.w2_8.version)
         return r
 
     @staticmethod
     def backward(ctx, dr):
-        block, (x, y, z, n8, h8, stats, before, after) = ctx.block, ctx.kept
+        block, (y, z, n8, h8, stats, before, after) = ctx.block, ctx.kept
+        x = ctx.saved_tensors[0]
         if (block.w1_8.version, block.w2_8.version) != ctx.versions:
             raise RuntimeError("the 8-bit weights have been set anew since the forward pass")
         n, width = x.shape

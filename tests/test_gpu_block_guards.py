@@ -1,0 +1,27 @@
+"""examples/fp8_block.py between its passes: what its backward pass reads is either what
+the forward pass read, or refused."""
+import pytest
+import torch
+
+from gpu_util import note
+from test_gpu_block_layer import example
+
+
+def made(ex, p=0.3, counter=None):
+    torch.manual_seed(5)
+    block = ex.Block(256, 344, p=p)
+    x = torch.randn(90, 256, device="cuda").requires_grad_()
+    return block, x, ex.il.Dropout(p, 77, 3, counter), torch.randn(90, 256, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["pre_w", "post_w", "gate", "x"])
+def test_what_the_backward_pass_reads_may_not_change(name):
+    ex = example()
+    note(f"8-bit block: {name} changed between the passes")
+    block, x, drop, dr = made(ex)
+    r = block(x, drop)
+    with torch.no_grad():
+        (x if name == "x" else getattr(block, name)).mul_(2.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        r.backward(dr)
