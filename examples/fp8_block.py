@@ -50,6 +50,10 @@ class BlockFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, block, dropout, x, *params):
         keep = any(ctx.needs_input_grad)
+        if keep and dropout is not None:
+            # the backward pass takes this pass's mask, wherever the caller's handle and counter have moved by then
+            at = dropout.counter
+            dropout = il.Dropout(dropout.p, dropout.seed, dropout.offset, None if at is None else at.clone())
         r, kept = forward(block, x, dropout, keep)
         if keep:
             # what the backward pass reads of the caller's: autograd refuses it if it has changed by then

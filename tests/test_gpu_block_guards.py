@@ -25,3 +25,31 @@ def test_what_the_backward_pass_reads_may_not_change(name):
         (x if name == "x" else getattr(block, name)).mul_(2.0)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         r.backward(dr)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("by", ["offset", "counter"])
+def test_a_dropout_that_moves_on_keeps_the_earlier_masks(by):
+    """Two forward passes with one handle that moves on between them, then their backward passes."""
+    ex = example()
+    note(f"8-bit block: two passes with one dropout, moved by its {by}")
+    results = []
+    for together in (False, True):
+        counter = torch.zeros(1, dtype=torch.int64, device="cuda") if by == "counter" else None
+        block, x, drop, dr = made(ex, counter=counter)
+        outs = []
+        for k in range(2):
+            r = block(x, drop)
+            if not together:
+                r.backward(dr)
+            outs.append(r)
+            if by == "offset":
+                drop.offset = drop.offset + 1
+            else:
+                counter.add_(1)
+        if together:
+            for r in outs:
+                r.backward(dr)
+        assert not torch.equal(outs[0], outs[1]), "a mask of its own for each pass"
+        results.append([r.detach() for r in outs] + [x.grad] + [getattr(block, k).grad for k in ex.NAMES])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
