@@ -62,6 +62,7 @@ class BlockFunction(torch.autograd.Function):
         return r
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dr):
         block, (y, z, n8, h8, stats, before, after) = ctx.block, ctx.kept
         x = ctx.saved_tensors[0]

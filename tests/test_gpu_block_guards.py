@@ -53,3 +53,16 @@ def test_a_dropout_that_moves_on_keeps_the_earlier_masks(by):
         assert not torch.equal(outs[0], outs[1]), "a mask of its own for each pass"
         results.append([r.detach() for r in outs] + [x.grad] + [getattr(block, k).grad for k in ex.NAMES])
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.gpu
+def test_a_second_derivative_is_refused():
+    """A loss with its gradient's norm in it: the gradient depends on x by way of dr and r, and has no derivative here."""
+    ex = example()
+    block, x, drop, dr = made(ex)
+    loss = (block(x, drop) - dr).square().sum()
+    (g,) = torch.autograd.grad(loss, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (loss + g.square().sum()).backward()
+    (g,) = torch.autograd.grad(block(x, drop), x, dr, create_graph=True)   # a given dr: nothing that a derivative could follow
+    assert not g.requires_grad
