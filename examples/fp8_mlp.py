@@ -57,6 +57,7 @@ class FeedForward(torch.autograd.Function):
         return y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         (x8, gate8, up8), (g8, u8, d8) = ctx.kept, ctx.weights
         if [w.version for w in ctx.weights] != ctx.versions:
