@@ -1013,7 +1013,8 @@ def iris_fp8_mm_act(C, A: Fp8, B: Fp8, act="none", bias=None, z=None, residual=N
     """C = residual + alpha m act(A @ B^T + bias), C (M, N) float16, bfloat16 or float32;
     q receives it in 8 bits, too or instead (C None: `dtype` then names the type of
     bias, z and residual, float16 if they do not). z receives the value before the
-    activation. act: "none", "relu", "gelu", "gelu_tanh", "silu". Precision: as iris_fp8_mm."""
+    activation. act: "none", "relu", "gelu", "gelu_tanh", "silu". Precision: as iris_fp8_mm,
+    by that type, of an 8-bit output alone too (float32: every product exact)."""
     M, N, K, dev, code = _mm_operands(A, B, act)
     shape = (M, N)
     if C is not None:

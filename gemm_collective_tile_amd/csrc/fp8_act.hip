@@ -415,7 +415,14 @@ __global__ __launch_bounds__(256) void fp8_mm_act_join_kernel(Fp8ActArgs a, cons
   }
 }
 
-constexpr int kJoinRows = 16, kJoinRowsSummed = 64;   // without and with column sums
+// Rows of a joining workgroup. Without column sums 16, a turn of its loop, so that as many
+// workgroups as there are share the latency: 301 x 397 x 4111 to 8 bits 12.8 us, with 32 rows
+// 16.4, with 64 23.6; 33 x 11008 x 4096 13.7, 14.6, 15.5; 517 x 2053 x 8305 27.0, 28.0, 31.0. With
+// column sums 64, four turns one after the other: a quarter of the rows of partial sums, for
+// which a call has to find room in the workspace (few rows of a wide B take all of the
+// library's own with two such rows). That costs time: with dbias the same three take 25.7,
+// 18.5 and 34.5 us, with 32 rows 18.5, 17.3 and 30.9, with 16 15.0, 16.3 and 30.0.
+constexpr int kJoinRows = 16, kJoinRowsSummed = 64;
 
 template <class OUT, int BM, int BN>
 hipError_t launch_tiles(const Fp8ActArgs& a, hipStream_t s) {

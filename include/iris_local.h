@@ -518,7 +518,8 @@ size_t iris_block_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  * of precision by C's type holds here too. C, z and residual are (M, N) of c_type with row
  * pitches of their own, bias N values of c_type; z, residual, bias may be NULL. z receives
  * the value before the activation, for the backward pass. q: C in 8 bits too (block 1,
- * from 32 bits), or instead of C (C NULL; c_type then is that of the others).
+ * from 32 bits), or instead of C (C NULL; c_type then is that of the others, and says as
+ * ever how precise the product is: fp32 for every product exact, with no others too).
  */
 int iris_fp8_mm_act(void* C, int32_t c_type, int64_t ldc, void* z, int64_t ld_z, const iris_fp8_t* q, const iris_fp8_t* A,
                     const iris_fp8_t* B, const void* bias, int32_t act, float alpha, const iris_drop_t* drop,
