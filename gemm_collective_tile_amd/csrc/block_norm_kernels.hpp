@@ -221,7 +221,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64, P == 1 ? 8 : 4) void block_no
 // of loads, two reductions over the waves and stores; the next row's loads go out ahead
 // of it, and the parameters stay in registers, as a load of them would be waited for
 // behind the next row's (without either, two workgroups a CU with 128 registers: 74 and
-// 6.2). 333 x 1376 in fp16 as a layer norm with all gradients 9.2 us and 2.8.
+// 6.2). 333 x 1376 in fp16 as a layer norm with all gradients 9.5 us and 2.8.
 template <class T, class X, int W, int P, bool WHOLE, bool BIAS>
 __global__ __launch_bounds__(64 * norm_bwd_waves(W), norm_bwd_ahead(W, WHOLE) ? 2 : 4) void block_norm_bwd_kernel(
     NormBwdArgs a, float inv_cols, FastDiv gate_rows) {

@@ -162,7 +162,7 @@ __device__ __forceinline__ void strip_barrier() {
 // Smaller tiles, two a CU, hide the epilogue and lose more in the products (through
 // gelu_tanh with z and 8-bit codes 420 us where these took 405, 4096 x 4096 x 11008 with
 // dropout and residual 184 and 153). Now 381-395 us, 152-161, and 4095 x 11008 x 4096
-// backwards through gelu_tanh with dropout and the bias's gradient 204-215 (product 166-170).
+// backwards through gelu_tanh with dropout and the bias's gradient 209-215 (product 166-170).
 //
 // What is read beside the sums (z or the residual) is fetched strips ahead of its use.
 // Vector memory operations are counted in their order, loads and stores alike: a load

@@ -493,7 +493,8 @@ int iris_block_norm(void* r, int64_t ld_r, void* n, int64_t ld_n, const iris_fp8
  * (contiguous rows of cols, one for each gate row that the rows use; without rows one of
  * zeros, as the others are). r is needed with dn,
  * y with dy, dgate, dpost_w or dpost_b. dx, dr, r of stream_type; dy, dn, y of type.
- * Sums over the rows run in 32 bits in an order that sizes and alignment alone decide.
+ * What dropout made 0 adds 0 to dgate, whatever y held there. Sums over the rows run in 32
+ * bits in an order that sizes and alignment alone decide.
  * workspace: at least iris_block_norm_bwd_workspace_size() bytes (at most 101 MB), 256-byte
  * aligned, contents of no account, for one call at a time; NULL: the library's own, as
  * with iris_fp8_mm (32 MiB, or a second one of 128 MiB for what needs more).
